@@ -35,6 +35,9 @@ def _load():
     if not os.path.exists(_PATH):
         raise ImportError("libstq.so is not built (%s); run quantized_linear_attention_amd/build.py "
                           "or __graft_entry__.build()" % _PATH)
+    # torch first: its HIP runtime then serves the library too.  Loaded the other
+    # way round there are two runtimes in the process, and the library's sees no device.
+    import torch  # noqa: F401
     L = ctypes.CDLL(_PATH)
     P, I, St = ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p
     DP = ctypes.POINTER(_Desc)

@@ -207,3 +207,14 @@ def test_binding_rejects_bad_prompt_offsets(stq):
     args["q"] = _FakeCuda(sizes["q"] + 5, f)
     with pytest.raises(stq.StqError, match="q must be"):
         stq.stq_prefill(pool, slots, _FakeCuda(4, torch.int32), **args)
+
+
+def test_one_hip_runtime_whatever_is_imported_first():
+    """Importing the package before torch must not load a second HIP runtime
+    (the library's launches would go to one that torch's memory is unknown to)."""
+    import subprocess
+    import sys
+    code = ("import quantized_linear_attention_amd, torch; "
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.stdout.strip() == "1", r.stdout + r.stderr
