@@ -397,6 +397,157 @@ stq_status stq_requant_fixed_scales(stq_pool* pool, const int32_t* slots_dev, in
  * device reciprocal exhaustively against IEEE division. */
 stq_status stq_debug_rcp_bf16(float* out_dev, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * THE SOFTMAX LAYERS OF A HYBRID MODEL.  The models whose recurrent states
+ * this pool holds mix those layers with softmax attention ([P5] Contexto;
+ * [P1] introduction).  The calls below serve the latter, in the pool's
+ * manner: the caller owns every device buffer and stream, nothing is
+ * allocated, nothing synchronises, arguments are checked on the host.  They
+ * take no handle: a descriptor is read during the call only.
+ *
+ * KEY/VALUE CACHE: n_blocks blocks of block_tokens token slots each; token
+ * slot s is slot s % block_tokens of block s / block_tokens.  A token's keys
+ * and values hold, per key/value head, d channels in 4 bits: E2M1 codes
+ * (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 for the low three bits, bit 3 the
+ * sign) with one power-of-two scale 2^e per 32 channels, stored as the byte
+ * e + 127.  Value = code * 2^e.  Of a block of 32 channels with largest
+ * magnitude m, e is the least integer with m <= 6 * 2^e, held in [-23, 13]
+ * (every cached value is then exact in binary16; magnitudes beyond 6 * 2^13
+ * saturate), e = 0 for m = 0; codes round to the nearest level, ties to the
+ * even code.  A token and head whose key or value has an infinity or a NaN
+ * is stored with NaN scales (byte 255) on the key and zeros as the value: a
+ * query that sees it gets NaN, every other query is unaffected.
+ * Bytes of block b, head h at (b * n_kv_heads + h) * block_tokens * d*17/16:
+ *   key codes   [block_tokens][d/2]   byte i: channel 2i low, 2i+1 high nibble
+ *   value codes [block_tokens][d/2]
+ *   key scales  [d/32][block_tokens], value scales [d/32][block_tokens]
+ */
+typedef struct stq_kv_desc {
+  int32_t n_blocks;      /* >= 1                                             */
+  int32_t block_tokens;  /* 32, 64, 128 or 256                               */
+  int32_t n_kv_heads;    /* >= 1                                             */
+  int32_t d;             /* 64 or 128 channels of a head                     */
+} stq_kv_desc;
+
+#define STQ_BF16 0  /* element types of the calls below */
+#define STQ_FP16 1
+#define STQ_FP32 2
+
+/* Bytes of the cache's device buffer; 0 for an invalid description.  The
+ * buffer must be 16-byte aligned; its contents need no initialisation. */
+size_t stq_kv_bytes(const stq_kv_desc* desc);
+
+/* Block tables and slot maps from request lengths, in one launch.  Request
+ * i < n has cached_dev[i] tokens in the cache and brings new_dev[i] more
+ * (negative counts are taken as 0); row i of table_dev [n][table_cols] holds
+ * its blocks, the first blocks(cached) entries on entry.  Writes
+ *   tok_start_dev [n+1]  exclusive prefix sums of the new counts, and their sum;
+ *   len_dev [n]          cached + new;
+ *   table_dev            entries blocks(cached) .. blocks(cached+new)-1 of each
+ *                        row, taken from free_dev in request order (-1 once
+ *                        its n_free entries are used up); columns from
+ *                        table_cols on are neither taken nor written, every
+ *                        other entry is left as it was;
+ *   pos_dev [n_tok]      position of new token t in its request;
+ *   slot_dev [n_tok]     its token slot; -1 where its table entry is outside
+ *                        [0, n_blocks) or past table_cols;
+ *   used_dev [1]         blocks wanted; above n_free, the free list was short.
+ * blocks(c) = ceil(c / block_tokens).  Entries of pos and slot from
+ * tok_start[n] on (a padded batch) become -1; new tokens past n_tok get no
+ * entry.  n in [1, 4096]; token and block sums must stay below 2^31. */
+stq_status stq_kv_plan(int32_t n, const int32_t* cached_dev, const int32_t* new_dev, const int32_t* free_dev,
+                       int32_t n_free, int32_t n_blocks, int32_t block_tokens, int32_t* table_dev,
+                       int32_t table_cols, int32_t n_tok, int32_t* tok_start_dev, int32_t* len_dev,
+                       int32_t* pos_dev, int64_t* slot_dev, int32_t* used_dev, hipStream_t stream);
+
+#define STQ_NORM_NONE 0
+#define STQ_NORM_RMS  1  /* y = x / sqrt(mean(x^2) + eps) * weight */
+#define STQ_NORM_L2   2  /* y = x / sqrt(sum(x^2) + eps) * weight  */
+#define STQ_ROT_HALVES   0  /* channel pairs (i, i + n_rot/2) */
+#define STQ_ROT_ADJACENT 1  /* channel pairs (2i, 2i + 1)     */
+
+/* Norm of queries and keys per head, with the position rotation of the first
+ * n_rot channels in the same pass (binary32 inside, one rounding at the end).
+ * The L2 form with binary32 output is the q and k of stq_decode_step and
+ * stq_prefill.  Heads of one token are contiguous ([n_heads][d]); tokens are
+ * *_stride elements apart. */
+typedef struct stq_norm_desc {
+  int32_t n_tok;            /* >= 0                                           */
+  int32_t n_q_heads;        /* >= 1                                           */
+  int32_t n_k_heads;        /* >= 0 (0: no keys, k pointers unused)           */
+  int32_t d;                /* 64, 128 or 256                                 */
+  int32_t in_type;          /* STQ_BF16, STQ_FP16 or STQ_FP32                 */
+  int32_t out_type;         /* in_type or STQ_FP32                            */
+  int32_t norm;             /* STQ_NORM_*                                     */
+  float eps;                /* > 0 with a norm                                */
+  int32_t n_rot;            /* channels rotated: 0 or a multiple of 16, <= d  */
+  int32_t rot_pairs;        /* STQ_ROT_*                                      */
+  int32_t n_pos;            /* rows of the cosine and sine table              */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} stq_norm_desc;
+
+/* q_weight_dev, k_weight_dev: fp32 [d] or NULL (ones).  With n_rot > 0,
+ * pos_dev int32 [n_tok] and cos_sin_dev fp32 [n_pos][n_rot], a row the n_rot/2
+ * cosines, then the n_rot/2 sines; pair (x, y) becomes (x cos - y sin,
+ * y cos + x sin).  Rows of a token whose position lies outside [0, n_pos)
+ * (a padded batch) are left as they were.  Outputs may be the inputs
+ * themselves (same pointer, type and stride).  Pointers 16-byte aligned,
+ * strides a multiple of 16 bytes, else STQ_ERR_LAYOUT. */
+stq_status stq_qk_norm_rope(const stq_norm_desc* desc, const void* q_dev, const void* k_dev,
+                            const float* q_weight_dev, const float* k_weight_dev, const int32_t* pos_dev,
+                            const float* cos_sin_dev, void* q_out_dev, void* k_out_dev, hipStream_t stream);
+
+/* Cache write: token t < n_tok of k_dev, v_dev ([n_kv_heads][d] contiguous,
+ * tokens k_stride, v_stride elements apart, element type `type`) goes to token
+ * slot slot_dev[t] in the format above.  Slots outside the cache (-1 of a
+ * padded batch) are skipped; a slot must not be named twice in one call. */
+stq_status stq_kv_store(const stq_kv_desc* desc, void* cache_dev, size_t bytes, const int64_t* slot_dev,
+                        int32_t n_tok, const void* k_dev, const void* v_dev, int64_t k_stride, int64_t v_stride,
+                        int32_t type, hipStream_t stream);
+
+/* Read-back: the values the cache holds at the listed slots, exact in every
+ * element type; k_out_dev, v_out_dev [n_tok][n_kv_heads][d] contiguous.
+ * Rows of slots outside the cache are left as they were. */
+stq_status stq_kv_fetch(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, const int64_t* slot_dev,
+                        int32_t n_tok, void* k_out_dev, void* v_out_dev, int32_t type, hipStream_t stream);
+
+/* Attention over the cache.  Request i < n_req owns query tokens
+ * tok_start[i] .. tok_start[i+1]-1; its cache (through its table row) holds
+ * len[i] tokens, the last of which are its query tokens' own, so query j sits
+ * at position p = len[i] - (tok_start[i+1] - tok_start[i]) + j.  It sees cached
+ * position s when s <= p and (window == 0, or s > p - window, or s < n_sink).
+ *   o = sum_s softmax_s(scale * q . k_s) v_s, query head h reading key/value
+ *   head h / (n_heads / n_kv_heads); a query that sees nothing gets 0. */
+typedef struct stq_attend_desc {
+  int32_t n_req;            /* requests (>= 0)                                */
+  int32_t n_tok;            /* rows of q and o (a padded batch may have more   */
+                            /* than tok_start[n_req]; those are left alone)   */
+  int32_t n_heads;          /* a multiple of n_kv_heads                       */
+  int32_t type;             /* of q and o: STQ_BF16 or STQ_FP16               */
+  int32_t table_cols;       /* columns of the block table                     */
+  int32_t max_new;          /* at least every request's query tokens: queries  */
+                            /* past it are left alone                         */
+  int32_t max_len;          /* about the longest len: sets the split of the    */
+                            /* work, never the result                         */
+  int32_t window, n_sink;   /* >= 0; window 0: none                           */
+  float scale;              /* finite                                         */
+  int64_t q_stride, o_stride;  /* elements between tokens ([n_heads][d] each)  */
+} stq_attend_desc;
+
+/* Bytes of the workspace a call with these descriptors needs (0: none). */
+size_t stq_kv_attend_bytes(const stq_kv_desc* desc, const stq_attend_desc* a);
+
+/* Lengths are taken as at most table_cols * block_tokens; blocks whose table
+ * entry lies outside [0, n_blocks) hold no visible token.  q and o 16-byte
+ * aligned with strides a multiple of 16 bytes, the workspace 16-byte aligned,
+ * else STQ_ERR_LAYOUT.  A workspace serves one call at a time.  o must not
+ * overlap q.  Products run on the matrix cores in binary16 (cached values and
+ * queries exact, the queries scaled by a power of two per row; softmax
+ * weights rounded to binary16), sums and statistics in binary32. */
+stq_status stq_kv_attend(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, const stq_attend_desc* a,
+                         const int32_t* table_dev, const int32_t* tok_start_dev, const int32_t* len_dev,
+                         const void* q_dev, void* o_dev, void* work_dev, size_t work_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,4 +10,7 @@ from ._lib import (  # noqa: F401
     make_desc, stq_decode_step, stq_pool_bytes, stq_pool_create, stq_pool_destroy,
     stq_pool_fetch, stq_pool_store, stq_requant_fixed_scales, stq_status_str,
     stq_allocate_bits, stq_decode_commit, stq_decode_readout, stq_prefill, stq_prefill_states, stq_window_flush,
+    STQ_BF16, STQ_FP16, STQ_FP32, STQ_NORM_L2, STQ_NORM_NONE, STQ_NORM_RMS, STQ_ROT_ADJACENT, STQ_ROT_HALVES,
+    make_kv, stq_kv_attend, stq_kv_attend_bytes, stq_kv_bytes, stq_kv_fetch, stq_kv_plan, stq_kv_store,
+    stq_qk_norm_rope,
 )

@@ -10,6 +10,9 @@ _PATH = os.path.join(_PKG, "libstq.so")
 STQ_OK = 0
 STQ_GATE_HEAD, STQ_GATE_CHANNEL = 0, 1
 STQ_UNIT_HEAD, STQ_UNIT_ROW = 0, 1
+STQ_BF16, STQ_FP16, STQ_FP32 = 0, 1, 2
+STQ_NORM_NONE, STQ_NORM_RMS, STQ_NORM_L2 = 0, 1, 2
+STQ_ROT_HALVES, STQ_ROT_ADJACENT = 0, 1
 
 
 class StqError(RuntimeError):
@@ -25,6 +28,22 @@ class _Desc(ctypes.Structure):
                 ("window", ctypes.c_int32), ("n_comp", ctypes.c_int32),
                 ("unit_bits", ctypes.POINTER(ctypes.c_int32)),
                 ("row_weight", ctypes.POINTER(ctypes.c_float))]
+
+
+class _KvDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_blocks", "block_tokens", "n_kv_heads", "d")]
+
+
+class _NormDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "n_k_heads", "d", "in_type", "out_type", "norm")] +
+                [("eps", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("n_rot", "rot_pairs", "n_pos")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")])
+
+
+class _AttendDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_req", "n_tok", "n_heads", "type", "table_cols", "max_new", "max_len",
+                                               "window", "n_sink")] +
+                [("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("q_stride", "o_stride")])
 
 
 def library_path():
@@ -67,6 +86,18 @@ def _load():
     for name in ("stq_window_flush", "stq_requant_fixed_scales"):
         getattr(L, name).restype = I
         getattr(L, name).argtypes = [P, P, I, St]
+    Z, I64 = ctypes.c_size_t, ctypes.c_int64
+    KP, NP, AP = ctypes.POINTER(_KvDesc), ctypes.POINTER(_NormDesc), ctypes.POINTER(_AttendDesc)
+    for name, args in (("stq_kv_plan", [I, P, P, P, I, I, I, P, I, I, P, P, P, P, P, St]),
+                       ("stq_qk_norm_rope", [NP, P, P, P, P, P, P, P, P, St]),
+                       ("stq_kv_store", [KP, P, Z, P, I, P, P, I64, I64, I, St]),
+                       ("stq_kv_fetch", [KP, P, Z, P, I, P, P, I, St]),
+                       ("stq_kv_attend", [KP, P, Z, AP, P, P, P, P, P, P, Z, St])):
+        getattr(L, name).restype = I
+        getattr(L, name).argtypes = args
+    for name, args in (("stq_kv_bytes", [KP]), ("stq_kv_attend_bytes", [KP, AP])):
+        getattr(L, name).restype = Z
+        getattr(L, name).argtypes = args
     return L
 
 
@@ -277,3 +308,161 @@ def stq_window_flush(pool, slots, stream=None):
 def stq_requant_fixed_scales(pool, slots, stream=None):
     sp, n = _slots(slots, pool)
     _check(_L.stq_requant_fixed_scales(pool.handle, sp, n, _stream(stream)), "stq_requant_fixed_scales")
+
+
+# ------------------------------------------- the softmax layers' operators
+
+def _type(t, what, allowed=(STQ_BF16, STQ_FP16, STQ_FP32)):
+    import torch
+    code = {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}.get(t.dtype)
+    if code not in allowed:
+        raise StqError(-1, "%s has element type %s" % (what, t.dtype))
+    return code
+
+
+def _heads(t, what, n=None, heads=None, d=None, device=None):
+    """(pointer, token stride) of a [tokens][heads][d] CUDA tensor whose heads are
+    contiguous within a token; n, heads, d, device: what it has to be."""
+    if t is None or t.dim() != 3:
+        raise StqError(-1, "%s must be [tokens][heads][d]" % what)
+    a, b, c = t.shape
+    if (n is not None and a != n) or (heads is not None and b != heads) or (d is not None and c != d):
+        raise StqError(-1, "%s is %s, expected [%s][%s][%s]" % (what, (a, b, c), n, heads, d))
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise StqError(-1, "%s is on %s, expected %s" % (what, t.device, device or "a CUDA device"))
+    st = t.stride()
+    if st[2] != 1 or (b > 1 and st[1] != c):
+        raise StqError(-1, "%s: the heads of a token must be contiguous" % what)
+    return ctypes.c_void_p(t.data_ptr()), max(st[0], b * c) if a > 1 else b * c
+
+
+def _call(name, device, stream, *args):
+    """One library call on `device` and its current stream (or the given one)."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    st = ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            r = getattr(_L, name)(*args, st)
+    else:
+        r = getattr(_L, name)(*args, st)
+    _check(r, name)
+
+
+class _Kv:
+    def __init__(self, desc, pages):
+        self.desc, self.pages, self.device = desc, pages, pages.device
+        self.ref, self.ptr, self.bytes = ctypes.byref(desc), ctypes.c_void_p(pages.data_ptr()), pages.numel()
+
+
+def stq_kv_bytes(n_blocks, block_tokens, n_kv_heads, d):
+    """Bytes of the cache's device buffer; 0 for sizes the library does not take."""
+    return int(_L.stq_kv_bytes(ctypes.byref(_KvDesc(int(n_blocks), int(block_tokens), int(n_kv_heads), int(d)))))
+
+
+def make_kv(pages, block_tokens, n_kv_heads, d):
+    """The 4-bit key/value cache that lives in `pages`, a contiguous uint8 CUDA
+    tensor: as many whole blocks as it holds.  No copy, no initialisation."""
+    import torch
+    _dev(pages, torch.uint8, "pages")
+    one = stq_kv_bytes(1, block_tokens, n_kv_heads, d)
+    if pages is None or not one or pages.numel() < one:
+        raise StqError(-1, "pages of %s bytes hold no block of %s tokens, %s heads, d = %s"
+                       % (None if pages is None else pages.numel(), block_tokens, n_kv_heads, d))
+    return _Kv(_KvDesc(min(pages.numel() // one, 2 ** 31 - 1), block_tokens, n_kv_heads, d), pages)
+
+
+def stq_kv_plan(cached, new, free, table, block_tokens, n_blocks, tok_start, lens, pos, slots, used, stream=None):
+    """cached, new int32 [n]; free int32; table int32 [n][cols], updated in place;
+    outputs tok_start int32 [n+1], lens int32 [n], pos int32 [tokens], slots int64
+    [tokens], used int32 [1]."""
+    import torch
+    i, dev = torch.int32, table.device
+    if table.dim() != 2:
+        raise StqError(-1, "table must be [requests][columns]")
+    n, cols = table.shape
+    tok = pos.numel()
+    _call("stq_kv_plan", dev, stream, n, _dev(cached, i, "cached", n, dev), _dev(new, i, "new", n, dev),
+          _dev(free, i, "free", None, dev), free.numel(), n_blocks, block_tokens, _dev(table, i, "table"), cols, tok,
+          _dev(tok_start, i, "tok_start", n + 1, dev), _dev(lens, i, "lens", n, dev), _dev(pos, i, "pos", tok, dev),
+          _dev(slots, torch.int64, "slots", tok, dev), _dev(used, i, "used", 1, dev))
+
+
+def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=None, k_weight=None, pos=None,
+                     cos_sin=None, rot_pairs=STQ_ROT_HALVES, stream=None):
+    """q, k [tokens][heads][d] (views with contiguous heads; k and k_out may be
+    None); outputs of the same type or float32; weights float32 [d]; with a
+    table cos_sin float32 [positions][n_rot], pos int32 [tokens]."""
+    import torch
+    f = torch.float32
+    qp, qs = _heads(q, "q")
+    n, hq, d = q.shape
+    dev = q.device
+    qop, qos = _heads(q_out, "q_out", n, hq, d, dev)
+    ti, to = _type(q, "q"), _type(q_out, "q_out")
+    kp, ks, kop, kos, hk = None, 0, None, 0, 0
+    if k is not None:
+        kp, ks = _heads(k, "k", n, None, d, dev)
+        hk = k.shape[1]
+        kop, kos = _heads(k_out, "k_out", n, hk, d, dev)
+        if _type(k, "k") != ti or _type(k_out, "k_out") != to:
+            raise StqError(-1, "k and k_out must have the types of q and q_out")
+    n_rot = n_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or pos is None:
+            raise StqError(-1, "a rotation takes cos_sin [positions][n_rot] and pos [tokens]")
+        n_pos, n_rot = cos_sin.shape
+    desc = _NormDesc(n, hq, hk, d, ti, to, norm, eps, n_rot, rot_pairs, n_pos, qs, ks, qos, kos)
+    _call("stq_qk_norm_rope", dev, stream, ctypes.byref(desc), qp, kp, _dev(q_weight, f, "q_weight", d, dev),
+          _dev(k_weight, f, "k_weight", d, dev), _dev(pos, torch.int32, "pos", n, dev),
+          _dev(cos_sin, f, "cos_sin", None, dev), qop, kop)
+
+
+def stq_kv_store(kv, slots, k, v, stream=None):
+    """slots int64 [tokens]; k, v [tokens][n_kv_heads][d] of one element type."""
+    import torch
+    n, dev = slots.numel(), kv.device
+    kp, ks = _heads(k, "k", n, kv.desc.n_kv_heads, kv.desc.d, dev)
+    vp, vs = _heads(v, "v", n, kv.desc.n_kv_heads, kv.desc.d, dev)
+    if v.dtype != k.dtype:
+        raise StqError(-1, "k and v must have one element type")
+    _call("stq_kv_store", dev, stream, kv.ref, kv.ptr, kv.bytes, _dev(slots, torch.int64, "slots", n, dev), n, kp, vp,
+          ks, vs, _type(k, "k"))
+
+
+def stq_kv_fetch(kv, slots, k_out, v_out, stream=None):
+    """slots int64 [tokens]; k_out, v_out contiguous [tokens][n_kv_heads][d] of one element type."""
+    import torch
+    n, dev = slots.numel(), kv.device
+    want = n * kv.desc.n_kv_heads * kv.desc.d
+    _call("stq_kv_fetch", dev, stream, kv.ref, kv.ptr, kv.bytes, _dev(slots, torch.int64, "slots", n, dev), n,
+          _dev(k_out, k_out.dtype, "k_out", want, dev), _dev(v_out, k_out.dtype, "v_out", want, dev),
+          _type(k_out, "k_out"))
+
+
+def stq_kv_attend_bytes(kv, n_req, n_tok, n_heads, max_new, max_len, window=0, n_sink=0):
+    """Bytes of the workspace that stq_kv_attend takes for these sizes (0: none)."""
+    a = _AttendDesc(n_req, n_tok, n_heads, STQ_BF16, 1, max_new, max_len, window, n_sink, 1.0, 0, 0)
+    return int(_L.stq_kv_attend_bytes(kv.ref, ctypes.byref(a)))
+
+
+def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, window=0, n_sink=0, work=None, stream=None):
+    """table int32 [requests][cols]; tok_start int32 [requests + 1]; lens int32
+    [requests]; q, o [tokens][n_heads][d], bfloat16 or float16; work: uint8
+    tensor of at least stq_kv_attend_bytes(...) bytes (None where that is 0)."""
+    import torch
+    i, dev = torch.int32, kv.device
+    if table.dim() != 2:
+        raise StqError(-1, "table must be [requests][columns]")
+    n, cols = table.shape
+    qp, qs = _heads(q, "q", None, None, kv.desc.d, dev)
+    tok, heads, d = q.shape
+    op, os_ = _heads(o, "o", tok, heads, d, dev)
+    ty = _type(q, "q", (STQ_BF16, STQ_FP16))
+    if o.dtype != q.dtype:
+        raise StqError(-1, "o must have the type of q")
+    desc = _AttendDesc(n, tok, heads, ty, cols, max_new, max_len, window, n_sink, scale, qs, os_)
+    _call("stq_kv_attend", dev, stream, kv.ref, kv.ptr, kv.bytes, ctypes.byref(desc), _dev(table, i, "table", None, dev),
+          _dev(tok_start, i, "tok_start", n + 1, dev), _dev(lens, i, "lens", n, dev), qp, op,
+          _dev(work, torch.uint8, "work", None, dev), 0 if work is None else work.numel())
