@@ -312,53 +312,83 @@ def stq_requant_fixed_scales(pool, slots, stream=None):
 
 # ------------------------------------------- the softmax layers' operators
 
-def _type(t, what, allowed=(STQ_BF16, STQ_FP16, STQ_FP32)):
+def _type_codes():
     import torch
-    code = {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}.get(t.dtype)
+    return {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}
+
+
+_TYPES = _type_codes()
+
+
+def _type(t, what, allowed=(STQ_BF16, STQ_FP16, STQ_FP32)):
+    code = _TYPES.get(t.dtype)
     if code not in allowed:
         raise StqError(-1, "%s has element type %s" % (what, t.dtype))
     return code
 
 
-def _heads(t, what, n=None, heads=None, d=None, device=None):
-    """(pointer, token stride) of a [tokens][heads][d] CUDA tensor whose heads are
-    contiguous within a token; n, heads, d, device: what it has to be."""
+def _ptr(t, dtype, what, numel, index):
+    """Address of a contiguous CUDA tensor of `dtype` with `numel` elements on
+    device `index`: the per-token calls' checks, as few Python steps as they
+    take (0.5 us a tensor; _dev words the refusal)."""
+    if t.dtype is dtype and t.numel() == numel and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    import torch
+    _dev(t, dtype, what, numel, torch.device("cuda", index))
+    raise StqError(-1, "%s is on %s, expected cuda:%d" % (what, t.device, index))
+
+
+def _heads(t, what, n, heads, d, index):
+    """(address, token stride) of a [tokens][heads][d] CUDA tensor whose heads are
+    contiguous within a token; n, heads, d, index: what it has to be (None: anything)."""
     if t is None or t.dim() != 3:
         raise StqError(-1, "%s must be [tokens][heads][d]" % what)
     a, b, c = t.shape
     if (n is not None and a != n) or (heads is not None and b != heads) or (d is not None and c != d):
         raise StqError(-1, "%s is %s, expected [%s][%s][%s]" % (what, (a, b, c), n, heads, d))
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise StqError(-1, "%s is on %s, expected %s" % (what, t.device, device or "a CUDA device"))
-    st = t.stride()
-    if st[2] != 1 or (b > 1 and st[1] != c):
+    i = t.get_device()
+    if i < 0 or (index is not None and i != index):
+        raise StqError(-1, "%s is on %s, expected %s" % (what, t.device, "cuda" if index is None else "cuda:%d" % index))
+    st, sh, sc = t.stride()
+    if sc != 1 or (b > 1 and sh != c):
         raise StqError(-1, "%s: the heads of a token must be contiguous" % what)
-    return ctypes.c_void_p(t.data_ptr()), max(st[0], b * c) if a > 1 else b * c
+    return t.data_ptr(), st if a > 1 and st > b * c else b * c
 
 
-def _call(name, device, stream, *args):
-    """One library call on `device` and its current stream (or the given one)."""
+def _i32(v, what):
+    """A count that the C struct holds in 32 bits (ctypes would drop the rest in silence)."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise StqError(-1, "%s = %s does not fit 32 bits" % (what, v))
+    return v
+
+
+def _call(name, index, stream, *args):
+    """One library call on device `index` and its current stream (or the given one)."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    st = ctypes.c_void_p(getattr(stream, "cuda_stream", stream))
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            r = getattr(_L, name)(*args, st)
+        stream = torch._C._cuda_getCurrentRawStream(index)
     else:
-        r = getattr(_L, name)(*args, st)
-    _check(r, name)
+        stream = getattr(stream, "cuda_stream", stream)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            r = getattr(_L, name)(*args, stream)
+    else:
+        r = getattr(_L, name)(*args, stream)
+    if r != STQ_OK:
+        raise StqError(r, name)
 
 
 class _Kv:
     def __init__(self, desc, pages):
-        self.desc, self.pages, self.device = desc, pages, pages.device
-        self.ref, self.ptr, self.bytes = ctypes.byref(desc), ctypes.c_void_p(pages.data_ptr()), pages.numel()
+        self.desc, self.pages, self.index = desc, pages, pages.get_device()
+        self.n_kv_heads, self.d = desc.n_kv_heads, desc.d
+        self.ref, self.ptr, self.bytes = ctypes.byref(desc), pages.data_ptr(), pages.numel()
 
 
 def stq_kv_bytes(n_blocks, block_tokens, n_kv_heads, d):
     """Bytes of the cache's device buffer; 0 for sizes the library does not take."""
-    return int(_L.stq_kv_bytes(ctypes.byref(_KvDesc(int(n_blocks), int(block_tokens), int(n_kv_heads), int(d)))))
+    desc = _KvDesc(*(_i32(int(x), "a size") for x in (n_blocks, block_tokens, n_kv_heads, d)))
+    return _L.stq_kv_bytes(ctypes.byref(desc))
 
 
 def make_kv(pages, block_tokens, n_kv_heads, d):
@@ -378,15 +408,16 @@ def stq_kv_plan(cached, new, free, table, block_tokens, n_blocks, tok_start, len
     outputs tok_start int32 [n+1], lens int32 [n], pos int32 [tokens], slots int64
     [tokens], used int32 [1]."""
     import torch
-    i, dev = torch.int32, table.device
+    i, dev = torch.int32, table.get_device()
     if table.dim() != 2:
         raise StqError(-1, "table must be [requests][columns]")
     n, cols = table.shape
-    tok = pos.numel()
-    _call("stq_kv_plan", dev, stream, n, _dev(cached, i, "cached", n, dev), _dev(new, i, "new", n, dev),
-          _dev(free, i, "free", None, dev), free.numel(), n_blocks, block_tokens, _dev(table, i, "table"), cols, tok,
-          _dev(tok_start, i, "tok_start", n + 1, dev), _dev(lens, i, "lens", n, dev), _dev(pos, i, "pos", tok, dev),
-          _dev(slots, torch.int64, "slots", tok, dev), _dev(used, i, "used", 1, dev))
+    tok, nf = pos.numel(), free.numel()
+    _call("stq_kv_plan", dev, stream, n, _ptr(cached, i, "cached", n, dev), _ptr(new, i, "new", n, dev),
+          _ptr(free, i, "free", nf, dev), _i32(nf, "free entries"), _i32(n_blocks, "n_blocks"),
+          _i32(block_tokens, "block_tokens"), _ptr(table, i, "table", n * cols, dev), cols, _i32(tok, "tokens"),
+          _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), _ptr(pos, i, "pos", tok, dev),
+          _ptr(slots, torch.int64, "slots", tok, dev), _ptr(used, i, "used", 1, dev))
 
 
 def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=None, k_weight=None, pos=None,
@@ -396,9 +427,9 @@ def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=N
     table cos_sin float32 [positions][n_rot], pos int32 [tokens]."""
     import torch
     f = torch.float32
-    qp, qs = _heads(q, "q")
+    qp, qs = _heads(q, "q", None, None, None, None)
     n, hq, d = q.shape
-    dev = q.device
+    dev = q.get_device()
     qop, qos = _heads(q_out, "q_out", n, hq, d, dev)
     ti, to = _type(q, "q"), _type(q_out, "q_out")
     kp, ks, kop, kos, hk = None, 0, None, 0, 0
@@ -406,45 +437,49 @@ def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=N
         kp, ks = _heads(k, "k", n, None, d, dev)
         hk = k.shape[1]
         kop, kos = _heads(k_out, "k_out", n, hk, d, dev)
-        if _type(k, "k") != ti or _type(k_out, "k_out") != to:
+        if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
             raise StqError(-1, "k and k_out must have the types of q and q_out")
     n_rot = n_pos = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2 or pos is None:
             raise StqError(-1, "a rotation takes cos_sin [positions][n_rot] and pos [tokens]")
         n_pos, n_rot = cos_sin.shape
-    desc = _NormDesc(n, hq, hk, d, ti, to, norm, eps, n_rot, rot_pairs, n_pos, qs, ks, qos, kos)
-    _call("stq_qk_norm_rope", dev, stream, ctypes.byref(desc), qp, kp, _dev(q_weight, f, "q_weight", d, dev),
-          _dev(k_weight, f, "k_weight", d, dev), _dev(pos, torch.int32, "pos", n, dev),
-          _dev(cos_sin, f, "cos_sin", None, dev), qop, kop)
+        pos, cos_sin = _ptr(pos, torch.int32, "pos", n, dev), _ptr(cos_sin, f, "cos_sin", n_pos * n_rot, dev)
+    elif pos is not None:
+        raise StqError(-1, "pos without cos_sin")
+    if q_weight is not None:
+        q_weight = _ptr(q_weight, f, "q_weight", d, dev)
+    if k_weight is not None:
+        k_weight = _ptr(k_weight, f, "k_weight", d, dev)
+    desc = _NormDesc(_i32(n, "tokens"), hq, hk, d, ti, to, norm, eps, n_rot, rot_pairs, _i32(n_pos, "positions"), qs, ks, qos, kos)
+    _call("stq_qk_norm_rope", dev, stream, ctypes.byref(desc), qp, kp, q_weight, k_weight, pos, cos_sin, qop, kop)
 
 
 def stq_kv_store(kv, slots, k, v, stream=None):
     """slots int64 [tokens]; k, v [tokens][n_kv_heads][d] of one element type."""
     import torch
-    n, dev = slots.numel(), kv.device
-    kp, ks = _heads(k, "k", n, kv.desc.n_kv_heads, kv.desc.d, dev)
-    vp, vs = _heads(v, "v", n, kv.desc.n_kv_heads, kv.desc.d, dev)
-    if v.dtype != k.dtype:
+    n, dev = slots.numel(), kv.index
+    kp, ks = _heads(k, "k", n, kv.n_kv_heads, kv.d, dev)
+    vp, vs = _heads(v, "v", n, kv.n_kv_heads, kv.d, dev)
+    if v.dtype is not k.dtype:
         raise StqError(-1, "k and v must have one element type")
-    _call("stq_kv_store", dev, stream, kv.ref, kv.ptr, kv.bytes, _dev(slots, torch.int64, "slots", n, dev), n, kp, vp,
-          ks, vs, _type(k, "k"))
+    _call("stq_kv_store", dev, stream, kv.ref, kv.ptr, kv.bytes, _ptr(slots, torch.int64, "slots", n, dev), _i32(n, "tokens"),
+          kp, vp, ks, vs, _type(k, "k"))
 
 
 def stq_kv_fetch(kv, slots, k_out, v_out, stream=None):
     """slots int64 [tokens]; k_out, v_out contiguous [tokens][n_kv_heads][d] of one element type."""
     import torch
-    n, dev = slots.numel(), kv.device
-    want = n * kv.desc.n_kv_heads * kv.desc.d
-    _call("stq_kv_fetch", dev, stream, kv.ref, kv.ptr, kv.bytes, _dev(slots, torch.int64, "slots", n, dev), n,
-          _dev(k_out, k_out.dtype, "k_out", want, dev), _dev(v_out, k_out.dtype, "v_out", want, dev),
-          _type(k_out, "k_out"))
+    n, dev = slots.numel(), kv.index
+    want, ty = n * kv.n_kv_heads * kv.d, k_out.dtype
+    _call("stq_kv_fetch", dev, stream, kv.ref, kv.ptr, kv.bytes, _ptr(slots, torch.int64, "slots", n, dev), _i32(n, "tokens"),
+          _ptr(k_out, ty, "k_out", want, dev), _ptr(v_out, ty, "v_out", want, dev), _type(k_out, "k_out"))
 
 
 def stq_kv_attend_bytes(kv, n_req, n_tok, n_heads, max_new, max_len, window=0, n_sink=0):
     """Bytes of the workspace that stq_kv_attend takes for these sizes (0: none)."""
-    a = _AttendDesc(n_req, n_tok, n_heads, STQ_BF16, 1, max_new, max_len, window, n_sink, 1.0, 0, 0)
-    return int(_L.stq_kv_attend_bytes(kv.ref, ctypes.byref(a)))
+    a = _AttendDesc(*(_i32(x, "a size") for x in (n_req, n_tok, n_heads, STQ_BF16, 1, max_new, max_len, window, n_sink)), 1.0, 0, 0)
+    return _L.stq_kv_attend_bytes(kv.ref, ctypes.byref(a))
 
 
 def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, window=0, n_sink=0, work=None, stream=None):
@@ -452,17 +487,21 @@ def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, win
     [requests]; q, o [tokens][n_heads][d], bfloat16 or float16; work: uint8
     tensor of at least stq_kv_attend_bytes(...) bytes (None where that is 0)."""
     import torch
-    i, dev = torch.int32, kv.device
+    i, dev = torch.int32, kv.index
     if table.dim() != 2:
         raise StqError(-1, "table must be [requests][columns]")
     n, cols = table.shape
-    qp, qs = _heads(q, "q", None, None, kv.desc.d, dev)
+    qp, qs = _heads(q, "q", None, None, kv.d, dev)
     tok, heads, d = q.shape
     op, os_ = _heads(o, "o", tok, heads, d, dev)
     ty = _type(q, "q", (STQ_BF16, STQ_FP16))
-    if o.dtype != q.dtype:
+    if o.dtype is not q.dtype:
         raise StqError(-1, "o must have the type of q")
-    desc = _AttendDesc(n, tok, heads, ty, cols, max_new, max_len, window, n_sink, scale, qs, os_)
-    _call("stq_kv_attend", dev, stream, kv.ref, kv.ptr, kv.bytes, ctypes.byref(desc), _dev(table, i, "table", None, dev),
-          _dev(tok_start, i, "tok_start", n + 1, dev), _dev(lens, i, "lens", n, dev), qp, op,
-          _dev(work, torch.uint8, "work", None, dev), 0 if work is None else work.numel())
+    wp = wn = 0
+    if work is not None:
+        wn = work.numel()
+        wp = _ptr(work, torch.uint8, "work", wn, dev)
+    desc = _AttendDesc(n, _i32(tok, "tokens"), heads, ty, _i32(cols, "table columns"), _i32(max_new, "max_new"),
+                       _i32(max_len, "max_len"), _i32(window, "window"), _i32(n_sink, "n_sink"), scale, qs, os_)
+    _call("stq_kv_attend", dev, stream, kv.ref, kv.ptr, kv.bytes, ctypes.byref(desc), _ptr(table, i, "table", n * cols, dev),
+          _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), qp, op, wp, wn)

@@ -443,6 +443,15 @@ __device__ __forceinline__ float sum_quads(float x) {
 
 constexpr float NEG_INF = -__builtin_inff();
 
+// Power of two that brings a row's largest magnitude m into [2^14, 2^15), and
+// the factor that turns products of such rows into base-2 logits.
+__device__ __forceinline__ int q_shift(float m) {
+  return m > 0.0f && m < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
+}
+__device__ __forceinline__ float q_factor(float scale_log2, int e) {
+  return __builtin_fmaxf(__builtin_ldexpf(__builtin_fabsf(scale_log2), -e), 1.17549435e-38f);
+}
+
 // A wave's query rows as matrix operands: row n = lane % 16 of tile nt, the
 // channels (D/4) G .. + D/4 of lane group G = lane / 16, in binary16 scaled by
 // a power of two that puts the row's largest magnitude in [2^14, 2^15) (exact
@@ -463,14 +472,13 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, bool on, int64_t at, f
 #pragma unroll
   for (int i = 0; i < D / 4; i++) m = __builtin_fmaxf(m, __builtin_fabsf(x[i]));
   m = max_quads(m);
-  int e = 0;
-  if (m > 0.0f && m < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(m) + 1;
+  const int e = q_shift(m);
   const float sign = A.scale_log2 < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
   for (int i = 0; i < D / 32; i++)
 #pragma unroll
     for (int j = 0; j < 8; j++) q[i][j] = (f16)(sign * __builtin_ldexpf(x[8 * i + j], e));
-  *c = __builtin_fmaxf(__builtin_ldexpf(__builtin_fabsf(A.scale_log2), -e), 1.17549435e-38f);
+  *c = q_factor(A.scale_log2, e);
 }
 
 // One chunk (32 cached tokens of one head) as a wave loads it.  Token 8G' + i
@@ -525,10 +533,12 @@ __device__ __forceinline__ void load_chunk(const AttnArgs& A, Chunk<D>& C, int b
   C.vs[1] = s[1];
 }
 
-// scale byte j of a dword as the binary32 power of two
+// Scale byte j of a dword where v_cvt_scalef32_* takes a scale: in the
+// exponent field of a binary32 (the conversion reads nothing else of it, and
+// gives NaN for the byte 255).
 template <int J>
 __device__ __forceinline__ float scale_of(uint32_t w) {
-  return bits_f((J < 3 ? w << (23 - 8 * J) : w >> 1) & 0x7F800000u);
+  return bits_f(J < 3 ? w << (23 - 8 * J) : w >> 1);
 }
 template <int J>
 __device__ __forceinline__ uint32_t cvt2(uint32_t w, float s) {   // codes 2J, 2J+1 of w as a binary16 pair
@@ -553,16 +563,13 @@ __device__ __forceinline__ void chunk_step(const AttnArgs& A, const Chunk<D>& C,
   f32x4 s[NT][2];
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    const float sc = bits_f(C.ks[u] << 23);
-    const bool nan = C.ks[u] == 255u;
+    const float sc = scale_of<0>(C.ks[u]);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) s[nt][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < D / 32; i++) {
       const uint32_t w = C.k[u][i];
-      uint32_t a = cvt2<0>(w, sc);
-      if (i == 0) a = nan ? 0x7E007E00u : a;           // a poisoned key: one NaN reaches every query
-      const f16x8 kf = frag(a, cvt2<1>(w, sc), cvt2<2>(w, sc), cvt2<3>(w, sc));
+      const f16x8 kf = frag(cvt2<0>(w, sc), cvt2<1>(w, sc), cvt2<2>(w, sc), cvt2<3>(w, sc));
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) s[nt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[nt][i], s[nt][u], 0, 0, 0);
     }
@@ -610,7 +617,7 @@ __device__ __forceinline__ void chunk_step(const AttnArgs& A, const Chunk<D>& C,
   vs[4] = scale_of<0>(C.vs[1]); vs[5] = scale_of<1>(C.vs[1]); vs[6] = scale_of<2>(C.vs[1]); vs[7] = scale_of<3>(C.vs[1]);
   if (MASK) {     // unwritten bytes behind the last token: any finite value, their weights are 0
 #pragma unroll
-    for (int j = 0; j < 8; j++) vs[j] = bits_f(min(__float_as_uint(vs[j]), (uint32_t)(E_MAX + 127) << 23));
+    for (int j = 0; j < 8; j++) vs[j] = bits_f(min(__float_as_uint(vs[j]) & 0x7F800000u, (uint32_t)(E_MAX + 127) << 23));
   }
   constexpr int NB = D / 32;                            // bytes of one token and lane
 #pragma unroll
@@ -774,6 +781,267 @@ __global__ void __launch_bounds__(256) k_attend_rows(AttnArgs A) {
   }
 }
 
+// Many query rows per key/value head (prompts): the matrix products bound the
+// work.  One workgroup = one (request, head, tile of 32 NW rows, split), each
+// wave 32 rows.  Tiles of 64 cached tokens (two chunks) go through LDS as
+// binary16, unpacked once for all the waves, double buffered: while the waves
+// work on one tile, the next one's bytes are converted and the one after it
+// is on its way from memory.  One barrier per tile.
+//
+// Products as in k_attend_rows (transposed, so that a lane keeps one query
+// row's statistics), on the 32x32x16 shape: lane n = lane % 32 is query row
+// n, and lane half G holds tokens 8a + 4G + b (b < 4) of a 32-token chunk in
+// elements 4a + b.  Eight consecutive elements are the operand of a product
+// over 16 tokens; the values meet it through ds_read_tr16_b64, which gives
+// lane i of 16 lanes channel i of four tokens whose 16-channel rows the lanes
+// address (lane 4t + c: channels 4c.. of token t).
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __fp16 fp16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) fp16x4 lds_fp16x4;
+
+// 16-byte slot of (token t of 64, channels 8c ..): rows rotated so that the 16
+// lanes of a read or write phase touch 16 different slots of the banks.
+template <int D>
+__device__ __forceinline__ int k_slot(int t, int c) {
+  if constexpr (D == 128) return t * 16 + ((c + t) & 15);
+  else return t * 8 + ((c + (t >> 1)) & 7);
+}
+template <int D>
+__device__ __forceinline__ int v_slot(int t, int c) {
+  if constexpr (D == 128) return t * 16 + ((c + 4 * (t & 3) + ((t >> 2) & 3)) & 15);
+  else return t * 8 + ((c + 4 * ((t >> 1) & 1) + ((t >> 2) & 3)) & 7);
+}
+
+__device__ __forceinline__ float max_halves(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(bits_f(a[0]), bits_f(a[1]));
+}
+
+template <int D, int TYPE, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
+  constexpr int NT = 64 * NW, ROWS = 32 * NW;
+  constexpr int KP = 2 * D;                            // 16-byte pieces of a tile's key codes (32 channels of a token)
+  constexpr int NP = (2 * KP + NT - 1) / NT;           // pieces of keys and values per thread
+  constexpr int KSTEP = D / 16, NC = D / 32;
+  __shared__ u32x4 sk[2][64 * D / 8], sv[2][64 * D / 8];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, G = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // (request, head) pairs fastest, the tiles with the most to see first: a pair's
+  // workgroups share an XCD where the pairs are a multiple of 8
+  int b = blockIdx.x;
+  const int pairs = A.n_req * A.hkv, pair = b % pairs; b /= pairs;
+  const int sp = b % A.splits, tile = A.tiles - 1 - b / A.splits;
+  const int h = pair % A.hkv, i = pair / A.hkv;
+  const Req R = req_args(A, i);
+  const int row0 = tile * ROWS, rows = min(R.n_new, A.max_new) * A.group;
+  if (row0 >= rows) return;
+  const int p0 = R.base + row0 / A.group, p1 = R.base + (min(row0 + ROWS, rows) - 1) / A.group;
+  const Span sn = span_of(p0, p1, A.window, A.sink);
+  const int per = split_chunks(sn.total, A.splits);
+  const int c0 = sp * per, c1 = min(c0 + per, sn.total);
+  if (c0 >= c1 && sp > 0) return;
+  const int parts = (sn.total + per - 1) / per;
+
+  // the wave's rows
+  const int r = row0 + 32 * wave + n, j = r / A.group, g = r - j * A.group;
+  const bool on = r < rows;
+  const int pw1 = R.base + (min(row0 + 32 * wave + 32, rows) - 1) / A.group;
+  const int pw0 = min(R.base + (row0 + 32 * wave) / A.group, pw1), pos = on ? R.base + j : pw1;
+  f16x8 q[KSTEP];
+  float cf;
+  {
+    float x[D / 2];
+    const int64_t at = (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + 8 * G;
+#pragma unroll
+    for (int s = 0; s < KSTEP; s++) {
+      if (on) load8<TYPE>(A.q, at + 16 * s, x + 8 * s);
+      else
+#pragma unroll
+        for (int u = 0; u < 8; u++) x[8 * s + u] = 0.0f;
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < D / 2; u++) m = __builtin_fmaxf(m, __builtin_fabsf(x[u]));
+    m = max_halves(m);
+    const int e = q_shift(m);
+    const float sign = A.scale_log2 < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int s = 0; s < KSTEP; s++)
+#pragma unroll
+      for (int u = 0; u < 8; u++) q[s][u] = (f16)(sign * __builtin_ldexpf(x[8 * s + u], e));
+    cf = q_factor(A.scale_log2, e);
+  }
+  f32x16 o[NC];
+#pragma unroll
+  for (int c = 0; c < NC; c++)
+#pragma unroll
+    for (int u = 0; u < 16; u++) o[c][u] = 0.0f;
+  float M = NEG_INF, L = 0.0f;
+
+  const int32_t* tab = A.table + (int64_t)i * A.cols;
+  const int per_blk = A.T >> 5, T = A.T;
+  auto chunk_at = [&](int k) { return k < sn.n_low ? k : sn.lo + k - sn.n_low; };
+  u32x4 raw[NP];
+  uint32_t sb[NP];
+  // this thread's pieces of chunks k, k + 1
+  auto fetch = [&](int k) {
+#pragma unroll
+    for (int s = 0; s < NP; s++) {
+      const int p = tid + s * NT;
+      if (2 * KP % NT && p >= 2 * KP) break;
+      const bool isv = p >= KP;
+      const int pp = isv ? p - KP : p;
+      const int u = pp / D, w = pp % D;                  // chunk, piece of it: D pieces
+      // keys: pieces of a token side by side; values: tokens side by side (the bank layouts of the writes)
+      const int t = isv ? w & 31 : w / (D / 32), c = isv ? w >> 5 : w % (D / 32);
+      const int ch = chunk_at(min(k + u, c1 - 1));
+      int blk = ld_const(tab + ch / per_blk);
+      blk = (uint32_t)blk < (uint32_t)A.n_blocks ? blk : 0;
+      const int off = ((ch * 32) & (T - 1)) + t;
+      const uint8_t* hb = A.cache + ((int64_t)blk * A.hkv + h) * (T * D / 16 * 17);
+      raw[s] = *(const u32x4*)(hb + (isv ? T * (D / 2) : 0) + off * (D / 2) + 16 * c);
+      sb[s] = hb[T * D + (isv ? T * (D / 32) : 0) + c * T + off];
+    }
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int s = 0; s < NP; s++) {
+      const int p = tid + s * NT;
+      if (2 * KP % NT && p >= 2 * KP) break;
+      const bool isv = p >= KP;
+      const int pp = isv ? p - KP : p;
+      const int u = pp / D, w = pp % D;
+      const int t = 32 * u + (isv ? w & 31 : w / (D / 32)), c = 4 * (isv ? w >> 5 : w % (D / 32));
+      // values: unwritten bytes behind the last token must not be NaN or infinite, their weights are 0
+      const float sc = scale_of<0>(isv ? min(sb[s], (uint32_t)(E_MAX + 127)) : sb[s]);
+#pragma unroll
+      for (int x = 0; x < 4; x++) {
+        const uint32_t d = raw[s][x];
+        const u32x4 v = {cvt2<0>(d, sc), cvt2<1>(d, sc), cvt2<2>(d, sc), cvt2<3>(d, sc)};
+        if (isv) sv[buf][v_slot<D>(t, c + x)] = v;
+        else sk[buf][k_slot<D>(t, c + x)] = v;
+      }
+    }
+  };
+  auto block_of = [&](int k) { return ld_const(tab + chunk_at(k) / per_blk); };
+  // rows that see all of chunk k
+  auto whole = [&](int k) {
+    if (k >= c1 || (uint32_t)block_of(k) >= (uint32_t)A.n_blocks) return false;
+    const int t0 = chunk_at(k) * 32, t1 = t0 + 31;
+    return t1 <= pw0 && (A.window == 0 || t0 > pw1 - A.window || t1 < A.sink);
+  };
+  if (c0 < c1) {
+    fetch(c0);
+    put(0);
+    if (c0 + 2 < c1) fetch(c0 + 2);
+    __syncthreads();
+    int buf = 0;
+    for (int k = c0; k < c1; k += 2, buf ^= 1) {
+      if (k + 2 < c1) {
+        put(buf ^ 1);
+        if (k + 4 < c1) fetch(k + 4);
+      }
+      if (chunk_at(k) * 32 <= pw1) {                    // else every token lies behind the wave's rows
+        f32x16 s[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+#pragma unroll
+          for (int x = 0; x < 16; x++) s[u][x] = 0.0f;
+#pragma unroll
+          for (int x = 0; x < KSTEP; x++) {
+            const f16x8 kf = __builtin_bit_cast(f16x8, sk[buf][k_slot<D>(32 * u + n, 2 * x + G)]);
+            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[x], s[u], 0, 0, 0);
+          }
+        }
+        if (!(whole(k) && whole(k + 1))) {
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            const bool there = k + u < c1 && (uint32_t)block_of(min(k + u, c1 - 1)) < (uint32_t)A.n_blocks;
+            const int t0 = chunk_at(min(k + u, c1 - 1)) * 32 + 4 * G;
+#pragma unroll
+            for (int x = 0; x < 16; x++) {
+              const int t = t0 + 8 * (x >> 2) + (x & 3);
+              const bool see = t <= pos && (A.window == 0 || t > pos - A.window || t < A.sink) && there;
+              s[u][x] = see ? s[u][x] : NEG_INF;
+            }
+          }
+        }
+        float m = s[0][0];
+#pragma unroll
+        for (int x = 1; x < 32; x++) m = __builtin_fmaxf(m, s[x >> 4][x & 15]);
+        m = __builtin_fmaxf(M, max_halves(m));
+        const float mc = m == NEG_INF ? 0.0f : m * cf;
+        if (__any(m > M)) {
+          const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(M, cf, -mc));
+          L *= f;
+#pragma unroll
+          for (int c = 0; c < NC; c++)
+#pragma unroll
+            for (int x = 0; x < 16; x++) o[c][x] *= f;
+          M = m;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+#pragma unroll
+          for (int y = 0; y < 2; y++) {                 // 16 tokens
+            uint32_t pk[4];
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+              const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x], cf, -mc));
+              const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x + 1], cf, -mc));
+              const f16x2 hh = {(f16)e0, (f16)e1};
+              pk[x] = h2_bits(hh);
+              L = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, L, false);
+            }
+            const f16x8 P = frag(pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+            for (int c = 0; c < NC; c++) {
+              const int t = 32 * u + 16 * y + 4 * G + ((lane >> 2) & 3);
+              const int cb = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);   // channels cb .. cb + 3
+              u32x4* base = sv[buf];
+              const fp16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+                  (lds_fp16x4*)((uint8_t*)(base + v_slot<D>(t, cb >> 3)) + 8 * ((cb >> 2) & 1)));
+              const fp16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+                  (lds_fp16x4*)((uint8_t*)(base + v_slot<D>(t + 8, cb >> 3)) + 8 * ((cb >> 2) & 1)));
+              const u32x2 a = __builtin_bit_cast(u32x2, lo), d = __builtin_bit_cast(u32x2, hi);
+              o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(a[0], a[1], d[0], d[1]), P, o[c], 0, 0, 0);
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+  {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(L), __float_as_uint(L), false, false);
+    L = bits_f(a[0]) + bits_f(a[1]);
+  }
+  if (!on) return;
+  // element 4a + b of tile c: channel 32c + 8a + 4G + b
+  if (parts <= 1) {
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint16_t* out = (uint16_t*)A.o + (int64_t)(R.first + j) * A.os + (int64_t)(h * A.group + g) * D + 4 * G;
+#pragma unroll
+    for (int c = 0; c < NC; c++)
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+        *(u32x2*)(out + 32 * c + 8 * a) = (u32x2){pack2<TYPE>(o[c][4 * a] * inv, o[c][4 * a + 1] * inv),
+                                                  pack2<TYPE>(o[c][4 * a + 2] * inv, o[c][4 * a + 3] * inv)};
+  } else {
+    const int64_t row = (int64_t)sp * A.n_tok * A.hq + (int64_t)(R.first + j) * A.hq + h * A.group + g;
+    if (G == 0) {
+      A.pml[2 * row] = M == NEG_INF ? NEG_INF : M * cf;
+      A.pml[2 * row + 1] = L;
+    }
+    float* out = A.po + row * D + 4 * G;
+#pragma unroll
+    for (int c = 0; c < NC; c++)
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+        *(f32x4*)(out + 32 * c + 8 * a) = (f32x4){o[c][4 * a], o[c][4 * a + 1], o[c][4 * a + 2], o[c][4 * a + 3]};
+  }
+}
+
 // Join the splits of one row: one wave per row, its channels over the lanes,
 // the splits in order.
 template <int D, int TYPE>
@@ -836,13 +1104,17 @@ bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
          (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
          a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
 }
-struct Split { int tiles, tile_rows, splits; };
+struct Split { int tiles, tile_rows, splits; bool staged; };
+// Query rows per key/value head from which the cache is staged through LDS.
+constexpr int STAGED_ROWS = 64;
+constexpr int TILE_WAVES = 4;
 // Workgroups wanted in all: enough for every CU to hold several and for ragged lengths to even out.
 constexpr int64_t WANT_GROUPS = 1536;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
   const int64_t rows = (int64_t)a->max_new * (a->n_heads / d->n_kv_heads);
-  s.tile_rows = 16;
+  s.staged = rows > STAGED_ROWS;
+  s.tile_rows = s.staged ? 32 * TILE_WAVES : 16;
   s.tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
   const int64_t base = (int64_t)a->n_req * d->n_kv_heads * s.tiles;
   int64_t seen = a->max_len;
@@ -859,7 +1131,8 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
 template <int D, int TYPE>
 void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
-  hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1>), dim3(grid), dim3(256), 0, st, A);
+  if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE, TILE_WAVES>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
+  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1>), dim3(grid), dim3(256), 0, st, A);
   if (A.splits > 1) {
     const int64_t rows = (int64_t)A.n_req * A.max_new * A.hq;
     hipLaunchKernelGGL((k_attend_join<D, TYPE>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, A, s.tile_rows);

@@ -169,6 +169,9 @@ class Fake:
     def data_ptr(self):
         return self._ptr
 
+    def get_device(self):
+        return self.device.index
+
 
 def test_binding_refusals(stq, monkeypatch):
     import torch
@@ -221,6 +224,11 @@ def test_binding_refusals(stq, monkeypatch):
         args.update(bad)
         with pytest.raises(E):
             stq.stq_qk_norm_rope(stream=0, **args)
+    for bad in (dict(max_new=2 ** 32 + 1), dict(max_len=2 ** 31), dict(window=2 ** 32), dict(n_sink=-2 ** 40)):
+        args = dict(ok, max_new=2, max_len=100)
+        args.update(bad)
+        with pytest.raises(E, match="32 bits"):
+            stq.stq_kv_attend(kv, scale=0.1, stream=0, **args)
     one = dict(cached=Fake([2], i), new=Fake([2], i), free=Fake([9], i), table=Fake([2, 5], i), block_tokens=64, n_blocks=10,
                tok_start=Fake([3], i), lens=Fake([2], i), pos=Fake([7], i), slots=Fake([7], l), used=Fake([1], i))
     for bad in (dict(cached=Fake([3], i)), dict(new=Fake([2], l)), dict(free=Fake([9], l)), dict(table=Fake([10], i)),
