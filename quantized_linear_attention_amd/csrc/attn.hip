@@ -394,7 +394,7 @@ struct AttnArgs {
   const void* q;
   void* o;
   float *po, *pml;          // partial results: [split][row][D], [split][row][2]
-  int n_req, n_tok, hq, hkv, group, T, n_blocks, cols, max_new, window, sink, splits, tiles;
+  int n_req, n_tok, hq, hkv, group, T, n_blocks, cols, max_new, window, sink, splits, per, tiles;
   int64_t qs, os;
   float scale_log2;
 };
@@ -411,12 +411,6 @@ __device__ __forceinline__ Span span_of(int p0, int p1, int window, int sink) {
   s.total = s.n_low + (p1 >> 5) + 1 - s.lo;
   return s;
 }
-// Chunks of one split: the work is cut into `splits` equal parts, but not
-// below SPLIT_MIN chunks; a part holds a multiple of four (one per wave).
-constexpr int SPLIT_MIN = 8;
-__device__ __forceinline__ int split_chunks(int total, int splits) {
-  return max((((total + splits - 1) / splits) + 3) & ~3, SPLIT_MIN);
-}
 struct Req { int first, n_new, len, base; };   // first row, query tokens, cached tokens, position of query 0
 __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
   Req r;
@@ -426,6 +420,14 @@ __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
   r.len = (int)min((int64_t)max(ld_const(A.len + i), 0), (int64_t)A.cols * A.T);
   r.base = r.len - r.n_new;
   return r;
+}
+
+// Chunks of one part of a request's work: the host's size for a request of the
+// stated longest length, more for a request that is longer than that (a
+// multiple of four: one per wave).  Shorter requests have fewer parts, all of
+// one size.
+__device__ __forceinline__ int split_chunks(const AttnArgs& A, int total) {
+  return max(((total + A.splits - 1) / A.splits + 3) & ~3, A.per);
 }
 
 __device__ __forceinline__ float max_quads(float x) {   // over the four 16-lane groups
@@ -439,6 +441,14 @@ __device__ __forceinline__ float sum_quads(float x) {
   x = bits_f(a[0]) + bits_f(a[1]);
   auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return bits_f(b[0]) + bits_f(b[1]);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+  x = __builtin_fmaxf(x, dpp<0xB1>(x));
+  x = __builtin_fmaxf(x, dpp<0x4E>(x));
+  x = __builtin_fmaxf(x, dpp<0x141>(x));
+  x = __builtin_fmaxf(x, dpp<0x140>(x));
+  return max_quads(x);
 }
 
 constexpr float NEG_INF = -__builtin_inff();
@@ -459,15 +469,10 @@ __device__ __forceinline__ float q_factor(float scale_log2, int e) {
 // from scaled products to base-2 logits, kept positive (a negative scale
 // turns the queries' signs) and normal.
 template <int D, int TYPE>
-__device__ __forceinline__ void load_q(const AttnArgs& A, bool on, int64_t at, f16x8* q, float* c) {
+__device__ __forceinline__ void load_q(const AttnArgs& A, int64_t at, f16x8* q, float* c) {
   float x[D / 4];
 #pragma unroll
-  for (int i = 0; i < D / 32; i++) {
-    if (on) load8<TYPE>(A.q, at + 8 * i, x + 8 * i);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; j++) x[8 * i + j] = 0.0f;
-  }
+  for (int i = 0; i < D / 32; i++) load8<TYPE>(A.q, at + 8 * i, x + 8 * i);
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 4; i++) m = __builtin_fmaxf(m, __builtin_fabsf(x[i]));
@@ -490,45 +495,48 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, bool on, int64_t at, f
 template <int D>
 struct Chunk {
   static constexpr int KD = D / 32;                    // dwords of keys per tile and lane
-  static constexpr int KS = D > 128 ? 2 : 1;           // key scales per tile and lane
   uint32_t k[2][KD], v[8];
   uint32_t ks[2];
   uint32_t vs[2];
-  bool dead;                                           // its block's table entry is no block
 };
 
+// A lane's places in a chunk, the same for every chunk (bytes from the chunk's
+// first key code, value code, key scale, value scale).
 template <int D>
-__device__ __forceinline__ void load_chunk(const AttnArgs& A, Chunk<D>& C, int blk, int h, int chunk) {
-  const int lane = threadIdx.x & 63, m = lane & 15, G = lane >> 4;
-  const int T = A.T, off = (chunk * 32) & (T - 1);
-  C.dead = (uint32_t)blk >= (uint32_t)A.n_blocks;
-  const uint8_t* hb = A.cache + ((int64_t)(C.dead ? 0 : blk) * A.hkv + h) * (T * D / 16 * 17);
-  const uint8_t* kc = hb + off * (D / 2);
-  const uint8_t* vc = kc + T * (D / 2);
-  const uint8_t* ksc = hb + T * D + off;
-  const uint8_t* vsc = ksc + T * (D / 32);
-  const int r = 8 * (m >> 2) + (m & 3);
+struct Places {
+  uint32_t k, v, ks, vs;
+  __device__ __forceinline__ explicit Places(int T) {
+    const int lane = threadIdx.x & 63, m = lane & 15, G = lane >> 4, r = 8 * (m >> 2) + (m & 3);
+    k = r * (D / 2) + G * (D / 8);
+    ks = (G * (D / 4) / 32) * T + r;
+    v = 8 * G * (D / 2) + m * (D / 32);
+    vs = (m * (D / 16) / 32) * T + 8 * G;
+  }
+};
+template <int D>
+__device__ __forceinline__ void load_keys(Chunk<D>& C, const Places<D>& W, const uint8_t* codes, const uint8_t* scales) {
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    const uint8_t* p = kc + (r + 4 * u) * (D / 2) + G * (D / 8);
     if constexpr (D == 128) {
-      const u32x4 w = *(const u32x4*)p;
+      const u32x4 w = *(const u32x4*)(codes + (W.k + 4 * u * (D / 2)));
 #pragma unroll
       for (int i = 0; i < 4; i++) C.k[u][i] = w[i];
     } else {
-      const u32x2 w = *(const u32x2*)p;
+      const u32x2 w = *(const u32x2*)(codes + (W.k + 4 * u * (D / 2)));
       C.k[u][0] = w[0];
       C.k[u][1] = w[1];
     }
-    C.ks[u] = ksc[(G * (D / 4) / 32) * T + r + 4 * u];
+    C.ks[u] = scales[W.ks + 4 * u];
   }
+}
+template <int D>
+__device__ __forceinline__ void load_values(Chunk<D>& C, const Places<D>& W, const uint8_t* codes, const uint8_t* scales) {
 #pragma unroll
   for (int j = 0; j < 8; j++) {
-    const uint8_t* p = vc + (8 * G + j) * (D / 2) + m * (D / 32);
-    if constexpr (D == 128) C.v[j] = *(const uint32_t*)p;
-    else C.v[j] = *(const uint16_t*)p;
+    if constexpr (D == 128) C.v[j] = *(const uint32_t*)(codes + (W.v + j * (D / 2)));
+    else C.v[j] = *(const uint16_t*)(codes + (W.v + j * (D / 2)));
   }
-  const u32x2 s = *(const u32x2*)(vsc + (m * (D / 16) / 32) * T + 8 * G);
+  const u32x2 s = *(const u32x2*)(scales + W.vs);
   C.vs[0] = s[0];
   C.vs[1] = s[1];
 }
@@ -538,7 +546,8 @@ __device__ __forceinline__ void load_chunk(const AttnArgs& A, Chunk<D>& C, int b
 // gives NaN for the byte 255).
 template <int J>
 __device__ __forceinline__ float scale_of(uint32_t w) {
-  return bits_f(J < 3 ? w << (23 - 8 * J) : w >> 1);
+  if constexpr (J < 3) return bits_f(w << (23 - 8 * J));
+  else return bits_f(w >> 1);
 }
 template <int J>
 __device__ __forceinline__ uint32_t cvt2(uint32_t w, float s) {   // codes 2J, 2J+1 of w as a binary16 pair
@@ -548,19 +557,42 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
   return __builtin_bit_cast(f16x8, (u32x4){a, b, c, d});
 }
 
-// Running softmax of a wave's 16-row tiles: o is the transposed product, tile
-// c element i = channel (D/16)(4G + i) + c of query row n = lane % 16.
-template <int D, int NT>
-struct Acc {
-  f32x4 o[NT][D / 16];
-  float m[NT], l[NT];      // largest scaled product (all lane groups alike), this lane group's part of the sum
+// What a row's weights are relative to, 2^(product * c - mc).  It follows the
+// row's largest product only when a weight would pass 2^8: until then it stays
+// (binary16 holds weights to 2^15, the sums are binary32, and a quotient does
+// not mind), which spares most steps the exchange between lanes and the
+// rescaling of the sums.
+struct Ref {
+  float m, mc, over;       // the product it stands at, times c; products above `over` move it
+  __device__ __forceinline__ void init() { m = over = NEG_INF; mc = 0.0f; }
+  // to the product x; the factor of what was summed so far.  (Nothing seen yet:
+  // any finite reference will do, every weight is 2^-inf.)
+  __device__ __forceinline__ float move(float x, float c) {
+    const float xc = x == NEG_INF ? 0.0f : x * c;
+    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(m, c, -xc));
+    m = x;
+    mc = xc;
+    over = x + 8.0f * __builtin_amdgcn_rcpf(c);
+    return f;
+  }
 };
 
-template <int D, int NT, bool MASK>
-__device__ __forceinline__ void chunk_step(const AttnArgs& A, const Chunk<D>& C, const f16x8 (*q)[D / 32], const float* c,
-                                           const int* p, int chunk, Acc<D, NT>& S) {
-  const int G = (threadIdx.x & 63) >> 4;
-  f32x4 s[NT][2];
+// acc *= f for the 16 registers from V%c[r] on, where any lane of `far` is set.
+// The branch lies inside the statement and the accumulators at registers of
+// their own: as an `if` around the products, the compiler kept the two sides'
+// accumulators apart and copied one to the other in every step, which costs as
+// much as the rescaling.  (The waits cover a matrix instruction's result read
+// by the multiplications, and theirs read by the next.)
+#define SCALE_WHERE(far, f, first, count, ...)                                                         \
+  asm volatile("s_cmp_eq_u64 %[m], 0\n\ts_cbranch_scc1 .Lkeep%=\n\ts_nop 15\n\ts_nop 7\n\t"            \
+               ".set stq_v, " #first "\n\t.rept " #count "\n\tv_mul_f32 v[stq_v], v[stq_v], %[x]\n\t" \
+               ".set stq_v, stq_v+1\n\t.endr\n\ts_nop 4\n.Lkeep%=:"                                  \
+               : __VA_ARGS__ : [m] "s"(far), [x] "v"(f) : "scc")
+#define AT(r) "+{v[" #r "]}"
+
+// Keys of a chunk and queries -> products s (tile u: tokens 8G + 4u ..).
+template <int D, int NT>
+__device__ __forceinline__ void key_products(const Chunk<D>& C, const f16x8 (*q)[D / 32], f32x4 (*s)[2]) {
 #pragma unroll
   for (int u = 0; u < 2; u++) {
     const float sc = scale_of<0>(C.ks[u]);
@@ -574,54 +606,21 @@ __device__ __forceinline__ void chunk_step(const AttnArgs& A, const Chunk<D>& C,
       for (int nt = 0; nt < NT; nt++) s[nt][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[nt][i], s[nt][u], 0, 0, 0);
     }
   }
-  f16x8 P[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    if (MASK) {
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const int t = chunk * 32 + 8 * G + e;
-        const bool see = t <= p[nt] && (A.window == 0 || t > p[nt] - A.window || t < A.sink) && !C.dead;
-        s[nt][e >> 2][e & 3] = see ? s[nt][e >> 2][e & 3] : NEG_INF;
-      }
-    }
-    float m = s[nt][0][0];
-#pragma unroll
-    for (int e = 1; e < 8; e++) m = __builtin_fmaxf(m, s[nt][e >> 2][e & 3]);
-    m = __builtin_fmaxf(S.m[nt], max_quads(m));
-    // nothing seen so far: any finite reference will do, every weight is 2^-inf
-    const float mc = m == NEG_INF ? 0.0f : m * c[nt];
-    if (__any(m > S.m[nt])) {
-      const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(S.m[nt], c[nt], -mc));
-      S.l[nt] *= f;
-#pragma unroll
-      for (int i = 0; i < D / 16; i++) S.o[nt][i] *= f;
-      S.m[nt] = m;
-    }
-    // Weights to binary16 in pairs; the sum takes the same rounded weights, so
-    // that a weight's rounding moves o by its own part only.
-    uint32_t pk[4];
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1)], c[nt], -mc));
-      const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1) + 1], c[nt], -mc));
-      const f16x2 h = {(f16)a, (f16)b};
-      pk[e] = h2_bits(h);
-      S.l[nt] = __builtin_amdgcn_fdot2(h, (f16x2){(f16)1.0f, (f16)1.0f}, S.l[nt], false);
-    }
-    P[nt] = frag(pk[0], pk[1], pk[2], pk[3]);
-  }
-  // Values: pairs of tokens of one channel, from pairs of channels of one token.
+}
+// Values of a chunk and weights: o += V^T P, tile c element i = channel
+// (D/16)(4G + i) + c of query row lane % 16.  Pairs of tokens of one channel
+// are put together from pairs of channels of one token.
+template <int D, int NT>
+__device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, const f16x8* P, f32x4 (*o)[D / 16]) {
   float vs[8];
   vs[0] = scale_of<0>(C.vs[0]); vs[1] = scale_of<1>(C.vs[0]); vs[2] = scale_of<2>(C.vs[0]); vs[3] = scale_of<3>(C.vs[0]);
   vs[4] = scale_of<0>(C.vs[1]); vs[5] = scale_of<1>(C.vs[1]); vs[6] = scale_of<2>(C.vs[1]); vs[7] = scale_of<3>(C.vs[1]);
-  if (MASK) {     // unwritten bytes behind the last token: any finite value, their weights are 0
+  if (!full) {    // unwritten bytes behind the last token: any finite value, their weights are 0
 #pragma unroll
     for (int j = 0; j < 8; j++) vs[j] = bits_f(min(__float_as_uint(vs[j]) & 0x7F800000u, (uint32_t)(E_MAX + 127) << 23));
   }
-  constexpr int NB = D / 32;                            // bytes of one token and lane
 #pragma unroll
-  for (int b = 0; b < NB; b++) {
+  for (int b = 0; b < D / 32; b++) {                   // bytes of one token and lane
     uint32_t lo[4], hi[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -636,8 +635,8 @@ __device__ __forceinline__ void chunk_step(const AttnArgs& A, const Chunk<D>& C,
     const f16x8 fl = frag(lo[0], lo[1], lo[2], lo[3]), fh = frag(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-      S.o[nt][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fl, P[nt], S.o[nt][2 * b], 0, 0, 0);
-      S.o[nt][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fh, P[nt], S.o[nt][2 * b + 1], 0, 0, 0);
+      o[nt][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fl, P[nt], o[nt][2 * b], 0, 0, 0);
+      o[nt][2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fh, P[nt], o[nt][2 * b + 1], 0, 0, 0);
     }
   }
 }
@@ -647,135 +646,218 @@ __device__ __forceinline__ void chunk_step(const AttnArgs& A, const Chunk<D>& C,
 // one (request, head, tile of 16 NT rows, split of the cache); its four
 // waves take every fourth chunk straight from memory into the operands'
 // registers and join their running softmaxes through LDS at the end.
+// o *= f of tile nt where any lane of `far` is set (accumulators of 16 rows and
+// D channels: D/4 registers)
+template <int D, int NT>
+__device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D / 16], int nt) {
+  if constexpr (D == 128) {
+    f32x4* x = o[nt];
+    if (nt == 0)
+      SCALE_WHERE(far, f, 96, 32, AT(96:99)(x[0]), AT(100:103)(x[1]), AT(104:107)(x[2]), AT(108:111)(x[3]),
+                  AT(112:115)(x[4]), AT(116:119)(x[5]), AT(120:123)(x[6]), AT(124:127)(x[7]));
+    else
+      SCALE_WHERE(far, f, 128, 32, AT(128:131)(x[0]), AT(132:135)(x[1]), AT(136:139)(x[2]), AT(140:143)(x[3]),
+                  AT(144:147)(x[4]), AT(148:151)(x[5]), AT(152:155)(x[6]), AT(156:159)(x[7]));
+  } else {
+    f32x4* x = o[nt];
+    if (nt == 0)
+      SCALE_WHERE(far, f, 96, 16, AT(96:99)(x[0]), AT(100:103)(x[1]), AT(104:107)(x[2]), AT(108:111)(x[3]));
+    else
+      SCALE_WHERE(far, f, 112, 16, AT(112:115)(x[0]), AT(116:119)(x[1]), AT(120:123)(x[2]), AT(124:127)(x[3]));
+  }
+}
+
+constexpr int ROW_WAVES = 4;
 template <int D, int TYPE, int NT>
-__global__ void __launch_bounds__(256) k_attend_rows(AttnArgs A) {
-  constexpr int NC = D / 16;
-  __shared__ f32x4 so[2][NT * NC][64];
-  __shared__ float sml[4][NT][16][2];
+__global__ void __launch_bounds__(64 * ROW_WAVES, 2) k_attend_rows(AttnArgs A) {
+  constexpr int NC = D / 16, NWV = ROW_WAVES;
+  __shared__ f32x4 so[NWV][NT * NC][64];
+  __shared__ f32x2 sml[NWV][NT][16];
   const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  // the splits slowest: a short request has none of the last ones, and
+  // neighbouring workgroups go to different XCDs
   int b = blockIdx.x;
-  const int sp = b % A.splits; b /= A.splits;
-  const int tile = b % A.tiles; b /= A.tiles;
-  const int h = b % A.hkv, i = b / A.hkv;
+  const int h = b % A.hkv; b /= A.hkv;
+  const int i = b % A.n_req; b /= A.n_req;
+  const int tile = b % A.tiles, sp = b / A.tiles;
   const Req R = req_args(A, i);
   const int row0 = tile * 16 * NT, rows = min(R.n_new, A.max_new) * A.group;
   if (row0 >= rows) return;
   const int j1 = (min(row0 + 16 * NT, rows) - 1) / A.group;
   const int p0 = R.base + row0 / A.group, p1 = R.base + j1;
   const Span sn = span_of(p0, p1, A.window, A.sink);
-  const int per = split_chunks(sn.total, A.splits);
+  const int per = split_chunks(A, sn.total);
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
   if (c0 >= c1 && sp > 0) return;
   const int parts = (sn.total + per - 1) / per;
 
+  const int32_t* tab = A.table + (int64_t)i * A.cols;
+  const int blk_shift = 31 - __builtin_clz(A.T) - 5;    // chunks of a block, as a power of two
+  auto chunk_at = [&](int k) { return k < sn.n_low ? k : sn.lo + k - sn.n_low; };
+  // The table entries of a wave's next 64 chunks lie in its lanes, so that no
+  // chunk's loads wait for a load of their own.
+  Chunk<D> C;
+  const Places<D> W(A.T);
+  const uint32_t block_bytes = (uint32_t)A.T * D / 16 * 17;
+  int k = c0 + wave, ahead = 0, entry = 0;
+  struct Next { const uint8_t* base; uint32_t off; bool dead; };
+  // Where chunk kf lies.  Past the end the last chunk once more: the loads are
+  // always made (from the cache then); with a branch around them the compiler has to
+  // wait for all of them at the first use of any.
+  auto locate = [&](int kf) {
+    if ((ahead & 63) == 0) {
+      entry = tab[chunk_at(min(kf + NWV * lane, c1 - 1)) >> blk_shift];
+      asm volatile("" : "+v"(entry));     // (waited for here, not behind the branch, where it would hold up every step)
+    }
+    Next x;
+    const int blk = __builtin_amdgcn_readlane(entry, ahead & 63);
+    x.dead = (uint32_t)blk >= (uint32_t)A.n_blocks;    // no block: no visible token (block 0 is read in its place)
+    x.off = (chunk_at(min(kf, c1 - 1)) * 32) & (A.T - 1);
+    x.base = A.cache + ((uint64_t)(uint32_t)(x.dead ? 0 : blk) * A.hkv + h) * block_bytes;
+    ahead++;
+    return x;
+  };
+  auto keys = [&](const Next& x) {
+    load_keys<D>(C, W, x.base + x.off * (D / 2), x.base + A.T * D + x.off);
+  };
+  auto values = [&](const Next& x) {
+    load_values<D>(C, W, x.base + A.T * (D / 2) + x.off * (D / 2), x.base + A.T * D + A.T * (D / 32) + x.off);
+  };
+  Next at;
+  at.dead = true;
+  if (k < c1) {
+    at = locate(k);
+    keys(at);
+    values(at);
+  }
   f16x8 q[NT][D / 32];
   float cf[NT];
   int pos[NT];
   int64_t grow[NT];            // row of q and o as (token, head) index, -1 outside
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    const int r = row0 + 16 * nt + n, j = r / A.group, g = r - j * A.group;
-    const bool on = r < rows;
-    grow[nt] = on ? (int64_t)(R.first + j) * A.hq + h * A.group + g : -1;
-    pos[nt] = on ? R.base + j : p1;
-    load_q<D, TYPE>(A, on, (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + G * (D / 4), q[nt], &cf[nt]);
+    // rows past the last compute the last one again and are not written
+    const int r = min(row0 + 16 * nt + n, rows - 1), j = r / A.group, g = r - j * A.group;
+    grow[nt] = row0 + 16 * nt + n < rows ? (int64_t)(R.first + j) * A.hq + h * A.group + g : -1;
+    pos[nt] = R.base + j;
+    load_q<D, TYPE>(A, (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + G * (D / 4), q[nt], &cf[nt]);
   }
-  Acc<D, NT> S;
+  Ref ref[NT];
+  float l[NT];             // this lane group's part of the sum
+  f32x4 o[NT][NC];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    S.m[nt] = NEG_INF;
-    S.l[nt] = 0.0f;
+    ref[nt].init();
+    l[nt] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NC; k++) S.o[nt][k] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < NC; c++) o[nt][c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const int32_t* tab = A.table + (int64_t)i * A.cols;
-  const int per_blk = A.T >> 5;
-  auto chunk_at = [&](int k) { return k < sn.n_low ? k : sn.lo + k - sn.n_low; };
-  Chunk<D> C[2];
-  int k = c0 + wave;
-  if (k < c1) load_chunk<D>(A, C[0], ld_const(tab + chunk_at(k) / per_blk), h, chunk_at(k));
-  auto one = [&](const Chunk<D>& X, int kk) {
-    const int ch = chunk_at(kk), t0 = ch * 32, t1 = t0 + 31;
-    const bool full = !X.dead && t1 <= p0 && (A.window == 0 || t0 > p1 - A.window || t1 < A.sink);
-    if (full) chunk_step<D, NT, false>(A, X, q, cf, pos, ch, S);
-    else chunk_step<D, NT, true>(A, X, q, cf, pos, ch, S);
-  };
+  // One set of registers for the codes: the next chunk's keys are asked for as
+  // soon as this one's are unpacked, its values likewise; the other waves of
+  // the SIMD cover what that does not.
   while (k < c1) {
-    if (k + 4 < c1) load_chunk<D>(A, C[1], ld_const(tab + chunk_at(k + 4) / per_blk), h, chunk_at(k + 4));
-    one(C[0], k);
-    if (k + 4 >= c1) break;
-    if (k + 8 < c1) load_chunk<D>(A, C[0], ld_const(tab + chunk_at(k + 8) / per_blk), h, chunk_at(k + 8));
-    one(C[1], k + 4);
-    k += 8;
+    const int ch = chunk_at(k), t0 = ch * 32, t1 = t0 + 31;
+    const bool dead = at.dead, full = !dead && t1 <= p0 && (A.window == 0 || t0 > p1 - A.window || t1 < A.sink);
+    k += NWV;
+    f32x4 s[NT][2];
+    key_products<D, NT>(C, q, s);
+    at = locate(k);
+    keys(at);
+    f16x8 P[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int t = t0 + 8 * G + e;
+          const bool see = t <= pos[nt] && (A.window == 0 || t > pos[nt] - A.window || t < A.sink) && !dead;
+          s[nt][e >> 2][e & 3] = see ? s[nt][e >> 2][e & 3] : NEG_INF;
+        }
+      }
+      float m = s[nt][0][0];
+#pragma unroll
+      for (int e = 1; e < 8; e++) m = __builtin_fmaxf(m, s[nt][e >> 2][e & 3]);
+      const uint64_t far = __builtin_amdgcn_ballot_w64(m > ref[nt].over);
+      float f = 1.0f;
+      if (far) f = ref[nt].move(__builtin_fmaxf(ref[nt].m, max_quads(m)), cf[nt]);
+      l[nt] *= f;
+      scale_rows<D, NT>(far, f, o, nt);
+      // Weights to binary16 in pairs; the sum takes the same rounded weights, so
+      // that a weight's rounding moves o by its own part only.
+      uint32_t pk[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1)], cf[nt], -ref[nt].mc));
+        const float b2 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1) + 1], cf[nt], -ref[nt].mc));
+        const f16x2 hh = {(f16)a, (f16)b2};
+        pk[e] = h2_bits(hh);
+        l[nt] = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, l[nt], false);
+      }
+      P[nt] = frag(pk[0], pk[1], pk[2], pk[3]);
+    }
+    value_products<D, NT>(C, full, P, o);
+    values(at);
   }
-  // Join the waves: each row's largest product, every wave rescaled to it, then
-  // 2 -> 0 and 3 -> 1, 1 -> 0 (a fixed order).
+  // Join the waves through LDS, each of them a share of the channels: the
+  // waves' sums are rescaled to the row's largest product where they are read.
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    S.l[nt] = sum_quads(S.l[nt]);
-    if (G == 0) { sml[wave][nt][n][0] = S.m[nt]; sml[wave][nt][n][1] = S.l[nt]; }
+    l[nt] = sum_quads(l[nt]);
+    if (G == 0) sml[wave][nt][n] = (f32x2){ref[nt].m, l[nt]};
+#pragma unroll
+    for (int c = 0; c < NC; c++) so[wave][nt * NC + c][lane] = o[nt][c];
   }
   __syncthreads();
-  float M[NT], L[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    M[nt] = NEG_INF;
-#pragma unroll
-    for (int w = 0; w < 4; w++) M[nt] = __builtin_fmaxf(M[nt], sml[w][nt][n][0]);
-    const float mc = M[nt] == NEG_INF ? 0.0f : M[nt] * cf[nt];
-    L[nt] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; w++) L[nt] += sml[w][nt][n][1] * __builtin_amdgcn_exp2f(__builtin_fmaf(sml[w][nt][n][0], cf[nt], -mc));
-    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(S.m[nt], cf[nt], -mc));
-#pragma unroll
-    for (int c = 0; c < NC; c++) S.o[nt][c] *= f;
-  }
-#pragma unroll
-  for (int step = 2; step >= 1; step >>= 1) {
-    if (wave >= step && wave < 2 * step) {
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int c = 0; c < NC; c++) so[wave - step][nt * NC + c][lane] = S.o[nt][c];
-    }
-    __syncthreads();
-    if (wave < step) {
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int c = 0; c < NC; c++) S.o[nt][c] += so[wave][nt * NC + c][lane];
-    }
-    __syncthreads();
-  }
-  if (wave != 0) return;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
     if (grow[nt] < 0) continue;
-    // this lane's channels: (D/16)(4G + i) + c, consecutive
+    f32x2 ml[NWV];
+    float M = NEG_INF;
+#pragma unroll
+    for (int w = 0; w < NWV; w++) {
+      ml[w] = sml[w][nt][n];
+      M = __builtin_fmaxf(M, ml[w][0]);
+    }
+    const float mc = M == NEG_INF ? 0.0f : M * cf[nt];
+    float L = 0.0f, f[NWV];
+#pragma unroll
+    for (int w = 0; w < NWV; w++) {
+      f[w] = __builtin_amdgcn_exp2f(__builtin_fmaf(ml[w][0], cf[nt], -mc));
+      L = __builtin_fmaf(ml[w][1], f[w], L);
+    }
+    // tiles CW * wave ..: channels (D/16)(4G + i) + c
+    constexpr int CW = NC > NWV ? NC / NWV : 1;
+    if (CW * wave >= NC) break;
+    f32x4 x[CW];
+#pragma unroll
+    for (int c = 0; c < CW; c++) {
+      x[c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < NWV; w++) {
+        const f32x4 y = so[w][nt * NC + CW * wave + c][lane];
+#pragma unroll
+        for (int i4 = 0; i4 < 4; i4++) x[c][i4] = __builtin_fmaf(y[i4], f[w], x[c][i4]);
+      }
+    }
+    const int ch0 = NC * 4 * G + CW * wave;
     if (parts <= 1) {
-      const float inv = L[nt] == 0.0f ? 0.0f : 1.0f / L[nt];
-      const int64_t t = grow[nt] / A.hq, hd = grow[nt] - t * A.hq;
-      const int64_t at = t * A.os + hd * D + G * (D / 4);
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      const int64_t t = R.first + (row0 + 16 * nt + n) / A.group;
+      uint16_t* out = (uint16_t*)A.o + t * A.os + (grow[nt] - t * A.hq) * D + ch0;
 #pragma unroll
-      for (int e = 0; e < D / 32; e++) {
-        float x[8];
-#pragma unroll
-        for (int u = 0; u < 8; u++) x[u] = S.o[nt][(8 * e + u) % NC][(8 * e + u) / NC] * inv;
-        store8<TYPE>(A.o, at + 8 * e, x);
+      for (int i4 = 0; i4 < 4; i4++) {
+        if constexpr (CW == 2) *(uint32_t*)(out + NC * i4) = pack2<TYPE>(x[0][i4] * inv, x[1][i4] * inv);
+        else out[NC * i4] = (uint16_t)pack2<TYPE>(x[0][i4] * inv, 0.0f);
       }
     } else {
       const int64_t row = (int64_t)sp * A.n_tok * A.hq + grow[nt];
-      if (G == 0) {
-        A.pml[2 * row] = M[nt] == NEG_INF ? NEG_INF : M[nt] * cf[nt];
-        A.pml[2 * row + 1] = L[nt];
-      }
+      if (G == 0 && wave == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){M == NEG_INF ? NEG_INF : mc, L};
+      float* out = A.po + row * D + ch0;
 #pragma unroll
-      for (int e = 0; e < D / 32; e++) {
-        float x[8];
-#pragma unroll
-        for (int u = 0; u < 8; u++) x[u] = S.o[nt][(8 * e + u) % NC][(8 * e + u) / NC];
-        store8<STQ_FP32>(A.po, row * D + G * (D / 4) + 8 * e, x);
+      for (int i4 = 0; i4 < 4; i4++) {
+        if constexpr (CW == 2) *(f32x2*)(out + NC * i4) = (f32x2){x[0][i4], x[1][i4]};
+        else out[NC * i4] = x[0][i4];
       }
     }
   }
@@ -826,39 +908,38 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   __shared__ u32x4 sk[2][64 * D / 8], sv[2][64 * D / 8];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, G = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // (request, head) pairs fastest, the tiles with the most to see first: a pair's
-  // workgroups share an XCD where the pairs are a multiple of 8
+  // Order of the work: every request's last tile first (it has the most to
+  // see), (request, head) pairs fastest, so that a pair's workgroups share an
+  // XCD where the heads are a multiple of 8.  The requests are rotated from
+  // level to level: workgroups are dealt to the XCDs and their shader engines
+  // in turn and in order, and a ragged batch whose long requests always met the
+  // same engine left the others empty (489 against 342 us for 4 prompts).
   int b = blockIdx.x;
-  const int pairs = A.n_req * A.hkv, pair = b % pairs; b /= pairs;
-  const int sp = b % A.splits, tile = A.tiles - 1 - b / A.splits;
-  const int h = pair % A.hkv, i = pair / A.hkv;
+  const int pair = b % (A.n_req * A.hkv); b /= A.n_req * A.hkv;
+  const int sp = b % A.splits, level = b / A.splits;
+  const int h = pair % A.hkv, i = (pair / A.hkv + (level >> 1)) % A.n_req;
   const Req R = req_args(A, i);
-  const int row0 = tile * ROWS, rows = min(R.n_new, A.max_new) * A.group;
-  if (row0 >= rows) return;
+  const int rows = min(R.n_new, A.max_new) * A.group, row0 = ((rows + ROWS - 1) / ROWS - 1 - level) * ROWS;
+  if (row0 < 0) return;
   const int p0 = R.base + row0 / A.group, p1 = R.base + (min(row0 + ROWS, rows) - 1) / A.group;
   const Span sn = span_of(p0, p1, A.window, A.sink);
-  const int per = split_chunks(sn.total, A.splits);
+  const int per = split_chunks(A, sn.total);
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
   if (c0 >= c1 && sp > 0) return;
   const int parts = (sn.total + per - 1) / per;
 
   // the wave's rows
-  const int r = row0 + 32 * wave + n, j = r / A.group, g = r - j * A.group;
-  const bool on = r < rows;
+  const bool on = row0 + 32 * wave + n < rows;         // rows past the last compute the last one again and are not written
+  const int r = min(row0 + 32 * wave + n, rows - 1), j = r / A.group, g = r - j * A.group;
   const int pw1 = R.base + (min(row0 + 32 * wave + 32, rows) - 1) / A.group;
-  const int pw0 = min(R.base + (row0 + 32 * wave) / A.group, pw1), pos = on ? R.base + j : pw1;
+  const int pw0 = min(R.base + (row0 + 32 * wave) / A.group, pw1), pos = R.base + j;
   f16x8 q[KSTEP];
   float cf;
   {
     float x[D / 2];
     const int64_t at = (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + 8 * G;
 #pragma unroll
-    for (int s = 0; s < KSTEP; s++) {
-      if (on) load8<TYPE>(A.q, at + 16 * s, x + 8 * s);
-      else
-#pragma unroll
-        for (int u = 0; u < 8; u++) x[8 * s + u] = 0.0f;
-    }
+    for (int s = 0; s < KSTEP; s++) load8<TYPE>(A.q, at + 16 * s, x + 8 * s);
     float m = 0.0f;
 #pragma unroll
     for (int u = 0; u < D / 2; u++) m = __builtin_fmaxf(m, __builtin_fabsf(x[u]));
@@ -876,7 +957,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   for (int c = 0; c < NC; c++)
 #pragma unroll
     for (int u = 0; u < 16; u++) o[c][u] = 0.0f;
-  float M = NEG_INF, L = 0.0f;
+  Ref ref;
+  ref.init();
+  float L = 0.0f;
 
   const int32_t* tab = A.table + (int64_t)i * A.cols;
   const int per_blk = A.T >> 5, T = A.T;
@@ -969,17 +1052,15 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
         float m = s[0][0];
 #pragma unroll
         for (int x = 1; x < 32; x++) m = __builtin_fmaxf(m, s[x >> 4][x & 15]);
-        m = __builtin_fmaxf(M, max_halves(m));
-        const float mc = m == NEG_INF ? 0.0f : m * cf;
-        if (__any(m > M)) {
-          const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(M, cf, -mc));
+        if (__any(m > ref.over)) {
+          const float f = ref.move(__builtin_fmaxf(ref.m, max_halves(m)), cf);
           L *= f;
 #pragma unroll
           for (int c = 0; c < NC; c++)
 #pragma unroll
             for (int x = 0; x < 16; x++) o[c][x] *= f;
-          M = m;
         }
+        const float mc = ref.mc;
 #pragma unroll
         for (int u = 0; u < 2; u++) {
 #pragma unroll
@@ -1030,7 +1111,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   } else {
     const int64_t row = (int64_t)sp * A.n_tok * A.hq + (int64_t)(R.first + j) * A.hq + h * A.group + g;
     if (G == 0) {
-      A.pml[2 * row] = M == NEG_INF ? NEG_INF : M * cf;
+      A.pml[2 * row] = ref.m == NEG_INF ? NEG_INF : ref.mc;
       A.pml[2 * row + 1] = L;
     }
     float* out = A.po + row * D + 4 * G;
@@ -1056,21 +1137,33 @@ __global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_rows) 
   const int row0 = (j * A.group + hd % A.group) / tile_rows * tile_rows, rows = min(R.n_new, A.max_new) * A.group;
   const int j1 = (min(row0 + tile_rows, rows) - 1) / A.group;
   const Span sn = span_of(R.base + row0 / A.group, R.base + j1, A.window, A.sink);
-  const int per = split_chunks(sn.total, A.splits), parts = (sn.total + per - 1) / per;
+  const int per = split_chunks(A, sn.total), parts = (sn.total + per - 1) / per;
   if (parts <= 1) return;                              // written by its only part
   const int64_t stride = (int64_t)A.n_tok * A.hq, row = (int64_t)(R.first + j) * A.hq + hd;
-  float M = NEG_INF;
-  for (int s = 0; s < parts; s++) M = __builtin_fmaxf(M, A.pml[2 * (s * stride + row)]);
+  // statistics: part s on lane s (and s + 64)
+  const f32x2 none = {NEG_INF, 0.0f};
+  const f32x2* ml = (const f32x2*)A.pml + row;
+  const f32x2 m0 = lane < parts ? ml[lane * stride] : none, m1 = lane + 64 < parts ? ml[(lane + 64) * stride] : none;
+  float M = wave_max(__builtin_fmaxf(m0[0], m1[0]));
   if (M == NEG_INF) M = 0.0f;
-  float L = 0.0f, x[D / 64];
+  const float f0 = __builtin_amdgcn_exp2f(m0[0] - M), f1 = __builtin_amdgcn_exp2f(m1[0] - M);
+  const float L = wave_sum(__builtin_fmaf(f0, m0[1], f1 * m1[1]));
+  float x[D / 64];
 #pragma unroll
   for (int u = 0; u < D / 64; u++) x[u] = 0.0f;
-  for (int s = 0; s < parts; s++) {
-    const int64_t at = s * stride + row;
-    const float f = __builtin_amdgcn_exp2f(A.pml[2 * at] - M);
-    L = __builtin_fmaf(f, A.pml[2 * at + 1], L);
+  const float* po = A.po + row * D + lane * (D / 64);
+  for (int s = 0; s < parts; s += 8) {                 // eight loads under way at a time (the last ones twice, with weight 0)
+    float y[8][D / 64];
 #pragma unroll
-    for (int u = 0; u < D / 64; u++) x[u] = __builtin_fmaf(f, A.po[at * D + lane * (D / 64) + u], x[u]);
+    for (int e = 0; e < 8; e++)
+#pragma unroll
+      for (int u = 0; u < D / 64; u++) y[e][u] = po[min(s + e, parts - 1) * stride * D + u];
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const float f = s + e < parts ? bits_f(__builtin_amdgcn_readlane(__float_as_uint(s + e < 64 ? f0 : f1), (s + e) & 63)) : 0.0f;
+#pragma unroll
+      for (int u = 0; u < D / 64; u++) x[u] = s + e < parts ? __builtin_fmaf(f, y[e][u], x[u]) : x[u];
+    }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   uint16_t* o = (uint16_t*)A.o + (int64_t)(R.first + j) * A.os + hd * D + lane * (D / 64);
@@ -1104,27 +1197,35 @@ bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
          (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
          a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
 }
-struct Split { int tiles, tile_rows, splits; bool staged; };
+struct Split { int tiles, tile_rows, splits, per; bool staged; };
 // Query rows per key/value head from which the cache is staged through LDS.
 constexpr int STAGED_ROWS = 64;
 constexpr int TILE_WAVES = 4;
-// Workgroups wanted in all: enough for every CU to hold several and for ragged lengths to even out.
-constexpr int64_t WANT_GROUPS = 1536;
+// A part of a request's work has its own start (three dependent loads) and end
+// (the joins), about 5 us.  Few workgroups are split down to 8 chunks until
+// every CU holds three; many only into parts of 48 chunks and up, which even
+// out ragged lengths (64 requests of 2,048 to 8,191 tokens, 8 heads: 83.1 us
+// whole, 78.3 in parts of 48 chunks, 85 in parts of 128, 91 in parts of 24).
+constexpr int64_t FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 3072, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
   const int64_t rows = (int64_t)a->max_new * (a->n_heads / d->n_kv_heads);
   s.staged = rows > STAGED_ROWS;
-  s.tile_rows = s.staged ? 32 * TILE_WAVES : 16;
+  s.tile_rows = s.staged ? 32 * TILE_WAVES : rows > 16 ? 32 : 16;
   s.tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
   const int64_t base = (int64_t)a->n_req * d->n_kv_heads * s.tiles;
   int64_t seen = a->max_len;
   if (a->window > 0) seen = seen < (int64_t)a->window + a->n_sink + 64 ? seen : (int64_t)a->window + a->n_sink + 64;
   const int64_t chunks = (seen + 31) / 32;
-  int64_t k = base > 0 ? WANT_GROUPS / base : 1;
-  const int64_t most = chunks / SPLIT_MIN;
-  if (k > most) k = most;
-  if (k > 64) k = 64;
-  s.splits = k < 1 ? 1 : (int)k;
+  auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  int64_t k = 1;
+  if (base > 0) {
+    const int64_t few = least(FEW_GROUPS / base, chunks / FEW_CHUNKS), many = least(MANY_GROUPS / base, chunks / MANY_CHUNKS);
+    k = least(few > many ? few : many, MOST_SPLITS);
+    if (k < 1) k = 1;
+  }
+  s.per = (int)(((chunks + k - 1) / k + 3) & ~3ll);
+  s.splits = (int)((chunks + s.per - 1) / s.per);
   return s;
 }
 
@@ -1132,7 +1233,8 @@ template <int D, int TYPE>
 void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
   if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE, TILE_WAVES>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
-  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1>), dim3(grid), dim3(256), 0, st, A);
+  else if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2>), dim3(grid), dim3(64 * ROW_WAVES), 0, st, A);
+  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1>), dim3(grid), dim3(64 * ROW_WAVES), 0, st, A);
   if (A.splits > 1) {
     const int64_t rows = (int64_t)A.n_req * A.max_new * A.hq;
     hipLaunchKernelGGL((k_attend_join<D, TYPE>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, A, s.tile_rows);
@@ -1289,7 +1391,7 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.q = q; A.o = o;
   A.n_req = a->n_req; A.n_tok = a->n_tok; A.hq = a->n_heads; A.hkv = d->n_kv_heads; A.group = a->n_heads / d->n_kv_heads;
   A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = a->table_cols; A.max_new = a->max_new; A.window = a->window;
-  A.sink = a->n_sink; A.splits = sp.splits; A.tiles = sp.tiles; A.qs = a->q_stride; A.os = a->o_stride;
+  A.sink = a->n_sink; A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles; A.qs = a->q_stride; A.os = a->o_stride;
   A.scale_log2 = a->scale * 1.44269504088896340736f;
   A.po = (float*)work;
   A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
