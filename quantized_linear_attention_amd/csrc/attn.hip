@@ -899,13 +899,17 @@ __device__ __forceinline__ float max_halves(float x) {
   return __builtin_fmaxf(bits_f(a[0]), bits_f(a[1]));
 }
 
+template <int I>
+struct Const { static constexpr int value = I; };
+
 template <int D, int TYPE, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   constexpr int NT = 64 * NW, ROWS = 32 * NW;
   constexpr int KP = 2 * D;                            // 16-byte pieces of a tile's key codes (32 channels of a token)
   constexpr int NP = (2 * KP + NT - 1) / NT;           // pieces of keys and values per thread
   constexpr int KSTEP = D / 16, NC = D / 32;
-  __shared__ u32x4 sk[2][64 * D / 8], sv[2][64 * D / 8];
+  constexpr int TILE = 2 * 64 * D * 2;                 // bytes of a tile's keys, then its values
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * TILE];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, G = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Order of the work: every request's last tile first (it has the most to
@@ -962,135 +966,163 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   float L = 0.0f;
 
   const int32_t* tab = A.table + (int64_t)i * A.cols;
-  const int per_blk = A.T >> 5, T = A.T;
+  const int T = A.T, blk_shift = 31 - __builtin_clz(T) - 5;
   auto chunk_at = [&](int k) { return k < sn.n_low ? k : sn.lo + k - sn.n_low; };
+  // This thread's pieces of a tile: whether of the keys or the values and of
+  // which chunk is the same over a wave.  Keys: the pieces of a token side by
+  // side; values: tokens side by side (what the slots' rotations want).
+  bool isv[NP], mine[NP];
+  int part[NP];
+  uint32_t code_at[NP], scale_at[NP], slot[NP][4];
+#pragma unroll
+  for (int s = 0; s < NP; s++) {
+    const int p = 64 * wave + s * NT;
+    mine[s] = p < 2 * KP;
+    isv[s] = p >= KP;
+    const int pp = isv[s] ? p - KP : p;
+    part[s] = pp / D;
+    const int w = pp % D + lane;
+    const int t = isv[s] ? w & 31 : w / (D / 32), c = isv[s] ? w >> 5 : w % (D / 32);
+    code_at[s] = (isv[s] ? T * (D / 2) : 0) + t * (D / 2) + 16 * c;
+    scale_at[s] = T * D + (isv[s] ? T * (D / 32) : 0) + c * T + t;
+#pragma unroll
+    for (int x = 0; x < 4; x++)
+      slot[s][x] = 16 * (isv[s] ? 64 * D / 8 + v_slot<D>(32 * part[s] + t, 4 * c + x) : k_slot<D>(32 * part[s] + t, 4 * c + x));
+  }
   u32x4 raw[NP];
   uint32_t sb[NP];
-  // this thread's pieces of chunks k, k + 1
+  const uint32_t block_bytes = (uint32_t)T * D / 16 * 17;
+  int ahead = 0, entry = 0;
+  // Asks for this thread's pieces of chunks k, k + 1; returns which of the two
+  // hold no visible token because they lie past the end or in no block.
   auto fetch = [&](int k) {
+    if ((ahead & 63) == 0) {
+      entry = tab[chunk_at(min(k + lane, c1 - 1)) >> blk_shift];
+      asm volatile("" : "+v"(entry));
+    }
+    const uint32_t e[2] = {(uint32_t)__builtin_amdgcn_readlane(entry, ahead & 63),
+                           (uint32_t)__builtin_amdgcn_readlane(entry, (ahead & 63) + 1)};
+    ahead += 2;
 #pragma unroll
     for (int s = 0; s < NP; s++) {
-      const int p = tid + s * NT;
-      if (2 * KP % NT && p >= 2 * KP) break;
-      const bool isv = p >= KP;
-      const int pp = isv ? p - KP : p;
-      const int u = pp / D, w = pp % D;                  // chunk, piece of it: D pieces
-      // keys: pieces of a token side by side; values: tokens side by side (the bank layouts of the writes)
-      const int t = isv ? w & 31 : w / (D / 32), c = isv ? w >> 5 : w % (D / 32);
-      const int ch = chunk_at(min(k + u, c1 - 1));
-      int blk = ld_const(tab + ch / per_blk);
-      blk = (uint32_t)blk < (uint32_t)A.n_blocks ? blk : 0;
-      const int off = ((ch * 32) & (T - 1)) + t;
-      const uint8_t* hb = A.cache + ((int64_t)blk * A.hkv + h) * (T * D / 16 * 17);
-      raw[s] = *(const u32x4*)(hb + (isv ? T * (D / 2) : 0) + off * (D / 2) + 16 * c);
-      sb[s] = hb[T * D + (isv ? T * (D / 32) : 0) + c * T + off];
+      if (!mine[s]) break;
+      const int u = part[s];
+      uint32_t blk = u ? e[1] : e[0];
+      blk = blk < (uint32_t)A.n_blocks ? blk : 0;
+      const uint32_t off = (chunk_at(min(k + u, c1 - 1)) * 32) & (T - 1);
+      const uint8_t* hb = A.cache + ((uint64_t)blk * A.hkv + h) * block_bytes;
+      raw[s] = *(const u32x4*)(hb + off * (D / 2) + code_at[s]);
+      sb[s] = (hb + off)[scale_at[s]];
     }
+    return (e[0] >= (uint32_t)A.n_blocks || k >= c1 ? 1 : 0) | (e[1] >= (uint32_t)A.n_blocks || k + 1 >= c1 ? 2 : 0);
   };
+  // Unpacks them into buffer `buf`.
   auto put = [&](int buf) {
 #pragma unroll
     for (int s = 0; s < NP; s++) {
-      const int p = tid + s * NT;
-      if (2 * KP % NT && p >= 2 * KP) break;
-      const bool isv = p >= KP;
-      const int pp = isv ? p - KP : p;
-      const int u = pp / D, w = pp % D;
-      const int t = 32 * u + (isv ? w & 31 : w / (D / 32)), c = 4 * (isv ? w >> 5 : w % (D / 32));
+      if (!mine[s]) break;
       // values: unwritten bytes behind the last token must not be NaN or infinite, their weights are 0
-      const float sc = scale_of<0>(isv ? min(sb[s], (uint32_t)(E_MAX + 127)) : sb[s]);
+      const float sc = scale_of<0>(isv[s] ? min(sb[s], (uint32_t)(E_MAX + 127)) : sb[s]);
 #pragma unroll
       for (int x = 0; x < 4; x++) {
         const uint32_t d = raw[s][x];
-        const u32x4 v = {cvt2<0>(d, sc), cvt2<1>(d, sc), cvt2<2>(d, sc), cvt2<3>(d, sc)};
-        if (isv) sv[buf][v_slot<D>(t, c + x)] = v;
-        else sk[buf][k_slot<D>(t, c + x)] = v;
+        *(u32x4*)(lds + buf * TILE + slot[s][x]) = (u32x4){cvt2<0>(d, sc), cvt2<1>(d, sc), cvt2<2>(d, sc), cvt2<3>(d, sc)};
       }
     }
   };
-  auto block_of = [&](int k) { return ld_const(tab + chunk_at(k) / per_blk); };
-  // rows that see all of chunk k
-  auto whole = [&](int k) {
-    if (k >= c1 || (uint32_t)block_of(k) >= (uint32_t)A.n_blocks) return false;
-    const int t0 = chunk_at(k) * 32, t1 = t0 + 31;
-    return t1 <= pw0 && (A.window == 0 || t0 > pw1 - A.window || t1 < A.sink);
+  // Where this lane reads: keys (token n, channels 16x + 8G ..), values (tokens
+  // 4G + .. and 8 more, channels 32c ..); other tokens of the tile lie whole rows on.
+  uint32_t kat[KSTEP], vat[NC][2];
+#pragma unroll
+  for (int x = 0; x < KSTEP; x++) kat[x] = 16 * k_slot<D>(n, 2 * x + G);
+#pragma unroll
+  for (int c = 0; c < NC; c++)
+#pragma unroll
+    for (int y = 0; y < 2; y++) {
+      const int ch = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);      // four channels of one token
+      vat[c][y] = 64 * D * 2 + 16 * v_slot<D>(8 * y + 4 * G + ((lane >> 2) & 3), ch >> 3) + 8 * ((ch >> 2) & 1);
+    }
+  auto work = [&](int k, int gone, auto buf_) {
+    constexpr int buf = decltype(buf_)::value;
+    const int ta = chunk_at(k) * 32, tb = chunk_at(min(k + 1, c1 - 1)) * 32;
+    if (ta > pw1) return;                               // every token lies behind the wave's rows
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+#pragma unroll
+      for (int x = 0; x < 16; x++) s[u][x] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < KSTEP; x++) {
+        const f16x8 kf = *(const f16x8*)(lds + buf * TILE + u * 32 * D * 2 + kat[x]);
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[x], s[u], 0, 0, 0);
+      }
+    }
+    const bool in_a = A.window == 0 || ta > pw1 - A.window || ta + 31 < A.sink;
+    const bool in_b = A.window == 0 || tb > pw1 - A.window || tb + 31 < A.sink;
+    if (gone || tb + 31 > pw0 || !in_a || !in_b) {
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const int t0 = (u ? tb : ta) + 4 * G;
+#pragma unroll
+        for (int x = 0; x < 16; x++) {
+          const int t = t0 + 8 * (x >> 2) + (x & 3);
+          const bool see = t <= pos && (A.window == 0 || t > pos - A.window || t < A.sink) && !(gone & (1 << u));
+          s[u][x] = see ? s[u][x] : NEG_INF;
+        }
+      }
+    }
+    float m = s[0][0];
+#pragma unroll
+    for (int x = 1; x < 32; x++) m = __builtin_fmaxf(m, s[x >> 4][x & 15]);
+    const uint64_t far = __builtin_amdgcn_ballot_w64(m > ref.over);
+    float f = 1.0f;
+    if (far) f = ref.move(__builtin_fmaxf(ref.m, max_halves(m)), cf);
+    L *= f;
+    if constexpr (NC == 4)
+      SCALE_WHERE(far, f, 192, 64, AT(192:207)(o[0]), AT(208:223)(o[1]), AT(224:239)(o[2]), AT(240:255)(o[3]));
+    else
+      SCALE_WHERE(far, f, 128, 32, AT(128:143)(o[0]), AT(144:159)(o[1]));
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int y = 0; y < 2; y++) {                     // 16 tokens
+        uint32_t pk[4];
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x], cf, -ref.mc));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x + 1], cf, -ref.mc));
+          const f16x2 hh = {(f16)e0, (f16)e1};
+          pk[x] = h2_bits(hh);
+          L = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, L, false);
+        }
+        const f16x8 P = frag(pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+          const uint32_t at = buf * TILE + (32 * u + 16 * y) * D * 2;
+          const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(lds + at + vat[c][0])));
+          const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(lds + at + vat[c][1])));
+          o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(lo[0], lo[1], hi[0], hi[1]), P, o[c], 0, 0, 0);
+        }
+      }
   };
   if (c0 < c1) {
-    fetch(c0);
+    // gone: of the tile at work, of the one in registers, of the one under way
+    int g0 = fetch(c0), g1 = 0;
     put(0);
-    if (c0 + 2 < c1) fetch(c0 + 2);
+    g1 = fetch(c0 + 2);
     __syncthreads();
-    int buf = 0;
-    for (int k = c0; k < c1; k += 2, buf ^= 1) {
-      if (k + 2 < c1) {
-        put(buf ^ 1);
-        if (k + 4 < c1) fetch(k + 4);
-      }
-      if (chunk_at(k) * 32 <= pw1) {                    // else every token lies behind the wave's rows
-        f32x16 s[2];
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-#pragma unroll
-          for (int x = 0; x < 16; x++) s[u][x] = 0.0f;
-#pragma unroll
-          for (int x = 0; x < KSTEP; x++) {
-            const f16x8 kf = __builtin_bit_cast(f16x8, sk[buf][k_slot<D>(32 * u + n, 2 * x + G)]);
-            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[x], s[u], 0, 0, 0);
-          }
-        }
-        if (!(whole(k) && whole(k + 1))) {
-#pragma unroll
-          for (int u = 0; u < 2; u++) {
-            const bool there = k + u < c1 && (uint32_t)block_of(min(k + u, c1 - 1)) < (uint32_t)A.n_blocks;
-            const int t0 = chunk_at(min(k + u, c1 - 1)) * 32 + 4 * G;
-#pragma unroll
-            for (int x = 0; x < 16; x++) {
-              const int t = t0 + 8 * (x >> 2) + (x & 3);
-              const bool see = t <= pos && (A.window == 0 || t > pos - A.window || t < A.sink) && there;
-              s[u][x] = see ? s[u][x] : NEG_INF;
-            }
-          }
-        }
-        float m = s[0][0];
-#pragma unroll
-        for (int x = 1; x < 32; x++) m = __builtin_fmaxf(m, s[x >> 4][x & 15]);
-        if (__any(m > ref.over)) {
-          const float f = ref.move(__builtin_fmaxf(ref.m, max_halves(m)), cf);
-          L *= f;
-#pragma unroll
-          for (int c = 0; c < NC; c++)
-#pragma unroll
-            for (int x = 0; x < 16; x++) o[c][x] *= f;
-        }
-        const float mc = ref.mc;
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-#pragma unroll
-          for (int y = 0; y < 2; y++) {                 // 16 tokens
-            uint32_t pk[4];
-#pragma unroll
-            for (int x = 0; x < 4; x++) {
-              const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x], cf, -mc));
-              const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x + 1], cf, -mc));
-              const f16x2 hh = {(f16)e0, (f16)e1};
-              pk[x] = h2_bits(hh);
-              L = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, L, false);
-            }
-            const f16x8 P = frag(pk[0], pk[1], pk[2], pk[3]);
-#pragma unroll
-            for (int c = 0; c < NC; c++) {
-              const int t = 32 * u + 16 * y + 4 * G + ((lane >> 2) & 3);
-              const int cb = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);   // channels cb .. cb + 3
-              u32x4* base = sv[buf];
-              const fp16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
-                  (lds_fp16x4*)((uint8_t*)(base + v_slot<D>(t, cb >> 3)) + 8 * ((cb >> 2) & 1)));
-              const fp16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
-                  (lds_fp16x4*)((uint8_t*)(base + v_slot<D>(t + 8, cb >> 3)) + 8 * ((cb >> 2) & 1)));
-              const u32x2 a = __builtin_bit_cast(u32x2, lo), d = __builtin_bit_cast(u32x2, hi);
-              o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(a[0], a[1], d[0], d[1]), P, o[c], 0, 0, 0);
-            }
-          }
-        }
-      }
+    for (int k = c0; k < c1; k += 4) {
+      if (k + 2 < c1) put(1);
+      const int g2 = fetch(k + 4);
+      work(k, g0, Const<0>());
       __syncthreads();
+      if (k + 2 >= c1) break;
+      if (k + 4 < c1) put(0);
+      const int g3 = fetch(k + 6);
+      work(k + 2, g1, Const<1>());
+      __syncthreads();
+      g0 = g2;
+      g1 = g3;
     }
   }
   {
