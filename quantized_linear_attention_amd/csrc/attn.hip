@@ -768,10 +768,11 @@ __global__ void __launch_bounds__(64 * ROW_WAVES, 2) k_attend_rows(AttnArgs A) {
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
       if (!full) {
+        const int low = A.window == 0 ? -1 : pos[nt] - A.window, last = dead ? -1 : pos[nt];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           const int t = t0 + 8 * G + e;
-          const bool see = t <= pos[nt] && (A.window == 0 || t > pos[nt] - A.window || t < A.sink) && !dead;
+          const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < A.sink));
           s[nt][e >> 2][e & 3] = see ? s[nt][e >> 2][e & 3] : NEG_INF;
         }
       }
@@ -881,17 +882,19 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __fp16 fp16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) fp16x4 lds_fp16x4;
 
-// 16-byte slot of (token t of 64, channels 8c ..): rows rotated so that the 16
-// lanes of a read or write phase touch 16 different slots of the banks.
+// 16-byte slot of (token t of 64, channels 8c ..).  The channel part is xored
+// with bits of the token so that the 16 lanes of a read or write phase touch
+// 16 different slots of the banks; as xors the places of a lane's other
+// channels are its first place with constant bits turned.
 template <int D>
 __device__ __forceinline__ int k_slot(int t, int c) {
-  if constexpr (D == 128) return t * 16 + ((c + t) & 15);
-  else return t * 8 + ((c + (t >> 1)) & 7);
+  if constexpr (D == 128) return t * 16 + (c ^ (t & 15));
+  else return t * 8 + (c ^ ((t >> 1) & 7));
 }
 template <int D>
 __device__ __forceinline__ int v_slot(int t, int c) {
-  if constexpr (D == 128) return t * 16 + ((c + 4 * (t & 3) + ((t >> 2) & 3)) & 15);
-  else return t * 8 + ((c + 4 * ((t >> 1) & 1) + ((t >> 2) & 3)) & 7);
+  if constexpr (D == 128) return t * 16 + (c ^ (4 * (t & 3) + ((t >> 2) & 3)));
+  else return t * 8 + (c ^ (4 * ((t >> 1) & 1) + ((t >> 2) & 3)));
 }
 
 __device__ __forceinline__ float max_halves(float x) {
@@ -899,17 +902,18 @@ __device__ __forceinline__ float max_halves(float x) {
   return __builtin_fmaxf(bits_f(a[0]), bits_f(a[1]));
 }
 
-template <int I>
-struct Const { static constexpr int value = I; };
-
+#ifndef SCHED
+#define SGB(m, n) __builtin_amdgcn_sched_group_barrier(m, n, 0);
+#define PH1 SGB(8, 1) SGB(0x100, 1) SGB(2, 6)
+#define PH2 SGB(0x100, 2) SGB(8, 1) SGB(2, 3) SGB(0x100, 2) SGB(8, 1) SGB(2, 3) SGB(0x200, 1)
+#define SCHED SGB(0x100, 4) PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH2 PH2 PH2 PH2 PH2 PH2 PH2 PH2
+#endif
 template <int D, int TYPE, int NW>
 __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   constexpr int NT = 64 * NW, ROWS = 32 * NW;
   constexpr int KP = 2 * D;                            // 16-byte pieces of a tile's key codes (32 channels of a token)
-  constexpr int NP = (2 * KP + NT - 1) / NT;           // pieces of keys and values per thread
   constexpr int KSTEP = D / 16, NC = D / 32;
-  constexpr int TILE = 2 * 64 * D * 2;                 // bytes of a tile's keys, then its values
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * TILE];
+  __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][64 * D * 2], lds_v[2][64 * D * 2];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, G = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Order of the work: every request's last tile first (it has the most to
@@ -968,112 +972,103 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   const int32_t* tab = A.table + (int64_t)i * A.cols;
   const int T = A.T, blk_shift = 31 - __builtin_clz(T) - 5;
   auto chunk_at = [&](int k) { return k < sn.n_low ? k : sn.lo + k - sn.n_low; };
-  // This thread's pieces of a tile: whether of the keys or the values and of
-  // which chunk is the same over a wave.  Keys: the pieces of a token side by
-  // side; values: tokens side by side (what the slots' rotations want).
-  bool isv[NP], mine[NP];
-  int part[NP];
-  uint32_t code_at[NP], scale_at[NP], slot[NP][4];
-#pragma unroll
-  for (int s = 0; s < NP; s++) {
-    const int p = 64 * wave + s * NT;
-    mine[s] = p < 2 * KP;
-    isv[s] = p >= KP;
-    const int pp = isv[s] ? p - KP : p;
-    part[s] = pp / D;
-    const int w = pp % D + lane;
-    const int t = isv[s] ? w & 31 : w / (D / 32), c = isv[s] ? w >> 5 : w % (D / 32);
-    code_at[s] = (isv[s] ? T * (D / 2) : 0) + t * (D / 2) + 16 * c;
-    scale_at[s] = T * D + (isv[s] ? T * (D / 32) : 0) + c * T + t;
-#pragma unroll
-    for (int x = 0; x < 4; x++)
-      slot[s][x] = 16 * (isv[s] ? 64 * D / 8 + v_slot<D>(32 * part[s] + t, 4 * c + x) : k_slot<D>(32 * part[s] + t, 4 * c + x));
-  }
-  u32x4 raw[NP];
-  uint32_t sb[NP];
+  // This thread's piece of a tile's keys and of its values: a quarter of a
+  // token's codes; waves 0 and 1 chunk k's, 2 and 3 chunk k + 1's.  Keys: the
+  // pieces of a token side by side; values: tokens side by side (what the
+  // slots' xors want).
+  static_assert(NT == 256, "a piece of the keys and one of the values per thread");
+  constexpr int PS = D / 32;                           // dwords, and slots, of a piece
+  const int half = wave >> 1, w128 = tid & 127;
+  const int tk = w128 >> 2, ck = w128 & 3, tv = w128 & 31, cv = w128 >> 5;
+  const uint32_t kc_at = tk * (D / 2) + 4 * PS * ck, ks_at = T * D + (PS * ck / 4) * T + tk;
+  const uint32_t vc_at = T * (D / 2) + tv * (D / 2) + 4 * PS * cv, vs_at = T * D + T * (D / 32) + (PS * cv / 4) * T + tv;
+  const uint32_t k_put = 16 * k_slot<D>(32 * half + tk, PS * ck), v_put = 16 * v_slot<D>(32 * half + tv, PS * cv);
   const uint32_t block_bytes = (uint32_t)T * D / 16 * 17;
   int ahead = 0, entry = 0;
-  // Asks for this thread's pieces of chunks k, k + 1; returns which of the two
-  // hold no visible token because they lie past the end or in no block.
-  auto fetch = [&](int k) {
+  // A tile: chunks k, k + 1; gone: which of them hold no visible token because
+  // they lie past the end or in no block.
+  struct Tile { int k; uint32_t blk[2]; int gone; };
+  auto locate = [&](int k) {
     if ((ahead & 63) == 0) {
       entry = tab[chunk_at(min(k + lane, c1 - 1)) >> blk_shift];
       asm volatile("" : "+v"(entry));
     }
-    const uint32_t e[2] = {(uint32_t)__builtin_amdgcn_readlane(entry, ahead & 63),
-                           (uint32_t)__builtin_amdgcn_readlane(entry, (ahead & 63) + 1)};
+    const uint32_t e0 = __builtin_amdgcn_readlane(entry, ahead & 63), e1 = __builtin_amdgcn_readlane(entry, (ahead & 63) + 1);
     ahead += 2;
-#pragma unroll
-    for (int s = 0; s < NP; s++) {
-      if (!mine[s]) break;
-      const int u = part[s];
-      uint32_t blk = u ? e[1] : e[0];
-      blk = blk < (uint32_t)A.n_blocks ? blk : 0;
-      const uint32_t off = (chunk_at(min(k + u, c1 - 1)) * 32) & (T - 1);
-      const uint8_t* hb = A.cache + ((uint64_t)blk * A.hkv + h) * block_bytes;
-      raw[s] = *(const u32x4*)(hb + off * (D / 2) + code_at[s]);
-      sb[s] = (hb + off)[scale_at[s]];
-    }
-    return (e[0] >= (uint32_t)A.n_blocks || k >= c1 ? 1 : 0) | (e[1] >= (uint32_t)A.n_blocks || k + 1 >= c1 ? 2 : 0);
+    Tile x;
+    x.k = k;
+    x.gone = (e0 >= (uint32_t)A.n_blocks || k >= c1 ? 1 : 0) | (e1 >= (uint32_t)A.n_blocks || k + 1 >= c1 ? 2 : 0);
+    x.blk[0] = e0 < (uint32_t)A.n_blocks ? e0 : 0;
+    x.blk[1] = e1 < (uint32_t)A.n_blocks ? e1 : 0;
+    return x;
   };
-  // Unpacks them into buffer `buf`.
-  auto put = [&](int buf) {
-#pragma unroll
-    for (int s = 0; s < NP; s++) {
-      if (!mine[s]) break;
-      // values: unwritten bytes behind the last token must not be NaN or infinite, their weights are 0
-      const float sc = scale_of<0>(isv[s] ? min(sb[s], (uint32_t)(E_MAX + 127)) : sb[s]);
-#pragma unroll
-      for (int x = 0; x < 4; x++) {
-        const uint32_t d = raw[s][x];
-        *(u32x4*)(lds + buf * TILE + slot[s][x]) = (u32x4){cvt2<0>(d, sc), cvt2<1>(d, sc), cvt2<2>(d, sc), cvt2<3>(d, sc)};
-      }
-    }
+  typedef uint32_t piece_t __attribute__((ext_vector_type(PS)));
+  piece_t kraw, vraw;
+  uint32_t ksb, vsb;
+  auto base_of = [&](const Tile& x) {                  // this wave's chunk: its head's bytes from the chunk's first token slot on
+    const uint32_t off = (chunk_at(min(x.k + half, c1 - 1)) * 32) & (T - 1);
+    return A.cache + ((uint64_t)(half ? x.blk[1] : x.blk[0]) * A.hkv + h) * block_bytes + off;
   };
-  // Where this lane reads: keys (token n, channels 16x + 8G ..), values (tokens
-  // 4G + .. and 8 more, channels 32c ..); other tokens of the tile lie whole rows on.
-  uint32_t kat[KSTEP], vat[NC][2];
+  auto off_of = [&](const Tile& x) { return (uint32_t)((chunk_at(min(x.k + half, c1 - 1)) * 32) & (T - 1)) * (D / 2 - 1); };
+  auto fetch_k = [&](const Tile& x) {
+    const uint8_t* p = base_of(x);
+    kraw = *(const piece_t*)(p + off_of(x) + kc_at);
+    ksb = p[ks_at];
+  };
+  auto fetch_v = [&](const Tile& x) {
+    const uint8_t* p = base_of(x);
+    vraw = *(const piece_t*)(p + off_of(x) + vc_at);
+    vsb = p[vs_at];
+  };
+  auto put = [&](uint8_t* buf, uint32_t at, const piece_t& raw, float sc) {
 #pragma unroll
-  for (int x = 0; x < KSTEP; x++) kat[x] = 16 * k_slot<D>(n, 2 * x + G);
-#pragma unroll
-  for (int c = 0; c < NC; c++)
-#pragma unroll
-    for (int y = 0; y < 2; y++) {
-      const int ch = 32 * c + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);      // four channels of one token
-      vat[c][y] = 64 * D * 2 + 16 * v_slot<D>(8 * y + 4 * G + ((lane >> 2) & 3), ch >> 3) + 8 * ((ch >> 2) & 1);
-    }
-  auto work = [&](int k, int gone, auto buf_) {
-    constexpr int buf = decltype(buf_)::value;
-    const int ta = chunk_at(k) * 32, tb = chunk_at(min(k + 1, c1 - 1)) * 32;
-    if (ta > pw1) return;                               // every token lies behind the wave's rows
-    f32x16 s[2];
+    for (int x = 0; x < PS; x++)
+      *(u32x4*)(buf + (at ^ (16 * x))) = (u32x4){cvt2<0>(raw[x], sc), cvt2<1>(raw[x], sc), cvt2<2>(raw[x], sc), cvt2<3>(raw[x], sc)};
+  };
+  auto put_k = [&](int b) { put(lds_k[b], k_put, kraw, scale_of<0>(ksb)); };
+  // (unwritten bytes behind the last token must not be NaN or infinite, their weights are 0)
+  auto put_v = [&](int b) { put(lds_v[b], v_put, vraw, scale_of<0>(min(vsb, (uint32_t)(E_MAX + 127)))); };
+  // Where this lane reads: keys (token n, channels 8G .., and 16x more), values
+  // (tokens 4G + .. and 8 more; four channels, and 32c more); other tokens of
+  // the tile lie whole rows on.
+  const uint32_t k_at = 16 * k_slot<D>(n, G);
+  const int vt = 4 * G + ((lane >> 2) & 3), vch = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const uint32_t v_at[2] = {16u * v_slot<D>(vt, vch >> 3) + 8 * ((vch >> 2) & 1), 16u * v_slot<D>(vt + 8, vch >> 3) + 8 * ((vch >> 2) & 1)};
+  auto key_tile = [&](const uint8_t* buf, f32x16* s) {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
 #pragma unroll
       for (int x = 0; x < 16; x++) s[u][x] = 0.0f;
 #pragma unroll
       for (int x = 0; x < KSTEP; x++) {
-        const f16x8 kf = *(const f16x8*)(lds + buf * TILE + u * 32 * D * 2 + kat[x]);
+        const f16x8 kf = *(const f16x8*)(buf + u * 32 * D * 2 + (k_at ^ (32 * x)));
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[x], s[u], 0, 0, 0);
       }
     }
+  };
+  // One tile: its products s become weights and meet its values, while the
+  // matrix cores make the next tile's products sn (nothing of one waits for the
+  // other, so the compiler interleaves them).
+  auto work = [&](const Tile& x, f32x16* s, f32x16* sn, const uint8_t* next_k, const uint8_t* v, auto&& stage) {
+    const int ta = chunk_at(x.k) * 32, tb = chunk_at(min(x.k + 1, c1 - 1)) * 32;
     const bool in_a = A.window == 0 || ta > pw1 - A.window || ta + 31 < A.sink;
     const bool in_b = A.window == 0 || tb > pw1 - A.window || tb + 31 < A.sink;
-    if (gone || tb + 31 > pw0 || !in_a || !in_b) {
+    if (x.gone || tb + 31 > pw0 || !in_a || !in_b) {
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        const int t0 = (u ? tb : ta) + 4 * G;
+        const int t0 = (u ? tb : ta) + 4 * G, low = A.window == 0 ? -1 : pos - A.window;
+        const int last = x.gone & (1 << u) ? -1 : pos;
 #pragma unroll
-        for (int x = 0; x < 16; x++) {
-          const int t = t0 + 8 * (x >> 2) + (x & 3);
-          const bool see = t <= pos && (A.window == 0 || t > pos - A.window || t < A.sink) && !(gone & (1 << u));
-          s[u][x] = see ? s[u][x] : NEG_INF;
+        for (int e = 0; e < 16; e++) {
+          const int t = t0 + 8 * (e >> 2) + (e & 3);
+          const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < A.sink));
+          s[u][e] = see ? s[u][e] : NEG_INF;
         }
       }
     }
     float m = s[0][0];
 #pragma unroll
-    for (int x = 1; x < 32; x++) m = __builtin_fmaxf(m, s[x >> 4][x & 15]);
+    for (int e = 1; e < 32; e++) m = __builtin_fmaxf(m, s[e >> 4][e & 15]);
     const uint64_t far = __builtin_amdgcn_ballot_w64(m > ref.over);
     float f = 1.0f;
     if (far) f = ref.move(__builtin_fmaxf(ref.m, max_halves(m)), cf);
@@ -1082,47 +1077,69 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
       SCALE_WHERE(far, f, 192, 64, AT(192:207)(o[0]), AT(208:223)(o[1]), AT(224:239)(o[2]), AT(240:255)(o[3]));
     else
       SCALE_WHERE(far, f, 128, 32, AT(128:143)(o[0]), AT(144:159)(o[1]));
+    key_tile(next_k, sn);
+    stage();
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
       for (int y = 0; y < 2; y++) {                     // 16 tokens
         uint32_t pk[4];
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x], cf, -ref.mc));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * x + 1], cf, -ref.mc));
+        for (int e = 0; e < 4; e++) {
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e], cf, -ref.mc));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e + 1], cf, -ref.mc));
           const f16x2 hh = {(f16)e0, (f16)e1};
-          pk[x] = h2_bits(hh);
+          pk[e] = h2_bits(hh);
           L = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, L, false);
         }
         const f16x8 P = frag(pk[0], pk[1], pk[2], pk[3]);
 #pragma unroll
         for (int c = 0; c < NC; c++) {
-          const uint32_t at = buf * TILE + (32 * u + 16 * y) * D * 2;
-          const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(lds + at + vat[c][0])));
-          const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(lds + at + vat[c][1])));
+          const uint8_t* at = v + (32 * u + 16 * y) * D * 2;
+          const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(at + (v_at[0] ^ (64 * c)))));
+          const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(at + (v_at[1] ^ (64 * c)))));
           o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(lo[0], lo[1], hi[0], hi[1]), P, o[c], 0, 0, 0);
         }
       }
+    SCHED
   };
   if (c0 < c1) {
-    // gone: of the tile at work, of the one in registers, of the one under way
-    int g0 = fetch(c0), g1 = 0;
-    put(0);
-    g1 = fetch(c0 + 2);
+    Tile t0 = locate(c0), t1 = locate(c0 + 2), t2 = locate(c0 + 4);
+    fetch_k(t0);
+    fetch_v(t0);
+    put_k(0);
+    put_v(0);
+    fetch_k(t1);
+    fetch_v(t1);
+    put_k(1);
+    fetch_k(t2);
     __syncthreads();
+    f32x16 sa[2], sb[2];
+    key_tile(lds_k[0], sa);
+    __syncthreads();
+    // in LDS: the values of tile t0, the keys of t1; in registers: the values of
+    // t1, the keys of t2
     for (int k = c0; k < c1; k += 4) {
-      if (k + 2 < c1) put(1);
-      const int g2 = fetch(k + 4);
-      work(k, g0, Const<0>());
+      const Tile t3 = locate(k + 6);
+      work(t0, sa, sb, lds_k[1], lds_v[0], [&] {
+        put_v(1);
+        put_k(0);
+        fetch_v(t2);
+        fetch_k(t3);
+      });
       __syncthreads();
       if (k + 2 >= c1) break;
-      if (k + 4 < c1) put(0);
-      const int g3 = fetch(k + 6);
-      work(k + 2, g1, Const<1>());
+      const Tile t4 = locate(k + 8);
+      work(t1, sb, sa, lds_k[0], lds_v[1], [&] {
+        put_v(0);
+        put_k(1);
+        fetch_v(t3);
+        fetch_k(t4);
+      });
       __syncthreads();
-      g0 = g2;
-      g1 = g3;
+      t0 = t2;
+      t1 = t3;
+      t2 = t4;
     }
   }
   {
