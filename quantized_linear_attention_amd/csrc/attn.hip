@@ -443,6 +443,14 @@ __device__ __forceinline__ float sum_quads(float x) {
   return bits_f(b[0]) + bits_f(b[1]);
 }
 
+__device__ __forceinline__ int wave_max_i(int x) {
+  x = max(x, dppi<0xB1>(x));
+  x = max(x, dppi<0x4E>(x));
+  x = max(x, dppi<0x141>(x));
+  x = max(x, dppi<0x140>(x));
+  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
 __device__ __forceinline__ float wave_max(float x) {
   x = __builtin_fmaxf(x, dpp<0xB1>(x));
   x = __builtin_fmaxf(x, dpp<0x4E>(x));
@@ -589,6 +597,16 @@ struct Ref {
                ".set stq_v, stq_v+1\n\t.endr\n\ts_nop 4\n.Lkeep%=:"                                  \
                : __VA_ARGS__ : [m] "s"(far), [x] "v"(f) : "scc")
 #define AT(r) "+{v[" #r "]}"
+
+// Two weights as a binary16 pair.  Outputs of binary16: to nearest.  bfloat16
+// outputs take the truncating conversion (one instruction at full rate against
+// one at half): off by 2^-10 of a weight at most where the output's own
+// rounding is 2^-8, and the weights' sum takes the same truncated values.
+template <int TYPE>
+__device__ __forceinline__ f16x2 weights(float a, float b) {
+  if constexpr (TYPE == STQ_BF16) return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b));
+  else return (f16x2){(f16)a, (f16)b};
+}
 
 // Keys of a chunk and queries -> products s (tile u: tokens 8G + 4u ..).
 template <int D, int NT>
@@ -791,7 +809,7 @@ __global__ void __launch_bounds__(64 * ROW_WAVES, 2) k_attend_rows(AttnArgs A) {
       for (int e = 0; e < 4; e++) {
         const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1)], cf[nt], -ref[nt].mc));
         const float b2 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1) + 1], cf[nt], -ref[nt].mc));
-        const f16x2 hh = {(f16)a, (f16)b2};
+        const f16x2 hh = weights<TYPE>(a, b2);
         pk[e] = h2_bits(hh);
         l[nt] = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, l[nt], false);
       }
@@ -865,8 +883,8 @@ __global__ void __launch_bounds__(64 * ROW_WAVES, 2) k_attend_rows(AttnArgs A) {
 }
 
 // Many query rows per key/value head (prompts): the matrix products bound the
-// work.  One workgroup = one (request, head, tile of 32 NW rows, split), each
-// wave 32 rows.  Tiles of 64 cached tokens (two chunks) go through LDS as
+// work.  One workgroup = one (request, head, tile of 128 rows, split), each wave
+// 32 rows.  Tiles of 64 cached tokens (two chunks) go through LDS as
 // binary16, unpacked once for all the waves, double buffered: while the waves
 // work on one tile, the next one's bytes are converted and the one after it
 // is on its way from memory.  One barrier per tile.
@@ -902,33 +920,64 @@ __device__ __forceinline__ float max_halves(float x) {
   return __builtin_fmaxf(bits_f(a[0]), bits_f(a[1]));
 }
 
-#ifndef SCHED
-#define SGB(m, n) __builtin_amdgcn_sched_group_barrier(m, n, 0);
-#define PH1 SGB(8, 1) SGB(0x100, 1) SGB(2, 6)
-#define PH2 SGB(0x100, 2) SGB(8, 1) SGB(2, 3) SGB(0x100, 2) SGB(8, 1) SGB(2, 3) SGB(0x200, 1)
-#define SCHED SGB(0x100, 4) PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH1 PH2 PH2 PH2 PH2 PH2 PH2 PH2 PH2
-#endif
-template <int D, int TYPE, int NW>
-__global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
-  constexpr int NT = 64 * NW, ROWS = 32 * NW;
-  constexpr int KP = 2 * D;                            // 16-byte pieces of a tile's key codes (32 channels of a token)
+// The x-th tile of a batch: request and first row.  Of up to 64 requests (one a
+// lane) the tiles come by the position they end at, in bands a tile high, the
+// latest first: they have the most to see, and a list that goes from long to
+// short leaves the least of the card idle at its end; no workgroup but the
+// last ones is without a tile.  (Requests in their own order met the same shader
+// engine again and again, since workgroups are dealt to the XCDs and engines
+// in turn: 4 prompts of 1,078 to 2,048 tokens 488 us, rotated from level to level
+// 325; a loop of 253 us rotated took 234 so.)
+// More requests: each one's last tile first, the requests rotated from level to level.
+__device__ __forceinline__ bool tile_of(const AttnArgs& A, int rows_of_tile, int x, int* req, int* row0) {
+  if (A.n_req > 64) {
+    const int level = x / A.n_req;
+    const int i = (x % A.n_req + (level >> 1)) % A.n_req;
+    const Req R = req_args(A, i);
+    *req = i;
+    *row0 = ((min(R.n_new, A.max_new) * A.group + rows_of_tile - 1) / rows_of_tile - 1 - level) * rows_of_tile;
+    return *row0 >= 0;
+  }
+  const int lane = threadIdx.x & 63, i = min(lane, A.n_req - 1);
+  const int first = min(max(A.tok_start[i], 0), A.n_tok), end = min(max(A.tok_start[i + 1], first), A.n_tok);
+  const int len = (int)min((int64_t)max(A.len[i], 0), (int64_t)A.cols * A.T);
+  const int fresh = min(end - first, A.max_new);
+  const int tiles = lane < A.n_req ? (fresh * A.group + rows_of_tile - 1) / rows_of_tile : 0;
+  const int last = tiles > 0 ? len - (end - first) + fresh : -(1 << 30);    // behind the last query's position
+  const int band = max(rows_of_tile / A.group, 1);
+  const int top = wave_max_i(last);                      // (by all lanes)
+  const int skip = tiles > 0 ? (top - last) / band : 0;  // bands above the request's first
+  int lo = 0, hi = wave_max_i(skip + tiles);
+  if (x >= wave_sum_i(tiles)) return false;
+  while (hi - lo > 1) {                                  // the band that holds tile x: at most x tiles lie above it
+    const int mid = (lo + hi) >> 1;
+    if (wave_sum_i(min(max(mid - skip, 0), tiles)) <= x) lo = mid; else hi = mid;
+  }
+  uint64_t in = __builtin_amdgcn_ballot_w64(lo >= skip && lo < skip + tiles);
+  for (int k = x - wave_sum_i(min(max(lo - skip, 0), tiles)); k > 0; k--) in &= in - 1;
+  *req = __builtin_ctzll(in);
+  *row0 = (__builtin_amdgcn_readlane(tiles, *req) - 1 - (lo - __builtin_amdgcn_readlane(skip, *req))) * rows_of_tile;
+  return true;
+}
+
+constexpr int TILE_WAVES = 4;
+template <int D, int TYPE>
+__global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A) {
+  constexpr int ROWS = 32 * TILE_WAVES;
   constexpr int KSTEP = D / 16, NC = D / 32;
   __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][64 * D * 2], lds_v[2][64 * D * 2];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, G = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Order of the work: every request's last tile first (it has the most to
-  // see), (request, head) pairs fastest, so that a pair's workgroups share an
-  // XCD where the heads are a multiple of 8.  The requests are rotated from
-  // level to level: workgroups are dealt to the XCDs and their shader engines
-  // in turn and in order, and a ragged batch whose long requests always met the
-  // same engine left the others empty (489 against 342 us for 4 prompts).
+  // heads fastest: a head's workgroups share an XCD where the heads are a
+  // multiple of 8
   int b = blockIdx.x;
-  const int pair = b % (A.n_req * A.hkv); b /= A.n_req * A.hkv;
-  const int sp = b % A.splits, level = b / A.splits;
-  const int h = pair % A.hkv, i = (pair / A.hkv + (level >> 1)) % A.n_req;
+  const int h = b % A.hkv; b /= A.hkv;
+  const int sp = b % A.splits;
+  int i, row0;
+  if (!tile_of(A, ROWS, b / A.splits, &i, &row0)) return;
   const Req R = req_args(A, i);
-  const int rows = min(R.n_new, A.max_new) * A.group, row0 = ((rows + ROWS - 1) / ROWS - 1 - level) * ROWS;
-  if (row0 < 0) return;
+  const int rows = min(R.n_new, A.max_new) * A.group;
+  if (row0 < 0 || row0 >= rows) return;
   const int p0 = R.base + row0 / A.group, p1 = R.base + (min(row0 + ROWS, rows) - 1) / A.group;
   const Span sn = span_of(p0, p1, A.window, A.sink);
   const int per = split_chunks(A, sn.total);
@@ -976,7 +1025,6 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   // token's codes; waves 0 and 1 chunk k's, 2 and 3 chunk k + 1's.  Keys: the
   // pieces of a token side by side; values: tokens side by side (what the
   // slots' xors want).
-  static_assert(NT == 256, "a piece of the keys and one of the values per thread");
   constexpr int PS = D / 32;                           // dwords, and slots, of a piece
   const int half = wave >> 1, w128 = tid & 127;
   const int tk = w128 >> 2, ck = w128 & 3, tv = w128 & 31, cv = w128 >> 5;
@@ -1010,24 +1058,30 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
     return A.cache + ((uint64_t)(half ? x.blk[1] : x.blk[0]) * A.hkv + h) * block_bytes + off;
   };
   auto off_of = [&](const Tile& x) { return (uint32_t)((chunk_at(min(x.k + half, c1 - 1)) * 32) & (T - 1)) * (D / 2 - 1); };
-  auto fetch_k = [&](const Tile& x) {
+  auto fetch = [&](const Tile& x, uint32_t code_at, uint32_t scale_at, piece_t& raw, uint32_t& sb) {
     const uint8_t* p = base_of(x);
-    kraw = *(const piece_t*)(p + off_of(x) + kc_at);
-    ksb = p[ks_at];
-  };
-  auto fetch_v = [&](const Tile& x) {
-    const uint8_t* p = base_of(x);
-    vraw = *(const piece_t*)(p + off_of(x) + vc_at);
-    vsb = p[vs_at];
+    raw = *(const piece_t*)(p + off_of(x) + code_at);
+    sb = p[scale_at];
   };
   auto put = [&](uint8_t* buf, uint32_t at, const piece_t& raw, float sc) {
 #pragma unroll
     for (int x = 0; x < PS; x++)
       *(u32x4*)(buf + (at ^ (16 * x))) = (u32x4){cvt2<0>(raw[x], sc), cvt2<1>(raw[x], sc), cvt2<2>(raw[x], sc), cvt2<3>(raw[x], sc)};
   };
+  // (Unwritten bytes behind the last token must not be NaN or infinite as
+  // values, their weights are 0; keys keep the NaN of scale byte 255.)
+  auto fetch_k = [&](const Tile& x) { fetch(x, kc_at, ks_at, kraw, ksb); };
+  auto fetch_v = [&](const Tile& x) { fetch(x, vc_at, vs_at, vraw, vsb); };
   auto put_k = [&](int b) { put(lds_k[b], k_put, kraw, scale_of<0>(ksb)); };
-  // (unwritten bytes behind the last token must not be NaN or infinite, their weights are 0)
   auto put_v = [&](int b) { put(lds_v[b], v_put, vraw, scale_of<0>(min(vsb, (uint32_t)(E_MAX + 127)))); };
+  // in the loop: the values of the next tile and the keys of the one after it
+  // move to buffers vb and kb, the ones behind them (tiles xv, xk) are asked for
+  auto stage = [&](int vb, int kb, const Tile& xv, const Tile& xk) {
+    put_v(vb);
+    put_k(kb);
+    fetch_v(xv);
+    fetch_k(xk);
+  };
   // Where this lane reads: keys (token n, channels 8G .., and 16x more), values
   // (tokens 4G + .. and 8 more; four channels, and 32c more); other tokens of
   // the tile lie whole rows on.
@@ -1049,7 +1103,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
   // One tile: its products s become weights and meet its values, while the
   // matrix cores make the next tile's products sn (nothing of one waits for the
   // other, so the compiler interleaves them).
-  auto work = [&](const Tile& x, f32x16* s, f32x16* sn, const uint8_t* next_k, const uint8_t* v, auto&& stage) {
+  auto work = [&](const Tile& x, f32x16* s, f32x16* sn, const uint8_t* next_k, const uint8_t* v, auto&& move_on) {
     const int ta = chunk_at(x.k) * 32, tb = chunk_at(min(x.k + 1, c1 - 1)) * 32;
     const bool in_a = A.window == 0 || ta > pw1 - A.window || ta + 31 < A.sink;
     const bool in_b = A.window == 0 || tb > pw1 - A.window || tb + 31 < A.sink;
@@ -1077,8 +1131,10 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
       SCALE_WHERE(far, f, 192, 64, AT(192:207)(o[0]), AT(208:223)(o[1]), AT(224:239)(o[2]), AT(240:255)(o[3]));
     else
       SCALE_WHERE(far, f, 128, 32, AT(128:143)(o[0]), AT(144:159)(o[1]));
+    // (the wave that has matrix work goes first: 234 -> 229 us)
+    __builtin_amdgcn_s_setprio(1);
     key_tile(next_k, sn);
-    stage();
+    f16x8 P[2][2];
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
@@ -1088,20 +1144,25 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
         for (int e = 0; e < 4; e++) {
           const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e], cf, -ref.mc));
           const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e + 1], cf, -ref.mc));
-          const f16x2 hh = {(f16)e0, (f16)e1};
+          const f16x2 hh = weights<TYPE>(e0, e1);
           pk[e] = h2_bits(hh);
           L = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, L, false);
         }
-        const f16x8 P = frag(pk[0], pk[1], pk[2], pk[3]);
+        P[u][y] = frag(pk[0], pk[1], pk[2], pk[3]);
+      }
+    move_on();
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+      for (int y = 0; y < 2; y++)
 #pragma unroll
         for (int c = 0; c < NC; c++) {
           const uint8_t* at = v + (32 * u + 16 * y) * D * 2;
           const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(at + (v_at[0] ^ (64 * c)))));
           const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4*)(at + (v_at[1] ^ (64 * c)))));
-          o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(lo[0], lo[1], hi[0], hi[1]), P, o[c], 0, 0, 0);
+          o[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(lo[0], lo[1], hi[0], hi[1]), P[u][y], o[c], 0, 0, 0);
         }
-      }
-    SCHED
+    __builtin_amdgcn_s_setprio(0);
   };
   if (c0 < c1) {
     Tile t0 = locate(c0), t1 = locate(c0 + 2), t2 = locate(c0 + 4);
@@ -1121,21 +1182,11 @@ __global__ void __launch_bounds__(64 * NW, 2) k_attend_tiles(AttnArgs A) {
     // t1, the keys of t2
     for (int k = c0; k < c1; k += 4) {
       const Tile t3 = locate(k + 6);
-      work(t0, sa, sb, lds_k[1], lds_v[0], [&] {
-        put_v(1);
-        put_k(0);
-        fetch_v(t2);
-        fetch_k(t3);
-      });
+      work(t0, sa, sb, lds_k[1], lds_v[0], [&] { stage(1, 0, t2, t3); });
       __syncthreads();
       if (k + 2 >= c1) break;
       const Tile t4 = locate(k + 8);
-      work(t1, sb, sa, lds_k[0], lds_v[1], [&] {
-        put_v(0);
-        put_k(1);
-        fetch_v(t3);
-        fetch_k(t4);
-      });
+      work(t1, sb, sa, lds_k[0], lds_v[1], [&] { stage(0, 1, t3, t4); });
       __syncthreads();
       t0 = t2;
       t1 = t3;
@@ -1249,7 +1300,6 @@ bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
 struct Split { int tiles, tile_rows, splits, per; bool staged; };
 // Query rows per key/value head from which the cache is staged through LDS.
 constexpr int STAGED_ROWS = 64;
-constexpr int TILE_WAVES = 4;
 // A part of a request's work has its own start (three dependent loads) and end
 // (the joins), about 5 us.  Few workgroups are split down to 8 chunks until
 // every CU holds three; many only into parts of 48 chunks and up, which even
@@ -1281,7 +1331,7 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
 template <int D, int TYPE>
 void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
-  if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE, TILE_WAVES>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
+  if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
   else if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2>), dim3(grid), dim3(64 * ROW_WAVES), 0, st, A);
   else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1>), dim3(grid), dim3(64 * ROW_WAVES), 0, st, A);
   if (A.splits > 1) {
