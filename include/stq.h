@@ -414,7 +414,7 @@ stq_status stq_debug_rcp_bf16(float* out_dev, hipStream_t stream);
  * magnitude m, e is the least integer with m <= 6 * 2^e, held in [-23, 13]
  * (every cached value is then exact in binary16; magnitudes beyond 6 * 2^13
  * saturate), e = 0 for m = 0; codes round to the nearest level, ties to the
- * even code.  A token and head whose key or value has an infinity or a NaN
+ * even code, and carry their element's sign, a zero's too.  A token and head whose key or value has an infinity or a NaN
  * is stored with NaN scales (byte 255) on the key and zeros as the value: a
  * query that sees it gets NaN, every other query is unaffected.
  * Bytes of block b, head h at (b * n_kv_heads + h) * block_tokens * d*17/16:

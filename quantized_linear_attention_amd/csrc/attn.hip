@@ -167,14 +167,18 @@ __global__ void __launch_bounds__(PLAN_NT) k_kv_plan(PlanArgs A) {
 //
 // One row (head of a token) on D/8 lanes of eight channels each: the row
 // stays in registers between its only load and its only store.  A wave takes
-// 64/(D/8) heads of one token at a time, so that the token's cosines and sines
-// are loaded once per lane and serve all its heads.
+// 64/(D/8) heads of one token at a time and all of a token's where there are
+// tokens enough (`per_tok` waves share a token's heads else), so that the
+// token's cosines and sines are loaded once for many rows; two such sets of
+// rows are under way at once.  A rotation's other half of a pair comes from
+// another lane by DPP (through LDS, as __shfl goes, the exchange alone took
+// longer than the memory: 137 us for 16,381 tokens of 40 heads).
 struct NormArgs {
   const void *q, *k;
   void *qo, *ko;
   const float *wq, *wk, *cs;
   const int32_t* pos;
-  int n_tok, hq, hk, n_rot, n_pos, norm, adjacent;
+  int n_tok, hq, hk, n_rot, n_pos, norm, adjacent, per_tok;
   float eps;
   int64_t qs, ks, qos, kos;
 };
@@ -189,85 +193,115 @@ __device__ __forceinline__ float row_sum(float x) {   // over LPR consecutive la
   return x;
 }
 
+// x of the lane m lanes up or down (m = half the lanes of the rotated
+// channels; lanes in pairs of groups of m)
+__device__ __forceinline__ float across(float x, int m, int mate) {
+  const int v = __builtin_bit_cast(int, x);
+  if (m == 8) return dpp<0x128>(x);                    // row_ror:8
+  if (m == 4)                                          // lanes 0-3 from 4 up, 4-7 from 4 down, and so on
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_amdgcn_update_dpp(0, v, 0x104, 0xF, 0x5, false), v, 0x114, 0xF, 0xA, false));
+  if (m == 2) return dpp<0x4E>(x);
+  if (m == 1) return dpp<0xB1>(x);
+  return __shfl(x, mate, 64);
+}
+
 template <int D, int IN, int OUT>
 __global__ void __launch_bounds__(256) k_qk_norm_rope(NormArgs A) {
-  constexpr int LPR = D / 8, RPW = 64 / LPR;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int LPR = D / 8, RPW = 64 / LPR, U = 2;
+  const int lane = threadIdx.x & 63;
   const int li = lane % LPR, c0 = 8 * li;
-  const int64_t t = blockIdx.x;
-  const int rows = A.hq + A.hk, R = A.n_rot;
+  const int gw = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  const int tok = gw / A.per_tok, part = gw - tok * A.per_tok;
+  if (tok >= A.n_tok) return;
+  const int64_t t = tok;
+  const int rows = A.hq + A.hk, R = A.n_rot, step = A.per_tok * RPW;
+  // rows of set x: first + x * step; past the end the last row, not stored
+  const int first = part * RPW + lane / LPR;
+  float x[U][8];
+  auto load = [&](int h, float* y) {
+    h = min(h, rows - 1);
+    if (h < A.hq) load8<IN>(A.q, t * A.qs + (int64_t)h * D + c0, y);
+    else load8<IN>(A.k, t * A.ks + (int64_t)(h - A.hq) * D + c0, y);
+  };
+#pragma unroll
+  for (int u = 0; u < U; u++) load(first + u * step, x[u]);
   float cs[8], sn[8];
   bool turn = false;
   if (R > 0) {
-    const int p = A.pos[t];
-    if ((uint32_t)p >= (uint32_t)A.n_pos) return;    // a padded row (the whole workgroup's token)
+    const int p = ld_const(A.pos + t);
+    if ((uint32_t)p >= (uint32_t)A.n_pos) return;      // a padded row: the whole token
     turn = c0 < R;
     if (turn) {
       const float* row = A.cs + (int64_t)p * R;
-      if (A.adjacent) {                               // pair i: channels 2i, 2i + 1
+      if (A.adjacent) {                                // pair i: channels 2i, 2i + 1
+        const f32x4 c = *(const f32x4*)(row + c0 / 2), s = *(const f32x4*)(row + R / 2 + c0 / 2);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          cs[2 * i] = cs[2 * i + 1] = row[c0 / 2 + i];
-          const float s = row[R / 2 + c0 / 2 + i];
-          sn[2 * i] = -s;
-          sn[2 * i + 1] = s;
+          cs[2 * i] = cs[2 * i + 1] = c[i];
+          sn[2 * i] = -s[i];
+          sn[2 * i + 1] = s[i];
         }
-      } else {                                        // pair i: channels i, i + R/2
+      } else {                                         // pair i: channels i, i + R/2
         const bool low = c0 < R / 2;
-        const int b = low ? c0 : c0 - R / 2;
+        const float* r = row + (low ? c0 : c0 - R / 2);
+        load8<STQ_FP32>(r, 0, cs);
+        load8<STQ_FP32>(r, R / 2, sn);
+        if (low)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          cs[i] = row[b + i];
-          const float s = row[R / 2 + b + i];
-          sn[i] = low ? -s : s;
-        }
+          for (int i = 0; i < 8; i++) sn[i] = -sn[i];
       }
     }
   }
-  // lane of the other half of a pair (halves); a row's rotated lanes are 0 .. R/8-1
-  const int mate = turn ? (lane - li) + (c0 < R / 2 ? li + R / 16 : li - R / 16) : lane;
+  // halves: the lane with the other half of this lane's pairs; a row's rotated lanes are 0 .. R/8-1
+  const int m = R / 16;
+  const int mate = turn ? (lane - li) + (c0 < R / 2 ? li + m : li - m) : lane;
   float wq[8], wk[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    wq[i] = A.wq ? A.wq[c0 + i] : 1.0f;
-    wk[i] = A.wk ? A.wk[c0 + i] : 1.0f;
-  }
-  for (int h0 = wave * RPW; h0 < rows; h0 += 4 * RPW) {
-    const int h = h0 + lane / LPR;
-    const bool on = h < rows, isq = h < A.hq;
-    float x[8];
-    if (on) {
-      if (isq) load8<IN>(A.q, t * A.qs + (int64_t)h * D + c0, x);
-      else load8<IN>(A.k, t * A.ks + (int64_t)(h - A.hq) * D + c0, x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; i++) x[i] = 0.0f;
-    }
+  for (int i = 0; i < 8; i++) wq[i] = wk[i] = 1.0f;
+  if (A.wq) load8<STQ_FP32>(A.wq, c0, wq);
+  if (A.wk) load8<STQ_FP32>(A.wk, c0, wk);
+  auto row = [&](int h, float* y) {
     if (A.norm != STQ_NORM_NONE) {
       float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) s = __builtin_fmaf(x[i], x[i], s);
+      for (int i = 0; i < 8; i++) s = __builtin_fmaf(y[i], y[i], s);
       s = row_sum<LPR>(s);
       if (A.norm == STQ_NORM_RMS) s *= 1.0f / D;
       const float f = 1.0f / __builtin_sqrtf(s + A.eps);
 #pragma unroll
-      for (int i = 0; i < 8; i++) x[i] *= f;
+      for (int i = 0; i < 8; i++) y[i] *= f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; i++) x[i] *= isq ? wq[i] : wk[i];
+    for (int i = 0; i < 8; i++) y[i] *= h < A.hq ? wq[i] : wk[i];
     if (R > 0) {
-      float y[8];
+      float z[8];
+      if (A.adjacent) {
 #pragma unroll
-      for (int i = 0; i < 8; i++) y[i] = A.adjacent ? x[i ^ 1] : __shfl(x[i], mate, 64);
+        for (int i = 0; i < 8; i++) z[i] = y[i ^ 1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) z[i] = across(y[i], m, mate);
+      }
       if (turn) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = __builtin_fmaf(x[i], cs[i], y[i] * sn[i]);
+        for (int i = 0; i < 8; i++) y[i] = __builtin_fmaf(y[i], cs[i], z[i] * sn[i]);
       }
     }
-    if (on) {
-      if (isq) store8<OUT>(A.qo, t * A.qos + (int64_t)h * D + c0, x);
-      else store8<OUT>(A.ko, t * A.kos + (int64_t)(h - A.hq) * D + c0, x);
+    if (h < rows) {
+      if (h < A.hq) store8<OUT>(A.qo, t * A.qos + (int64_t)h * D + c0, y);
+      else store8<OUT>(A.ko, t * A.kos + (int64_t)(h - A.hq) * D + c0, y);
     }
+  };
+  for (int h = first; h - lane / LPR < rows; h += U * step) {
+    float next[U][8];
+#pragma unroll
+    for (int u = 0; u < U; u++) load(h + (U + u) * step, next[u]);
+#pragma unroll
+    for (int u = 0; u < U; u++) row(h + u * step, x[u]);
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int i = 0; i < 8; i++) x[u][i] = next[u][i];
   }
 }
 
@@ -289,50 +323,66 @@ __device__ __forceinline__ int scale_exp(float m) {
   const int e = (u & 0x7FFFFFu) > 0x400000u ? x - 1 : x - 2;
   return m == 0.0f ? 0 : min(max(e, E_MIN), E_MAX);
 }
-// Code of |y| (already divided by the scale) with y's sign: nearest of
-// 0 .5 1 1.5 2 3 4 6, ties to the even code.
-__device__ __forceinline__ uint32_t code_of(float y) {
-  const float a = __builtin_fabsf(y);
-  uint32_t c = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) + (uint32_t)(a >= 1.75f) +
-               (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
-  return c | ((c != 0 && y < 0.0f) ? 8u : 0u);
-}
-// eight channels as one dword of codes; the block's largest magnitude over its four lanes
+// eight channels as one dword of codes; the block's largest magnitude over its
+// four lanes.  The conversion divides by the scale, rounds to nearest with ties
+// to the even code and saturates (tests/test_gpu_attn.py goes through every
+// level, midpoint and neighbour at every exponent).
 __device__ __forceinline__ uint32_t codes8(const float* x, int* e_out) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, __builtin_fabsf(x[i]));
   m = rb_max_pos<4>(m);
   const int e = scale_exp(m);
+  const float sc = bits_f((uint32_t)(e + 127) << 23);
   uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 8; i++) w |= code_of(__builtin_ldexpf(x[i], -e)) << (4 * i);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], sc, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], sc, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], sc, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], sc, 3);
   *e_out = e;
   return w;
 }
 
-// One (token, head) on D/8 lanes, keys and values together (the NaN rule needs both).
+// One (token, head) on D/8 lanes, keys and values together (the NaN rule needs
+// both).  A workgroup takes consecutive tokens of one head, whose codes and
+// scales lie side by side where the slots do; the heads come fastest, so that
+// the workgroups at work share the tokens' rows.
+struct StoreAt { int64_t t; int h, li; bool on; };
+template <int D>
+__device__ __forceinline__ StoreAt store_at(const StoreArgs& A) {
+  constexpr int LPR = D / 8, RPB = 256 / LPR;
+  StoreAt s;
+  const uint32_t tile = blockIdx.x / (uint32_t)A.heads;
+  s.h = (int)(blockIdx.x - tile * (uint32_t)A.heads);
+  s.li = threadIdx.x % LPR;
+  s.t = (int64_t)tile * RPB + threadIdx.x / LPR;
+  s.on = s.t < A.n_tok;
+  return s;
+}
+// first byte of the slot's block for this head, and the slot's place in it
+template <int D>
+__device__ __forceinline__ uint8_t* block_at(const StoreArgs& A, int64_t slot, int h, int* off) {
+  const int shift = 31 - __builtin_clz(A.T);
+  *off = (int)(slot & (A.T - 1));
+  return A.cache + ((slot >> shift) * A.heads + h) * ((int64_t)A.T * D / 16 * 17);
+}
+
 template <int D, int TYPE>
 __global__ void __launch_bounds__(256) k_kv_store(StoreArgs A) {
-  constexpr int LPR = D / 8, RPB = 256 / LPR;
-  const int li = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-  const int64_t t = row / A.heads;
-  const int h = (int)(row - t * A.heads);
-  const bool on = t < A.n_tok;
-  const int64_t slot = on ? A.slot[t] : -1;
-  const bool live = slot >= 0 && slot < A.n_slots;
+  constexpr int LPR = D / 8;
+  const StoreAt s = store_at<D>(A);
+  const int li = s.li;
+  const int64_t t = s.on ? s.t : A.n_tok - 1;          // (lanes past the end read the last token's row again)
+  const int64_t slot = A.slot[t];
+  const bool live = s.on && slot >= 0 && slot < A.n_slots;
   float k[8], v[8];
+  load8<TYPE>(A.k, t * A.ks + (int64_t)s.h * D + 8 * li, k);
+  load8<TYPE>(A.v, t * A.vs + (int64_t)s.h * D + 8 * li, v);
+  // 0 * x is 0 for every finite x, NaN for the others
+  float z = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) k[i] = v[i] = 0.0f;
-  if (live) {
-    load8<TYPE>(A.k, t * A.ks + (int64_t)h * D + 8 * li, k);
-    load8<TYPE>(A.v, t * A.vs + (int64_t)h * D + 8 * li, v);
-  }
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; i++) bad |= !(__builtin_fabsf(k[i]) < __builtin_inff()) || !(__builtin_fabsf(v[i]) < __builtin_inff());
-  const uint64_t any = __ballot(bad);
+  for (int i = 0; i < 8; i++) z = __builtin_fmaf(k[i], 0.0f, __builtin_fmaf(v[i], 0.0f, z));
+  const uint64_t any = __ballot(z != z);
   const int l0 = (threadIdx.x & 63) - li;
   const bool poison = ((any >> l0) & ((1ull << LPR) - 1)) != 0;
   if (poison) {
@@ -342,8 +392,9 @@ __global__ void __launch_bounds__(256) k_kv_store(StoreArgs A) {
   int ek, ev;
   const uint32_t ck = codes8(k, &ek), cv = codes8(v, &ev);
   if (!live) return;
-  const int T = A.T, off = (int)(slot % T);
-  uint8_t* hb = A.cache + ((slot / T) * A.heads + h) * ((int64_t)T * D * 17 / 16);
+  const int T = A.T;
+  int off;
+  uint8_t* hb = block_at<D>(A, slot, s.h, &off);
   *(uint32_t*)(hb + off * (D / 2) + 4 * li) = ck;
   *(uint32_t*)(hb + T * (D / 2) + off * (D / 2) + 4 * li) = cv;
   if ((li & 3) == 0) {
@@ -353,38 +404,43 @@ __global__ void __launch_bounds__(256) k_kv_store(StoreArgs A) {
   }
 }
 
-// eight codes of a dword as binary32 values
-__device__ __forceinline__ void values8(uint32_t w, uint32_t sbyte, float* x) {
-  const float sc = sbyte == 255 ? __builtin_nanf("") : bits_f(sbyte << 23);
+// eight codes of a dword as elements: the conversion's binary16 pairs are
+// exact, and NaN for scale byte 255
+template <int TYPE>
+__device__ __forceinline__ void fetch8(uint32_t w, uint32_t sbyte, void* out, int64_t at) {
+  const float sc = bits_f(sbyte << 23);
+  uint32_t h[4];
+  h[0] = h2_bits(__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 0)));
+  h[1] = h2_bits(__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 1)));
+  h[2] = h2_bits(__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 2)));
+  h[3] = h2_bits(__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 3)));
+  if constexpr (TYPE == STQ_FP16) {
+    *(u32x4*)((uint16_t*)out + at) = (u32x4){h[0], h[1], h[2], h[3]};
+  } else {
+    float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const uint32_t c = (w >> (4 * i)) & 7u;
-    // magnitude: exponent bits c >> 1, mantissa bit c & 1; below 2 the codes are 0 and 0.5
-    const float m = c < 2 ? 0.5f * c : bits_f(((126u + (c >> 1)) << 23) | ((c & 1u) << 22));
-    x[i] = (((w >> (4 * i)) & 8u) ? -m : m) * sc;
+    for (int i = 0; i < 8; i++) x[i] = (float)as_h2(h[i >> 1])[i & 1];
+    store8<TYPE>(out, at, x);
   }
 }
 
 template <int D, int TYPE>
 __global__ void __launch_bounds__(256) k_kv_fetch(StoreArgs A) {
-  constexpr int LPR = D / 8, RPB = 256 / LPR;
-  const int li = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-  const int64_t t = row / A.heads;
-  const int h = (int)(row - t * A.heads);
-  if (t >= A.n_tok) return;
-  const int64_t slot = A.slot[t];
+  const StoreAt s = store_at<D>(A);
+  if (!s.on) return;
+  const int li = s.li;
+  const int64_t slot = A.slot[s.t];
   if (slot < 0 || slot >= A.n_slots) return;
-  const int T = A.T, off = (int)(slot % T);
-  const uint8_t* hb = A.cache + ((slot / T) * A.heads + h) * ((int64_t)T * D * 17 / 16);
+  const int T = A.T;
+  int off;
+  const uint8_t* hb = block_at<D>(A, slot, s.h, &off);
   const uint32_t ck = *(const uint32_t*)(hb + off * (D / 2) + 4 * li);
   const uint32_t cv = *(const uint32_t*)(hb + T * (D / 2) + off * (D / 2) + 4 * li);
   const uint8_t* sc = hb + T * D + (li >> 2) * T + off;
-  float x[8];
-  values8(ck, sc[0], x);
-  store8<TYPE>(A.ko, row * D + 8 * li, x);
-  values8(cv, sc[T * (D / 32)], x);
-  store8<TYPE>(A.vo, row * D + 8 * li, x);
+  const uint32_t sk = sc[0], sv = sc[T * (D / 32)];
+  const int64_t at = (s.t * A.heads + s.h) * D + 8 * li;
+  fetch8<TYPE>(ck, sk, A.ko, at);
+  fetch8<TYPE>(cv, sv, A.vo, at);
 }
 
 // ------------------------------------------------------------- attention
@@ -1284,6 +1340,7 @@ stq_status kv_check(const stq_kv_desc* d, const void* cache, size_t bytes) {
   if (!cache || ((uintptr_t)cache & 15u) || bytes < kv_size(d)) return STQ_ERR_LAYOUT;
   return STQ_OK;
 }
+int64_t kv_grid(const stq_kv_desc* d, int64_t n_tok) { return (n_tok + 2048 / d->d - 1) / (2048 / d->d) * d->n_kv_heads; }
 bool aligned(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 int elem_bytes(int type) { return type == STQ_FP32 ? 4 : 2; }
 bool stride_ok(int64_t stride, int64_t least, int type) {
@@ -1340,9 +1397,10 @@ void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   }
 }
 
+constexpr int64_t NORM_WAVES = 8192;
 template <int D, int IN>
 void launch_norm(const NormArgs& A, int out, hipStream_t st) {
-  const dim3 g((unsigned)A.n_tok), b(256);
+  const dim3 g((unsigned)(((int64_t)A.n_tok * A.per_tok + 3) / 4)), b(256);
   if (out == STQ_FP32) hipLaunchKernelGGL((k_qk_norm_rope<D, IN, STQ_FP32>), g, b, 0, st, A);
   else hipLaunchKernelGGL((k_qk_norm_rope<D, IN, IN>), g, b, 0, st, A);
 }
@@ -1356,7 +1414,7 @@ void launch_norm_in(const NormArgs& A, int in, int out, hipStream_t st) {
 template <int D>
 void launch_kv(const StoreArgs& A, int type, bool store, hipStream_t st) {
   constexpr int RPB = 256 / (D / 8);
-  const dim3 g((unsigned)(((int64_t)A.n_tok * A.heads + RPB - 1) / RPB)), b(256);
+  const dim3 g((unsigned)(((int64_t)A.n_tok + RPB - 1) / RPB * A.heads)), b(256);
   if (store) {
     if (type == STQ_BF16) hipLaunchKernelGGL((k_kv_store<D, STQ_BF16>), g, b, 0, st, A);
     else if (type == STQ_FP16) hipLaunchKernelGGL((k_kv_store<D, STQ_FP16>), g, b, 0, st, A);
@@ -1421,6 +1479,11 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   A.n_tok = d->n_tok; A.hq = d->n_q_heads; A.hk = d->n_k_heads; A.n_rot = d->n_rot; A.n_pos = d->n_pos; A.norm = d->norm;
   A.adjacent = d->rot_pairs == STQ_ROT_ADJACENT; A.eps = d->eps;
   A.qs = d->q_stride; A.ks = d->k_stride; A.qos = d->q_out_stride; A.kos = d->k_out_stride;
+  // waves of one token: as many as fill the card, each with two sets of rows at least
+  const int sets = (A.hq + A.hk + 512 / d->d - 1) / (512 / d->d);
+  A.per_tok = (int)((NORM_WAVES + A.n_tok - 1) / A.n_tok);
+  if (A.per_tok > (sets + 1) / 2) A.per_tok = (sets + 1) / 2;
+  if ((int64_t)A.n_tok * A.per_tok > INT32_MAX) A.per_tok = 1;
   if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, st);
   else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, st);
   else launch_norm_in<256>(A, d->in_type, d->out_type, st);
@@ -1436,6 +1499,7 @@ stq_status stq_kv_store(const stq_kv_desc* d, void* cache, size_t bytes, const i
   if (!slot || !k || !v) return STQ_ERR_ARG;
   const int64_t w = (int64_t)d->n_kv_heads * d->d;
   if (!aligned(k) || !aligned(v) || !stride_ok(k_stride, w, type) || !stride_ok(v_stride, w, type)) return STQ_ERR_LAYOUT;
+  if (kv_grid(d, n_tok) > INT32_MAX) return STQ_ERR_UNSUPPORTED;
   StoreArgs A;
   memset(&A, 0, sizeof(A));
   A.cache = (uint8_t*)cache; A.slot = slot; A.k = k; A.v = v; A.n_tok = n_tok; A.heads = d->n_kv_heads;
@@ -1453,6 +1517,7 @@ stq_status stq_kv_fetch(const stq_kv_desc* d, const void* cache, size_t bytes, c
   if (n_tok == 0) return STQ_OK;
   if (!slot || !k_out || !v_out) return STQ_ERR_ARG;
   if (!aligned(k_out) || !aligned(v_out)) return STQ_ERR_LAYOUT;
+  if (kv_grid(d, n_tok) > INT32_MAX) return STQ_ERR_UNSUPPORTED;
   StoreArgs A;
   memset(&A, 0, sizeof(A));
   A.cache = (uint8_t*)cache; A.slot = slot; A.ko = k_out; A.vo = v_out; A.n_tok = n_tok; A.heads = d->n_kv_heads;

@@ -27,7 +27,7 @@ def quantise(x):
     a = np.minimum(np.abs(b) / 2.0 ** e[..., None].astype(np.float64), 6.0)    # saturation
     order = np.array([0, 2, 4, 6, 1, 3, 5, 7])            # even codes first: they take the ties
     code = order[np.abs(a[..., None] - LEVELS[order]).argmin(-1)]
-    code = np.where((code > 0) & (b < 0), code + 8, code)
+    code = np.where(np.signbit(b), code + 8, code)          # a zero keeps its sign
     return code.reshape(x.shape).astype(np.uint8), e.reshape(x.shape[:-1] + (d // 32,))
 
 
