@@ -3,6 +3,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch    # before the library: see _load
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _PATH = os.path.join(_PKG, "libstq.so")
@@ -54,9 +55,9 @@ def _load():
     if not os.path.exists(_PATH):
         raise ImportError("libstq.so is not built (%s); run quantized_linear_attention_amd/build.py "
                           "or __graft_entry__.build()" % _PATH)
-    # torch first: its HIP runtime then serves the library too.  Loaded the other
-    # way round there are two runtimes in the process, and the library's sees no device.
-    import torch  # noqa: F401
+    # torch has been imported above: its HIP runtime then serves the library too.
+    # Loaded the other way round there are two runtimes in the process, and the
+    # library's sees no device.
     L = ctypes.CDLL(_PATH)
     P, I, St = ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p
     DP = ctypes.POINTER(_Desc)
@@ -312,12 +313,7 @@ def stq_requant_fixed_scales(pool, slots, stream=None):
 
 # ------------------------------------------- the softmax layers' operators
 
-def _type_codes():
-    import torch
-    return {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}
-
-
-_TYPES = _type_codes()
+_TYPES = {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}
 
 
 def _type(t, what, allowed=(STQ_BF16, STQ_FP16, STQ_FP32)):
@@ -331,9 +327,10 @@ def _ptr(t, dtype, what, numel, index):
     """Address of a contiguous CUDA tensor of `dtype` with `numel` elements on
     device `index`: the per-token calls' checks, as few Python steps as they
     take (0.5 us a tensor; _dev words the refusal)."""
-    if t.dtype is dtype and t.numel() == numel and t.get_device() == index and t.is_contiguous():
+    if t is not None and t.dtype is dtype and t.numel() == numel and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
-    import torch
+    if t is None:
+        raise StqError(-1, "%s is missing" % what)
     _dev(t, dtype, what, numel, torch.device("cuda", index))
     raise StqError(-1, "%s is on %s, expected cuda:%d" % (what, t.device, index))
 
@@ -355,16 +352,14 @@ def _heads(t, what, n, heads, d, index):
     return t.data_ptr(), st if a > 1 and st > b * c else b * c
 
 
-def _i32(v, what):
-    """A count that the C struct holds in 32 bits (ctypes would drop the rest in silence)."""
-    if not -2 ** 31 <= v < 2 ** 31:
-        raise StqError(-1, "%s = %s does not fit 32 bits" % (what, v))
-    return v
+def _i32(*sizes):
+    """Sizes that C takes in 32 bits (ctypes would drop the rest in silence)."""
+    if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:
+        raise StqError(-1, "one of the sizes %s does not fit 32 bits" % (sizes,))
 
 
 def _call(name, index, stream, *args):
     """One library call on device `index` and its current stream (or the given one)."""
-    import torch
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(index)
     else:
@@ -387,35 +382,37 @@ class _Kv:
 
 def stq_kv_bytes(n_blocks, block_tokens, n_kv_heads, d):
     """Bytes of the cache's device buffer; 0 for sizes the library does not take."""
-    desc = _KvDesc(*(_i32(int(x), "a size") for x in (n_blocks, block_tokens, n_kv_heads, d)))
-    return _L.stq_kv_bytes(ctypes.byref(desc))
+    _i32(n_blocks, block_tokens, n_kv_heads, d)
+    return _L.stq_kv_bytes(ctypes.byref(_KvDesc(n_blocks, block_tokens, n_kv_heads, d)))
 
 
 def make_kv(pages, block_tokens, n_kv_heads, d):
     """The 4-bit key/value cache that lives in `pages`, a contiguous uint8 CUDA
     tensor: as many whole blocks as it holds.  No copy, no initialisation."""
-    import torch
+    n = 0 if pages is None else pages.numel()
     _dev(pages, torch.uint8, "pages")
-    one = stq_kv_bytes(1, block_tokens, n_kv_heads, d)
-    if pages is None or not one or pages.numel() < one:
-        raise StqError(-1, "pages of %s bytes hold no block of %s tokens, %s heads, d = %s"
-                       % (None if pages is None else pages.numel(), block_tokens, n_kv_heads, d))
-    return _Kv(_KvDesc(min(pages.numel() // one, 2 ** 31 - 1), block_tokens, n_kv_heads, d), pages)
+    _i32(block_tokens, n_kv_heads, d)
+    desc = _KvDesc(1, block_tokens, n_kv_heads, d)
+    one = _L.stq_kv_bytes(ctypes.byref(desc))
+    if not one or n < one:
+        raise StqError(-1, "pages of %d bytes hold no block of %s tokens, %s heads, d = %s" % (n, block_tokens, n_kv_heads, d))
+    desc.n_blocks = min(n // one, 2 ** 31 - 1)
+    return _Kv(desc, pages)
 
 
 def stq_kv_plan(cached, new, free, table, block_tokens, n_blocks, tok_start, lens, pos, slots, used, stream=None):
     """cached, new int32 [n]; free int32; table int32 [n][cols], updated in place;
     outputs tok_start int32 [n+1], lens int32 [n], pos int32 [tokens], slots int64
     [tokens], used int32 [1]."""
-    import torch
     i, dev = torch.int32, table.get_device()
     if table.dim() != 2:
         raise StqError(-1, "table must be [requests][columns]")
     n, cols = table.shape
     tok, nf = pos.numel(), free.numel()
+    _i32(n, cols, tok, nf, n_blocks, block_tokens)
     _call("stq_kv_plan", dev, stream, n, _ptr(cached, i, "cached", n, dev), _ptr(new, i, "new", n, dev),
-          _ptr(free, i, "free", nf, dev), _i32(nf, "free entries"), _i32(n_blocks, "n_blocks"),
-          _i32(block_tokens, "block_tokens"), _ptr(table, i, "table", n * cols, dev), cols, _i32(tok, "tokens"),
+          _ptr(free, i, "free", nf, dev), nf, n_blocks,
+          block_tokens, _ptr(table, i, "table", n * cols, dev), cols, tok,
           _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), _ptr(pos, i, "pos", tok, dev),
           _ptr(slots, torch.int64, "slots", tok, dev), _ptr(used, i, "used", 1, dev))
 
@@ -425,7 +422,6 @@ def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=N
     """q, k [tokens][heads][d] (views with contiguous heads; k and k_out may be
     None); outputs of the same type or float32; weights float32 [d]; with a
     table cos_sin float32 [positions][n_rot], pos int32 [tokens]."""
-    import torch
     f = torch.float32
     qp, qs = _heads(q, "q", None, None, None, None)
     n, hq, d = q.shape
@@ -451,34 +447,36 @@ def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=N
         q_weight = _ptr(q_weight, f, "q_weight", d, dev)
     if k_weight is not None:
         k_weight = _ptr(k_weight, f, "k_weight", d, dev)
-    desc = _NormDesc(_i32(n, "tokens"), hq, hk, d, ti, to, norm, eps, n_rot, rot_pairs, _i32(n_pos, "positions"), qs, ks, qos, kos)
+    _i32(n, n_rot, n_pos, norm, rot_pairs)
+    desc = _NormDesc(n, hq, hk, d, ti, to, norm, eps, n_rot, rot_pairs, n_pos, qs, ks, qos, kos)
     _call("stq_qk_norm_rope", dev, stream, ctypes.byref(desc), qp, kp, q_weight, k_weight, pos, cos_sin, qop, kop)
 
 
 def stq_kv_store(kv, slots, k, v, stream=None):
     """slots int64 [tokens]; k, v [tokens][n_kv_heads][d] of one element type."""
-    import torch
     n, dev = slots.numel(), kv.index
+    _i32(n)
     kp, ks = _heads(k, "k", n, kv.n_kv_heads, kv.d, dev)
     vp, vs = _heads(v, "v", n, kv.n_kv_heads, kv.d, dev)
     if v.dtype is not k.dtype:
         raise StqError(-1, "k and v must have one element type")
-    _call("stq_kv_store", dev, stream, kv.ref, kv.ptr, kv.bytes, _ptr(slots, torch.int64, "slots", n, dev), _i32(n, "tokens"),
+    _call("stq_kv_store", dev, stream, kv.ref, kv.ptr, kv.bytes, _ptr(slots, torch.int64, "slots", n, dev), n,
           kp, vp, ks, vs, _type(k, "k"))
 
 
 def stq_kv_fetch(kv, slots, k_out, v_out, stream=None):
     """slots int64 [tokens]; k_out, v_out contiguous [tokens][n_kv_heads][d] of one element type."""
-    import torch
     n, dev = slots.numel(), kv.index
+    _i32(n)
     want, ty = n * kv.n_kv_heads * kv.d, k_out.dtype
-    _call("stq_kv_fetch", dev, stream, kv.ref, kv.ptr, kv.bytes, _ptr(slots, torch.int64, "slots", n, dev), _i32(n, "tokens"),
+    _call("stq_kv_fetch", dev, stream, kv.ref, kv.ptr, kv.bytes, _ptr(slots, torch.int64, "slots", n, dev), n,
           _ptr(k_out, ty, "k_out", want, dev), _ptr(v_out, ty, "v_out", want, dev), _type(k_out, "k_out"))
 
 
 def stq_kv_attend_bytes(kv, n_req, n_tok, n_heads, max_new, max_len, window=0, n_sink=0):
     """Bytes of the workspace that stq_kv_attend takes for these sizes (0: none)."""
-    a = _AttendDesc(*(_i32(x, "a size") for x in (n_req, n_tok, n_heads, STQ_BF16, 1, max_new, max_len, window, n_sink)), 1.0, 0, 0)
+    _i32(n_req, n_tok, n_heads, max_new, max_len, window, n_sink)
+    a = _AttendDesc(n_req, n_tok, n_heads, STQ_BF16, 1, max_new, max_len, window, n_sink, 1.0, 0, 0)
     return _L.stq_kv_attend_bytes(kv.ref, ctypes.byref(a))
 
 
@@ -486,7 +484,6 @@ def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, win
     """table int32 [requests][cols]; tok_start int32 [requests + 1]; lens int32
     [requests]; q, o [tokens][n_heads][d], bfloat16 or float16; work: uint8
     tensor of at least stq_kv_attend_bytes(...) bytes (None where that is 0)."""
-    import torch
     i, dev = torch.int32, kv.index
     if table.dim() != 2:
         raise StqError(-1, "table must be [requests][columns]")
@@ -501,7 +498,8 @@ def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, win
     if work is not None:
         wn = work.numel()
         wp = _ptr(work, torch.uint8, "work", wn, dev)
-    desc = _AttendDesc(n, _i32(tok, "tokens"), heads, ty, _i32(cols, "table columns"), _i32(max_new, "max_new"),
-                       _i32(max_len, "max_len"), _i32(window, "window"), _i32(n_sink, "n_sink"), scale, qs, os_)
+    _i32(tok, cols, max_new, max_len, window, n_sink)
+    desc = _AttendDesc(n, tok, heads, ty, cols, max_new,
+                       max_len, window, n_sink, scale, qs, os_)
     _call("stq_kv_attend", dev, stream, kv.ref, kv.ptr, kv.bytes, ctypes.byref(desc), _ptr(table, i, "table", n * cols, dev),
           _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), qp, op, wp, wn)

@@ -717,8 +717,8 @@ __device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, con
 
 // Few query rows per key/value head (a token's head group, drafted tokens):
 // the cache's bytes bound the work, so nothing is staged.  One workgroup =
-// one (request, head, tile of 16 NT rows, split of the cache); its four
-// waves take every fourth chunk straight from memory into the operands'
+// one (request, head, tile of 16 NT rows, split of the cache); its NWV
+// waves take every NWV-th chunk straight from memory into the operands'
 // registers and join their running softmaxes through LDS at the end.
 // o *= f of tile nt where any lane of `far` is set (accumulators of 16 rows and
 // D channels: D/4 registers)
@@ -741,10 +741,9 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
   }
 }
 
-constexpr int ROW_WAVES = 4;
-template <int D, int TYPE, int NT>
-__global__ void __launch_bounds__(64 * ROW_WAVES, 2) k_attend_rows(AttnArgs A) {
-  constexpr int NC = D / 16, NWV = ROW_WAVES;
+template <int D, int TYPE, int NT, int NWV>
+__global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(AttnArgs A) {
+  constexpr int NC = D / 16;
   __shared__ f32x4 so[NWV][NT * NC][64];
   __shared__ f32x2 sml[NWV][NT][16];
   const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
@@ -1354,7 +1353,7 @@ bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
          (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
          a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
 }
-struct Split { int tiles, tile_rows, splits, per; bool staged; };
+struct Split { int tiles, tile_rows, splits, per, waves; bool staged; };
 // Query rows per key/value head from which the cache is staged through LDS.
 constexpr int STAGED_ROWS = 64;
 // A part of a request's work has its own start (three dependent loads) and end
@@ -1362,7 +1361,7 @@ constexpr int STAGED_ROWS = 64;
 // every CU holds three; many only into parts of 48 chunks and up, which even
 // out ragged lengths (64 requests of 2,048 to 8,191 tokens, 8 heads: 83.1 us
 // whole, 78.3 in parts of 48 chunks, 85 in parts of 128, 91 in parts of 24).
-constexpr int64_t FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 3072, MANY_CHUNKS = 48, MOST_SPLITS = 128;
+constexpr int64_t CUS = 256, FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 3072, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
   const int64_t rows = (int64_t)a->max_new * (a->n_heads / d->n_kv_heads);
@@ -1380,6 +1379,15 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
     k = least(few > many ? few : many, MOST_SPLITS);
     if (k < 1) k = 1;
   }
+  // One workgroup a CU or fewer, and not much for each: sixteen waves and no
+  // second launch (1 x 500 tokens 8.5 -> 7.9 us, 32 x 1,000 14.1 -> 11.8; 1 x
+  // 1,021 8.6 -> 9.5 but 2.5 us less on the host; 8 x 2,000 would lose, 12.1 ->
+  // 13.4, and so would up to 8 chunks, 5.4 -> 6.2).
+  s.waves = 4;
+  if (s.tile_rows == 16 && base <= CUS && chunks > 8 && chunks <= (2 * base >= CUS ? 64 : 32)) {
+    s.waves = 16;
+    k = 1;
+  }
   s.per = (int)(((chunks + k - 1) / k + 3) & ~3ll);
   s.splits = (int)((chunks + s.per - 1) / s.per);
   return s;
@@ -1389,8 +1397,9 @@ template <int D, int TYPE>
 void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
   if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
-  else if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2>), dim3(grid), dim3(64 * ROW_WAVES), 0, st, A);
-  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1>), dim3(grid), dim3(64 * ROW_WAVES), 0, st, A);
+  else if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4>), dim3(grid), dim3(256), 0, st, A);
+  else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16>), dim3(grid), dim3(1024), 0, st, A);
+  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4>), dim3(grid), dim3(256), 0, st, A);
   if (A.splits > 1) {
     const int64_t rows = (int64_t)A.n_req * A.max_new * A.hq;
     hipLaunchKernelGGL((k_attend_join<D, TYPE>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, A, s.tile_rows);
