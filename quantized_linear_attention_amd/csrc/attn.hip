@@ -20,16 +20,30 @@ constexpr int E_MIN = -23, E_MAX = 13;   // exponents of the cache's scales
 
 __device__ __forceinline__ float bits_f(uint32_t u) { return __uint_as_float(u); }
 
+// A 16-byte load that leaves no trace in the caches (once = true: data that no
+// one reads again) or an ordinary one.
+template <bool ONCE, typename T>
+__device__ __forceinline__ T load16(const T* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+// A 16-byte store past the caches (PAST: an output larger than they are) or into them.
+template <bool PAST, typename T>
+__device__ __forceinline__ void store16(T* p, T v) {
+  if constexpr (PAST) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 // Eight consecutive elements as binary32 (16-byte loads; 2 of them for fp32).
-template <int TYPE>
+template <int TYPE, bool ONCE = false>
 __device__ __forceinline__ void load8(const void* base, int64_t at, float* x) {
   if constexpr (TYPE == STQ_FP32) {
     const f32x4* p = (const f32x4*)((const float*)base + at);
-    const f32x4 a = p[0], b = p[1];
+    const f32x4 a = load16<ONCE>(p), b = load16<ONCE>(p + 1);
 #pragma unroll
     for (int i = 0; i < 4; i++) { x[i] = a[i]; x[4 + i] = b[i]; }
   } else {
-    const u32x4 a = *(const u32x4*)((const uint16_t*)base + at);
+    const u32x4 a = load16<ONCE>((const u32x4*)((const uint16_t*)base + at));
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       if constexpr (TYPE == STQ_BF16) {
@@ -53,17 +67,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return h2_bits((f16x2){(f16)a, (f16)b});
   }
 }
-template <int TYPE>
+template <int TYPE, bool PAST = false>
 __device__ __forceinline__ void store8(void* base, int64_t at, const float* x) {
   if constexpr (TYPE == STQ_FP32) {
     f32x4* p = (f32x4*)((float*)base + at);
-    p[0] = (f32x4){x[0], x[1], x[2], x[3]};
-    p[1] = (f32x4){x[4], x[5], x[6], x[7]};
+    store16<PAST>(p, (f32x4){x[0], x[1], x[2], x[3]});
+    store16<PAST>(p + 1, (f32x4){x[4], x[5], x[6], x[7]});
   } else {
     u32x4 a;
 #pragma unroll
     for (int i = 0; i < 4; i++) a[i] = pack2<TYPE>(x[2 * i], x[2 * i + 1]);
-    *(u32x4*)((uint16_t*)base + at) = a;
+    store16<PAST>((u32x4*)((uint16_t*)base + at), a);
   }
 }
 
@@ -205,7 +219,7 @@ __device__ __forceinline__ float across(float x, int m, int mate) {
   return __shfl(x, mate, 64);
 }
 
-template <int D, int IN, int OUT>
+template <int D, int IN, int OUT, bool PAST>
 __global__ void __launch_bounds__(256) k_qk_norm_rope(NormArgs A) {
   constexpr int LPR = D / 8, RPW = 64 / LPR, U = 2;
   const int lane = threadIdx.x & 63;
@@ -220,8 +234,8 @@ __global__ void __launch_bounds__(256) k_qk_norm_rope(NormArgs A) {
   float x[U][8];
   auto load = [&](int h, float* y) {
     h = min(h, rows - 1);
-    if (h < A.hq) load8<IN>(A.q, t * A.qs + (int64_t)h * D + c0, y);
-    else load8<IN>(A.k, t * A.ks + (int64_t)(h - A.hq) * D + c0, y);
+    if (h < A.hq) load8<IN, true>(A.q, t * A.qs + (int64_t)h * D + c0, y);
+    else load8<IN, true>(A.k, t * A.ks + (int64_t)(h - A.hq) * D + c0, y);
   };
 #pragma unroll
   for (int u = 0; u < U; u++) load(first + u * step, x[u]);
@@ -288,8 +302,8 @@ __global__ void __launch_bounds__(256) k_qk_norm_rope(NormArgs A) {
       }
     }
     if (h < rows) {
-      if (h < A.hq) store8<OUT>(A.qo, t * A.qos + (int64_t)h * D + c0, y);
-      else store8<OUT>(A.ko, t * A.kos + (int64_t)(h - A.hq) * D + c0, y);
+      if (h < A.hq) store8<OUT, PAST>(A.qo, t * A.qos + (int64_t)h * D + c0, y);
+      else store8<OUT, PAST>(A.ko, t * A.kos + (int64_t)(h - A.hq) * D + c0, y);
     }
   };
   for (int h = first; h - lane / LPR < rows; h += U * step) {
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(256) k_kv_store(StoreArgs A) {
 
 // eight codes of a dword as elements: the conversion's binary16 pairs are
 // exact, and NaN for scale byte 255
-template <int TYPE>
+template <int TYPE, bool PAST>
 __device__ __forceinline__ void fetch8(uint32_t w, uint32_t sbyte, void* out, int64_t at) {
   const float sc = bits_f(sbyte << 23);
   uint32_t h[4];
@@ -415,16 +429,16 @@ __device__ __forceinline__ void fetch8(uint32_t w, uint32_t sbyte, void* out, in
   h[2] = h2_bits(__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 2)));
   h[3] = h2_bits(__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, sc, 3)));
   if constexpr (TYPE == STQ_FP16) {
-    *(u32x4*)((uint16_t*)out + at) = (u32x4){h[0], h[1], h[2], h[3]};
+    store16<PAST>((u32x4*)((uint16_t*)out + at), (u32x4){h[0], h[1], h[2], h[3]});
   } else {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = (float)as_h2(h[i >> 1])[i & 1];
-    store8<TYPE>(out, at, x);
+    store8<TYPE, PAST>(out, at, x);
   }
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool PAST>
 __global__ void __launch_bounds__(256) k_kv_fetch(StoreArgs A) {
   const StoreAt s = store_at<D>(A);
   if (!s.on) return;
@@ -439,8 +453,8 @@ __global__ void __launch_bounds__(256) k_kv_fetch(StoreArgs A) {
   const uint8_t* sc = hb + T * D + (li >> 2) * T + off;
   const uint32_t sk = sc[0], sv = sc[T * (D / 32)];
   const int64_t at = (s.t * A.heads + s.h) * D + 8 * li;
-  fetch8<TYPE>(ck, sk, A.ko, at);
-  fetch8<TYPE>(cv, sv, A.vo, at);
+  fetch8<TYPE, PAST>(ck, sk, A.ko, at);
+  fetch8<TYPE, PAST>(cv, sv, A.vo, at);
 }
 
 // ------------------------------------------------------------- attention
@@ -560,8 +574,8 @@ template <int D>
 struct Chunk {
   static constexpr int KD = D / 32;                    // dwords of keys per tile and lane
   uint32_t k[2][KD], v[8];
-  uint32_t ks[2];
-  uint32_t vs[2];
+  uint32_t ks[2];                                      // scales of tokens 8 (m / 4) + 4u .., this lane's row is number m % 4
+  uint32_t vs[2];                                      // scales of tokens 8G ..
 };
 
 // A lane's places in a chunk, the same for every chunk (bytes from the chunk's
@@ -572,7 +586,7 @@ struct Places {
   __device__ __forceinline__ explicit Places(int T) {
     const int lane = threadIdx.x & 63, m = lane & 15, G = lane >> 4, r = 8 * (m >> 2) + (m & 3);
     k = r * (D / 2) + G * (D / 8);
-    ks = (G * (D / 4) / 32) * T + r;
+    ks = (G * (D / 4) / 32) * T + 8 * (m >> 2);
     v = 8 * G * (D / 2) + m * (D / 32);
     vs = (m * (D / 16) / 32) * T + 8 * G;
   }
@@ -590,8 +604,10 @@ __device__ __forceinline__ void load_keys(Chunk<D>& C, const Places<D>& W, const
       C.k[u][0] = w[0];
       C.k[u][1] = w[1];
     }
-    C.ks[u] = scales[W.ks + 4 * u];
   }
+  const u32x2 s = *(const u32x2*)(scales + W.ks);
+  C.ks[0] = s[0];
+  C.ks[1] = s[1];
 }
 template <int D>
 __device__ __forceinline__ void load_values(Chunk<D>& C, const Places<D>& W, const uint8_t* codes, const uint8_t* scales) {
@@ -669,7 +685,7 @@ template <int D, int NT>
 __device__ __forceinline__ void key_products(const Chunk<D>& C, const f16x8 (*q)[D / 32], f32x4 (*s)[2]) {
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    const float sc = scale_of<0>(C.ks[u]);
+    const float sc = scale_of<0>(C.ks[u] >> (8 * (threadIdx.x & 3)));
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) s[nt][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -828,7 +844,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
   }
   // One set of registers for the codes: the next chunk's keys are asked for as
   // soon as this one's are unpacked, its values likewise; the other waves of
-  // the SIMD cover what that does not.
+  // the SIMD cover what that does not (a second set measured the same or worse).
   while (k < c1) {
     const int ch = chunk_at(k), t0 = ch * 32, t1 = t0 + 31;
     const bool dead = at.dead, full = !dead && t1 <= p0 && (A.window == 0 || t0 > p1 - A.window || t1 < A.sink);
@@ -1340,6 +1356,11 @@ stq_status kv_check(const stq_kv_desc* d, const void* cache, size_t bytes) {
   return STQ_OK;
 }
 int64_t kv_grid(const stq_kv_desc* d, int64_t n_tok) { return (n_tok + 2048 / d->d - 1) / (2048 / d->d) * d->n_kv_heads; }
+// The L2s of the eight dies together: a larger output cannot stay there for its
+// reader, and stored past them it leaves room and saves their write-back
+// (16,381 tokens of 40 heads normed 74.8 -> 67.8 us with loads past them as
+// well, 32,749 tokens' values read back with the write before it 39.8 -> 29.2).
+constexpr int64_t CACHE_BYTES = 32 << 20;
 bool aligned(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 int elem_bytes(int type) { return type == STQ_FP32 ? 4 : 2; }
 bool stride_ok(int64_t stride, int64_t least, int type) {
@@ -1407,32 +1428,37 @@ void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
 }
 
 constexpr int64_t NORM_WAVES = 8192;
-template <int D, int IN>
-void launch_norm(const NormArgs& A, int out, hipStream_t st) {
+template <int D, int IN, int OUT>
+void launch_norm(const NormArgs& A, bool past, hipStream_t st) {
   const dim3 g((unsigned)(((int64_t)A.n_tok * A.per_tok + 3) / 4)), b(256);
-  if (out == STQ_FP32) hipLaunchKernelGGL((k_qk_norm_rope<D, IN, STQ_FP32>), g, b, 0, st, A);
-  else hipLaunchKernelGGL((k_qk_norm_rope<D, IN, IN>), g, b, 0, st, A);
+  if (past) hipLaunchKernelGGL((k_qk_norm_rope<D, IN, OUT, true>), g, b, 0, st, A);
+  else hipLaunchKernelGGL((k_qk_norm_rope<D, IN, OUT, false>), g, b, 0, st, A);
+}
+template <int D, int IN>
+void launch_norm_out(const NormArgs& A, int out, bool past, hipStream_t st) {
+  if (out == STQ_FP32) launch_norm<D, IN, STQ_FP32>(A, past, st);
+  else launch_norm<D, IN, IN>(A, past, st);
 }
 template <int D>
-void launch_norm_in(const NormArgs& A, int in, int out, hipStream_t st) {
-  if (in == STQ_BF16) launch_norm<D, STQ_BF16>(A, out, st);
-  else if (in == STQ_FP16) launch_norm<D, STQ_FP16>(A, out, st);
-  else launch_norm<D, STQ_FP32>(A, out, st);
+void launch_norm_in(const NormArgs& A, int in, int out, bool past, hipStream_t st) {
+  if (in == STQ_BF16) launch_norm_out<D, STQ_BF16>(A, out, past, st);
+  else if (in == STQ_FP16) launch_norm_out<D, STQ_FP16>(A, out, past, st);
+  else launch_norm_out<D, STQ_FP32>(A, out, past, st);
 }
 
-template <int D>
-void launch_kv(const StoreArgs& A, int type, bool store, hipStream_t st) {
+template <int D, int TYPE>
+void launch_kv_type(const StoreArgs& A, bool store, hipStream_t st) {
   constexpr int RPB = 256 / (D / 8);
   const dim3 g((unsigned)(((int64_t)A.n_tok + RPB - 1) / RPB * A.heads)), b(256);
-  if (store) {
-    if (type == STQ_BF16) hipLaunchKernelGGL((k_kv_store<D, STQ_BF16>), g, b, 0, st, A);
-    else if (type == STQ_FP16) hipLaunchKernelGGL((k_kv_store<D, STQ_FP16>), g, b, 0, st, A);
-    else hipLaunchKernelGGL((k_kv_store<D, STQ_FP32>), g, b, 0, st, A);
-  } else {
-    if (type == STQ_BF16) hipLaunchKernelGGL((k_kv_fetch<D, STQ_BF16>), g, b, 0, st, A);
-    else if (type == STQ_FP16) hipLaunchKernelGGL((k_kv_fetch<D, STQ_FP16>), g, b, 0, st, A);
-    else hipLaunchKernelGGL((k_kv_fetch<D, STQ_FP32>), g, b, 0, st, A);
-  }
+  if (store) hipLaunchKernelGGL((k_kv_store<D, TYPE>), g, b, 0, st, A);
+  else if (2 * (int64_t)A.n_tok * A.heads * D * elem_bytes(TYPE) > CACHE_BYTES) hipLaunchKernelGGL((k_kv_fetch<D, TYPE, true>), g, b, 0, st, A);
+  else hipLaunchKernelGGL((k_kv_fetch<D, TYPE, false>), g, b, 0, st, A);
+}
+template <int D>
+void launch_kv(const StoreArgs& A, int type, bool store, hipStream_t st) {
+  if (type == STQ_BF16) launch_kv_type<D, STQ_BF16>(A, store, st);
+  else if (type == STQ_FP16) launch_kv_type<D, STQ_FP16>(A, store, st);
+  else launch_kv_type<D, STQ_FP32>(A, store, st);
 }
 
 }  // namespace
@@ -1488,14 +1514,15 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   A.n_tok = d->n_tok; A.hq = d->n_q_heads; A.hk = d->n_k_heads; A.n_rot = d->n_rot; A.n_pos = d->n_pos; A.norm = d->norm;
   A.adjacent = d->rot_pairs == STQ_ROT_ADJACENT; A.eps = d->eps;
   A.qs = d->q_stride; A.ks = d->k_stride; A.qos = d->q_out_stride; A.kos = d->k_out_stride;
+  const bool past = (int64_t)A.n_tok * (A.hq + A.hk) * d->d * elem_bytes(d->out_type) > CACHE_BYTES;
   // waves of one token: as many as fill the card, each with two sets of rows at least
   const int sets = (A.hq + A.hk + 512 / d->d - 1) / (512 / d->d);
   A.per_tok = (int)((NORM_WAVES + A.n_tok - 1) / A.n_tok);
   if (A.per_tok > (sets + 1) / 2) A.per_tok = (sets + 1) / 2;
   if ((int64_t)A.n_tok * A.per_tok > INT32_MAX) A.per_tok = 1;
-  if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, st);
-  else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, st);
-  else launch_norm_in<256>(A, d->in_type, d->out_type, st);
+  if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, past, st);
+  else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, past, st);
+  else launch_norm_in<256>(A, d->in_type, d->out_type, past, st);
   return launched();
 }
 
