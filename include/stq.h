@@ -472,7 +472,7 @@ stq_status stq_kv_plan(int32_t n, const int32_t* cached_dev, const int32_t* new_
  * stq_prefill.  Heads of one token are contiguous ([n_heads][d]); tokens are
  * *_stride elements apart. */
 typedef struct stq_norm_desc {
-  int32_t n_tok;            /* >= 0                                           */
+  int32_t n_tok;            /* 0 .. 2^28                                      */
   int32_t n_q_heads;        /* >= 1                                           */
   int32_t n_k_heads;        /* >= 0 (0: no keys, k pointers unused)           */
   int32_t d;                /* 64, 128 or 256                                 */
@@ -491,7 +491,7 @@ typedef struct stq_norm_desc {
  * cosines, then the n_rot/2 sines; pair (x, y) becomes (x cos - y sin,
  * y cos + x sin).  Rows of a token whose position lies outside [0, n_pos)
  * (a padded batch) are left as they were.  Outputs may be the inputs
- * themselves (same pointer, type and stride).  Pointers 16-byte aligned,
+ * themselves (same pointer, type and stride), else they must not overlap them.  Pointers 16-byte aligned,
  * strides a multiple of 16 bytes, else STQ_ERR_LAYOUT. */
 stq_status stq_qk_norm_rope(const stq_norm_desc* desc, const void* q_dev, const void* k_dev,
                             const float* q_weight_dev, const float* k_weight_dev, const int32_t* pos_dev,
@@ -520,8 +520,8 @@ stq_status stq_kv_fetch(const stq_kv_desc* desc, const void* cache_dev, size_t b
  *   head h / (n_heads / n_kv_heads); a query that sees nothing gets 0. */
 typedef struct stq_attend_desc {
   int32_t n_req;            /* requests (>= 0)                                */
-  int32_t n_tok;            /* rows of q and o (a padded batch may have more   */
-                            /* than tok_start[n_req]; those are left alone)   */
+  int32_t n_tok;            /* rows of q and o, 0 .. 2^28 (a padded batch may   */
+                            /* have more than tok_start[n_req]: left alone)   */
   int32_t n_heads;          /* a multiple of n_kv_heads                       */
   int32_t type;             /* of q and o: STQ_BF16 or STQ_FP16               */
   int32_t table_cols;       /* columns of the block table                     */

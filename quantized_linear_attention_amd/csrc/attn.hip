@@ -83,6 +83,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float* x) {
 
 // ------------------------------------------------------------ block plan
 //
+// Latency bound: a chain of one read of the counts, the scans, a search and the
+// writes (64 requests of one token 4.1 us, 512 requests with 33,000 tokens 6.3
+// us, of which a launch alone takes 2).
 // Every workgroup scans all n requests by itself (8 n bytes from the L2 and
 // two scans in LDS), so the plan needs one launch and no traffic between
 // workgroups; then the new table entries and the new tokens are dealt out
@@ -152,7 +155,8 @@ __global__ void __launch_bounds__(PLAN_NT) k_kv_plan(PlanArgs A) {
   const uint32_t step = gridDim.x * PLAN_NT, first = blockIdx.x * PLAN_NT + tid;
   for (uint32_t i = first; i <= (uint32_t)n; i += step) A.tok_start[i] = (int32_t)tok0[i];
   if (blockIdx.x == 0 && tid == 0) A.used[0] = (int32_t)run_b;
-  for (uint32_t u = first; u < run_b; u += step) {
+  for (uint64_t v = first; v < run_b; v += step) {       // (64 bits: garbage counts must not keep it going)
+    const uint32_t u = (uint32_t)v;
     const int i = owner(blk0, n, u);
     const int have = (int)(((int64_t)max(A.cached[i], 0) + T - 1) / T);
     const int64_t col = (int64_t)have + (u - blk0[i]);
@@ -187,6 +191,8 @@ __global__ void __launch_bounds__(PLAN_NT) k_kv_plan(PlanArgs A) {
 // rows are under way at once.  A rotation's other half of a pair comes from
 // another lane by DPP (through LDS, as __shfl goes, the exchange alone took
 // longer than the memory: 137 us for 16,381 tokens of 40 heads).
+// Memory bound: those 16,381 tokens take 67 us, 5.0 TB/s read and written (a
+// copy of 1 GiB runs at 5.16); 64 tokens 4.7 us.
 struct NormArgs {
   const void *q, *k;
   void *qo, *ko;
@@ -357,6 +363,10 @@ __device__ __forceinline__ uint32_t codes8(const float* x, int* e_out) {
   return w;
 }
 
+// Memory bound: 32,749 tokens of 8 heads at d = 64 written from binary16 and
+// read back as bfloat16 take 29 us for 170 MB (the codes in between stay in
+// the caches), 512 tokens 4.5 us in two launches.
+//
 // One (token, head) on D/8 lanes, keys and values together (the NaN rule needs
 // both).  A workgroup takes consecutive tokens of one head, whose codes and
 // scales lie side by side where the slots do; the heads come fastest, so that
@@ -657,7 +667,7 @@ struct Ref {
   }
 };
 
-// acc *= f for the 16 registers from V%c[r] on, where any lane of `far` is set.
+// x *= f for `count` registers from V`first` on, where any lane of `far` is set.
 // The branch lies inside the statement and the accumulators at registers of
 // their own: as an `if` around the products, the compiler kept the two sides'
 // accumulators apart and copied one to the other in every step, which costs as
@@ -736,6 +746,12 @@ __device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, con
 // one (request, head, tile of 16 NT rows, split of the cache); its NWV
 // waves take every NWV-th chunk straight from memory into the operands'
 // registers and join their running softmaxes through LDS at the end.
+// Measured (32 heads over 8, d = 128, one token): 8 requests of 32,768 to
+// 131,072 tokens 164 us for 777 MB of codes and scales = 4.7 TB/s (loads alone
+// 161); 64 of 2,048 to 8,191 tokens 80 us = 4.6 TB/s (loads alone 74, work on
+// resident data 57: the two overlap but for the waits inside a wave); one of
+// 1,021 tokens 9.4 us.  Three tokens of 8 heads each over windows of 1,024 at d
+// = 64, 128 requests: 17.5 us, bound by the instructions of two waves a SIMD.
 // o *= f of tile nt where any lane of `far` is set (accumulators of 16 rows and
 // D channels: D/4 registers)
 template <int D, int NT>
@@ -967,6 +983,15 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
 // over 16 tokens; the values meet it through ds_read_tr16_b64, which gives
 // lane i of 16 lanes channel i of four tokens whose 16-channel rows the lanes
 // address (lane 4t + c: channels 4c.. of token t).
+//
+// Measured (4 prompts of 1,078 to 2,048 tokens over up to 2,048 cached ones, 32
+// heads over 8, d = 128): 231 us = 926 TFLOP/s, where a library product of
+// 8,192 x 8,192 x 8,192 in binary16 runs at 1,150.  A tile costs a wave about
+// 1,000 cycles of matrix instructions and as many of vector ones (32 exp2 at
+// half rate, the conversions, the sums), which share the SIMD's issue with the
+// other wave's; 256 registers allow two.  (Eight waves over 256 rows, one
+// workgroup a CU: 441 us, its waves wait for each other in step; products one
+// chunk ahead instead of a tile: 268 against 253.)
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __fp16 fp16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) fp16x4 lds_fp16x4;
@@ -1369,20 +1394,26 @@ bool stride_ok(int64_t stride, int64_t least, int type) {
 stq_status launched() { return hipGetLastError() == hipSuccess ? STQ_OK : STQ_ERR_HIP; }
 
 bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
-  return a && a->n_req >= 0 && a->n_tok >= 0 && a->n_heads >= 1 && a->n_heads % d->n_kv_heads == 0 &&
+  return a && a->n_req >= 0 && a->n_tok >= 0 && a->n_tok <= (1 << 28) && a->n_heads >= 1 && a->n_heads % d->n_kv_heads == 0 &&
          a->n_heads <= 65536 && (a->type == STQ_BF16 || a->type == STQ_FP16) && a->table_cols >= 1 &&
          (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
          a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
 }
 struct Split { int tiles, tile_rows, splits, per, waves; bool staged; };
-// Query rows per key/value head from which the cache is staged through LDS.
+// Query rows per key/value head up to which each wave unpacks the cache for
+// itself, 32 rows at a time; above, it is staged through LDS for 128 rows (16
+// requests of up to 8,192 tokens, 8 heads: 36 rows 43 against 89 us staged, 64
+// rows 62 against 95, 128 rows 99 staged alike; 64 requests of up to 2,048:
+// 64 rows 54 against 63, 96 rows 67 against 62, 128 rows 84 against 67).
 constexpr int STAGED_ROWS = 64;
 // A part of a request's work has its own start (three dependent loads) and end
 // (the joins), about 5 us.  Few workgroups are split down to 8 chunks until
 // every CU holds three; many only into parts of 48 chunks and up, which even
-// out ragged lengths (64 requests of 2,048 to 8,191 tokens, 8 heads: 83.1 us
-// whole, 78.3 in parts of 48 chunks, 85 in parts of 128, 91 in parts of 24).
-constexpr int64_t CUS = 256, FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 3072, MANY_CHUNKS = 48, MOST_SPLITS = 128;
+// out ragged lengths, and until every CU has eight of them (64 requests of 2,048
+// to 8,191 tokens, 8 heads: 83 us whole, 85 in parts of 128 chunks, 80 in parts
+// of 64, 80 of 48, 91 of 24; 8 requests of 32,768 to 131,072 tokens: 171 us at
+// six workgroups a CU, 164 at eight, 167 at ten, 169 at sixteen).
+constexpr int64_t CUS = 256, FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
   const int64_t rows = (int64_t)a->max_new * (a->n_heads / d->n_kv_heads);
@@ -1487,7 +1518,7 @@ stq_status stq_kv_plan(int32_t n, const int32_t* cached, const int32_t* fresh, c
 
 stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k, const float* wq, const float* wk,
                             const int32_t* pos, const float* cos_sin, void* qo, void* ko, hipStream_t st) {
-  if (!d || d->n_tok < 0 || d->n_q_heads < 1 || d->n_k_heads < 0 || d->n_q_heads > 65536 || d->n_k_heads > 65536)
+  if (!d || d->n_tok < 0 || d->n_tok > (1 << 28) || d->n_q_heads < 1 || d->n_k_heads < 0 || d->n_q_heads > 65536 || d->n_k_heads > 65536)
     return STQ_ERR_ARG;
   if (d->d != 64 && d->d != 128 && d->d != 256) return STQ_ERR_ARG;
   if (d->in_type < STQ_BF16 || d->in_type > STQ_FP32) return STQ_ERR_ARG;
@@ -1519,7 +1550,6 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   const int sets = (A.hq + A.hk + 512 / d->d - 1) / (512 / d->d);
   A.per_tok = (int)((NORM_WAVES + A.n_tok - 1) / A.n_tok);
   if (A.per_tok > (sets + 1) / 2) A.per_tok = (sets + 1) / 2;
-  if ((int64_t)A.n_tok * A.per_tok > INT32_MAX) A.per_tok = 1;
   if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, past, st);
   else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, past, st);
   else launch_norm_in<256>(A, d->in_type, d->out_type, past, st);

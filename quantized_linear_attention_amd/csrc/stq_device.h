@@ -1,6 +1,6 @@
 // stq_device.h — gfx950 device building blocks of the decode-step kernels:
 // tile geometry, lane-stream unpack/pack, cross-lane reductions and the
-// binary32 format helpers of the refit.  Included by stq.hip only.
+// binary32 format helpers of the refit.  Included by stq.hip and attn.hip.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

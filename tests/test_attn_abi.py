@@ -70,7 +70,7 @@ def test_norm_refusals(L):
         p = dict(q=D, k=D, wq=None, wk=None, pos=D, cs=D, qo=P(0x20000), ko=P(0x30000))
         p.update(null)
         return L.stq_qk_norm_rope(ctypes.byref(d), p["q"], p["k"], p["wq"], p["wk"], p["pos"], p["cs"], p["qo"], p["ko"], None)
-    for kw in (dict(n_tok=-1), dict(n_q_heads=0), dict(n_k_heads=-1), dict(d=96), dict(d=32), dict(in_type=3), dict(out_type=1),
+    for kw in (dict(n_tok=-1), dict(n_tok=(1 << 28) + 1), dict(n_q_heads=0), dict(n_k_heads=-1), dict(d=96), dict(d=32), dict(in_type=3), dict(out_type=1),
                dict(in_type=2, out_type=0), dict(norm=3), dict(norm=-1), dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")),
                dict(eps=float("inf")), dict(n_rot=8), dict(n_rot=-16), dict(n_rot=144), dict(rot_pairs=2), dict(n_pos=0)):
         assert call(nd(**kw)) == -1, kw
@@ -120,7 +120,7 @@ def test_attend_refusals(L):
         a = ad() if a is None else a
         return L.stq_kv_attend(ctypes.byref(d), p["cache"], size, ctypes.byref(a), p["table"], p["tok"], p["len"], p["q"],
                                p["o"], work, wbytes, None)
-    for kw in (dict(n_req=-1), dict(n_tok=-1), dict(n_heads=0), dict(n_heads=3), dict(n_heads=-2), dict(type=2), dict(type=-1),
+    for kw in (dict(n_req=-1), dict(n_tok=-1), dict(n_tok=(1 << 28) + 1), dict(n_heads=0), dict(n_heads=3), dict(n_heads=-2), dict(type=2), dict(type=-1),
                dict(table_cols=0), dict(table_cols=1 << 25), dict(max_new=0), dict(max_len=0), dict(window=-1), dict(n_sink=-1),
                dict(scale=float("inf")), dict(scale=float("nan"))):
         assert call(ad(**kw)) == -1, kw

@@ -354,6 +354,109 @@ def test_attend_split(stq, lens, news):
     B.check(B.run(window=1500, sink=10), 1500, 10)
 
 
+@pytest.mark.parametrize("news", [1, 3, 30])
+def test_attend_split_narrow_heads(stq, news):
+    """The same at d = 64, one request's length far above the stated longest."""
+    B = Batch(stq, [3333, 900, 2500], [news] * 3, 6, 1, 64, 128, "bf16", seed=news)
+    for hint in (None, 1100):
+        B.check(B.run(max_len=hint))
+
+
+@pytest.mark.parametrize("news", [30, 70])
+def test_attend_many_requests(stq, news):
+    """More requests than the order of the prompts' tiles is worked out for; new
+    tokens and lengths ragged, some requests without any."""
+    rng = np.random.default_rng(news)
+    new = rng.integers(0, news + 1, 67)
+    new[5], new[66], new[11] = news, news, 0
+    B = Batch(stq, new + rng.integers(0, 60, 67), new, 3, 1, 64, 32, "bf16", seed=news, pad=4)
+    B.check(B.run())
+
+
+def test_attend_head_groups_larger_than_a_tile(stq):
+    """160 query heads of one key/value head: a token's rows fill more than one tile."""
+    B = Batch(stq, [300, 45, 0], [3, 1, 1], 160, 1, 64, 32, "bf16", seed=5, pad=1)
+    B.check(B.run())
+
+
+def test_attend_order_of_ragged_prompts(stq):
+    """Up to 64 requests: every tile of every request, whatever their number and
+    lengths (bands that no request's tile lies in, requests without new tokens)."""
+    rng = np.random.default_rng(7)
+    for n in (1, 2, 5, 23, 64):
+        new = rng.integers(0, 200 if n < 10 else 50, n)
+        new[-1] = 131
+        old = rng.integers(0, 40, n)
+        old[n // 2] += 900
+        B = Batch(stq, new + old, new, 2, 1, 64, 64, "fp16", seed=n, pad=1)
+        B.check(B.run(window=70, sink=3), 70, 3)
+
+
+def test_offsets_past_32_bits(stq):
+    """Blocks whose bytes lie past 4 GiB hold what blocks at the front hold."""
+    import torch
+    T, heads, d = 256, 8, 128
+    one = stq.stq_kv_bytes(1, T, heads, d)
+    n_blocks = (9 << 29) // one                              # 4.5 GiB
+    pages = torch.empty(n_blocks * one, dtype=torch.uint8, device="cuda")
+    kv = stq.make_kv(pages, T, heads, d)
+    assert kv.desc.n_blocks == n_blocks
+    rng = np.random.default_rng(2)
+    L = 700
+    k, v = rnd(rng, (L, heads, d), "bf16"), rnd(rng, (L, heads, d), "bf16")
+    q = rnd(rng, (L, 16, d), "bf16")
+    outs = []
+    for first in (0, n_blocks - 3):
+        t = np.arange(L)
+        slots = cu((first + t // T) * T + t % T)
+        stq.stq_kv_store(kv, slots, k, v)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        stq.stq_kv_fetch(kv, slots, ko, vo)
+        got = [ko, vo]
+        for new in (1, 3, 300):
+            i = torch.int32
+            o = torch.empty(new, 16, d, dtype=q.dtype, device="cuda")
+            size = stq.stq_kv_attend_bytes(kv, 1, new, 16, new, L)
+            stq.stq_kv_attend(kv, cu(np.arange(3)[None] + first, i), cu([0, new], i), cu([L], i), q[:new], o, d ** -0.5, new, L,
+                              work=torch.empty(size, dtype=torch.uint8, device="cuda") if size else None)
+            got.append(o)
+        torch.cuda.synchronize()
+        outs.append(got)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_large_outputs(stq):
+    """Outputs larger than the caches take other stores: the same values as calls
+    on slices of the tokens, which do not."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(4)
+    n, heads, kv, d = 4500, 32, 4, 128
+    both = torch.randn(n, heads + kv, d, device="cuda", generator=g).bfloat16()
+    q, k = both[:, :heads], both[:, heads:]
+    table = cu(cos_sin(2048, 64))
+    pos = torch.randint(0, 2048, (n,), device="cuda", generator=g).to(torch.int32)
+    for dt in (torch.bfloat16, torch.float32):
+        whole = [torch.empty(n, heads, d, dtype=dt, device="cuda"), torch.empty(n, kv, d, dtype=dt, device="cuda")]
+        parts = [torch.empty_like(x) for x in whole]
+        stq.stq_qk_norm_rope(q, k, *whole, pos=pos, cos_sin=table)
+        for a in range(0, n, 500):
+            s = slice(a, a + 500)
+            stq.stq_qk_norm_rope(q[s], k[s], parts[0][s], parts[1][s], pos=pos[s], cos_sin=table)
+        assert all(torch.equal(a, b) for a, b in zip(whole, parts))
+    cache = stq.make_kv(torch.empty(stq.stq_kv_bytes(300, 64, 8, d), dtype=torch.uint8, device="cuda"), 64, 8, d)
+    m = 19000
+    kk, vv = (torch.randn(m, 8, d, device="cuda", generator=g).half() for _ in range(2))
+    slots = torch.randperm(300 * 64, device="cuda", generator=g)[:m].contiguous()
+    stq.stq_kv_store(cache, slots, kk, vv)
+    whole, parts = [torch.empty_like(kk) for _ in range(2)], [torch.empty_like(kk) for _ in range(2)]
+    stq.stq_kv_fetch(cache, slots, *whole)
+    for a in range(0, m, 1000):
+        s = slice(a, a + 1000)
+        stq.stq_kv_fetch(cache, slots[s], parts[0][s], parts[1][s])
+    assert all(torch.equal(a, b) for a, b in zip(whole, parts))
+
+
 def test_attend_scale_and_large_queries(stq):
     """Negative, zero and large scales; queries far outside binary16's range and
     far below it; rows of zeros."""
