@@ -349,7 +349,7 @@ def _heads(t, what, n, heads, d, index):
     st, sh, sc = t.stride()
     if sc != 1 or (b > 1 and sh != c):
         raise StqError(-1, "%s: the heads of a token must be contiguous" % what)
-    return t.data_ptr(), st if a > 1 and st > b * c else b * c
+    return t.data_ptr(), st if a > 1 else b * c     # one shorter than a token is the library's to refuse
 
 
 def _i32(*sizes):

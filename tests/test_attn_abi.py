@@ -238,3 +238,20 @@ def test_binding_refusals(stq, monkeypatch):
         args.update(bad)
         with pytest.raises(E):
             stq.stq_kv_plan(stream=0, **args)
+
+
+def test_binding_passes_short_strides_on(stq, monkeypatch):
+    """Tokens that overlap (one row expanded over the batch) keep their stride, which the library refuses."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    b, i, l, u = torch.bfloat16, torch.int32, torch.int64, torch.uint8
+    kv = stq.make_kv(Fake([10 * 2 * 64 * 136], u), 64, 2, 128)
+    good, flat = Fake([4, 2, 128], b), Fake([4, 2, 128], b, stride=(0, 128, 1))
+    calls = [lambda x, y: stq.stq_kv_store(kv, Fake([4], l), x, y, stream=0),
+             lambda x, y: stq.stq_kv_attend(kv, Fake([2, 5], i), Fake([3], i), Fake([2], i), x, y, 0.1, 2, 100, stream=0),
+             lambda x, y: stq.stq_qk_norm_rope(x, None, y, None, stream=0)]
+    for call in calls:
+        for x, y in ((flat, good), (good, flat)):
+            with pytest.raises(stq.StqError) as e:
+                call(x, y)
+            assert e.value.status in (-1, -2)       # before any launch
