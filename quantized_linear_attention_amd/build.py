@@ -1,13 +1,16 @@
-"""Build the gfx950 HIP library in-tree: quantized_linear_attention_amd/libstq.so."""
+"""Build the gfx950 HIP library in-tree: quantized_linear_attention_amd/libstq.so,
+and the binding's compiled checks beside it, _tensor.so."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = [os.path.join(PKG, "csrc", f) for f in ("stq.hip", "attn.hip", "alloc.cpp")]
 DEPS = SRC + [os.path.join(PKG, "csrc", "stq_device.h"), os.path.join(ROOT, "include", "stq.h")]
 LIB = os.path.join(PKG, "libstq.so")
+TENSOR_SRC, TENSOR_LIB = os.path.join(PKG, "csrc", "tensor.cpp"), os.path.join(PKG, "_tensor.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -20,19 +23,31 @@ FLAGS = [
 ]
 
 
-def build(force=True, verbose=False):
-    """Compile libstq.so (always when force=True)."""
-    if not force and os.path.exists(LIB) and all(os.path.getmtime(LIB) >= os.path.getmtime(d) for d in DEPS):
-        return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC] + FLAGS + SRC + ["-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _run(cmd, out, verbose):
+    tmp = out + ".tmp%d" % os.getpid()
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed (%d)" % r.returncode)
+        raise RuntimeError("%s failed (%d)" % (os.path.basename(cmd[0]), r.returncode))
     if verbose:
         sys.stderr.write(r.stderr)
-    os.replace(tmp, LIB)
+    os.replace(tmp, out)
+
+
+def _current(out, deps):
+    return os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in deps)
+
+
+def build(force=True, verbose=False):
+    """Compile libstq.so and _tensor.so (always when force=True)."""
+    if force or not _current(TENSOR_LIB, [TENSOR_SRC]):
+        from torch.utils.cpp_extension import include_paths, library_paths
+        inc = include_paths() + [sysconfig.get_paths()["include"]]
+        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared"] + ["-I" + d for d in inc] +
+             [TENSOR_SRC] + ["-L" + d for d in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"],
+             TENSOR_LIB, verbose)
+    if force or not _current(LIB, DEPS):
+        _run([HIPCC] + FLAGS + SRC, LIB, verbose)
     return LIB
 
 

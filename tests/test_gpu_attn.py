@@ -692,3 +692,33 @@ def test_two_streams(stq):
             want = ls[0].o.clone()
         for x in ls:
             assert torch.equal(x.o, want)
+
+
+def test_tensor_checks(stq):
+    """The compiled checks pass what the calls take and nothing else (the refusals' words are Python's)."""
+    import torch
+    from quantized_linear_attention_amd import _tensor
+    f, i = torch.float32, torch.int32
+    t = torch.zeros(5, 6, 64, device="cuda")
+    assert _tensor.address(t, f, t.numel(), 0) == t.data_ptr()
+    cpu, wide = torch.zeros(5, 6, 64), torch.zeros(5, 10, 64, device="cuda")
+    for x, ty, n, dev in ((t, i, t.numel(), 0), (t, f, 7, 0), (t, f, t.numel(), 1), (cpu, f, t.numel(), 0), (cpu, f, t.numel(), -1),
+                          (t.transpose(0, 1), f, t.numel(), 0), (None, f, 0, 0), (3, f, 0, 0), (t, "f", t.numel(), 0), (t, f, 2 ** 70, 0),
+                          (t, f, None, 0)):
+        assert _tensor.address(x, ty, n, dev) is None
+    part = wide[:, 2:8]
+    assert _tensor.rows(part, 5, 6, 64, 0) == _tensor.rows(part, None, None, None, None) == (part.data_ptr(), 640)
+    assert _tensor.rows(t[:1], 1, 6, 64, 0) == (t.data_ptr(), 384)
+    assert _tensor.rows(t[0:1].expand(5, 6, 64), 5, 6, 64, 0) == (t.data_ptr(), 0)
+    for x, want in ((part, (4, 6, 64, 0)), (part, (5, 5, 64, 0)), (part, (5, 6, 32, 0)), (part, (5, 6, 64, 1)), (part, (5, 6, 64, -1)),
+                    (wide[:, ::2], (None,) * 4), (wide[..., ::2], (None,) * 4), (t[0], (None,) * 4), (cpu, (None,) * 4),
+                    (None, (None,) * 4), (t, ("5", None, None, None))):
+        assert _tensor.rows(x, *want) is None
+    q, o = torch.zeros(3, 4, 64, device="cuda").bfloat16(), torch.zeros(3, 4, 64, device="cuda").bfloat16()
+    kv = stq.make_kv(torch.zeros(stq.stq_kv_bytes(2, 32, 2, 64), dtype=torch.uint8, device="cuda"), 32, 2, 64)
+    ok = dict(table=torch.zeros(1, 2, dtype=i, device="cuda"), tok_start=torch.zeros(2, dtype=i, device="cuda"),
+              lens=torch.zeros(1, dtype=i, device="cuda"), q=q, o=o)
+    for bad in (dict(table=ok["table"].long()), dict(tok_start=ok["lens"]), dict(lens=ok["lens"].cpu()), dict(q=q.float()), dict(o=o.half()),
+                dict(o=o[:2]), dict(q=q.cpu()), dict(q=q[:, :, :32]), dict(q=q[:1].expand(3, 4, 64)), dict(work=torch.zeros(8, device="cuda"))):
+        with pytest.raises(stq.StqError):
+            stq.stq_kv_attend(kv, **dict(ok, **bad), scale=1.0, max_new=3, max_len=3)
