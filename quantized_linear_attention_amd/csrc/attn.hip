@@ -985,7 +985,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
 // address (lane 4t + c: channels 4c.. of token t).
 //
 // Measured (4 prompts of 1,078 to 2,048 tokens over up to 2,048 cached ones, 32
-// heads over 8, d = 128): 231 us = 926 TFLOP/s, where a library product of
+// heads over 8, d = 128): 230 us = 930 TFLOP/s, where a library product of
 // 8,192 x 8,192 x 8,192 in binary16 runs at 1,150.  A tile costs a wave about
 // 1,000 cycles of matrix instructions and as many of vector ones (32 exp2 at
 // half rate, the conversions, the sums), which share the SIMD's issue with the
@@ -997,8 +997,8 @@ typedef __fp16 fp16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) fp16x4 lds_fp16x4;
 
 // 16-byte slot of (token t of 64, channels 8c ..).  The channel part is xored
-// with bits of the token so that the 16 lanes of a read or write phase touch
-// 16 different slots of the banks; as xors the places of a lane's other
+// with bits of the token so that the 16 lanes of a read phase touch 16 different
+// slots of the banks (a write phase is eight lanes: see `tk`); as xors the places of a lane's other
 // channels are its first place with constant bits turned.
 template <int D>
 __device__ __forceinline__ int k_slot(int t, int c) {
@@ -1118,12 +1118,17 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
   const int T = A.T, blk_shift = 31 - __builtin_clz(T) - 5;
   auto chunk_at = [&](int k) { return k < sn.n_low ? k : sn.lo + k - sn.n_low; };
   // This thread's piece of a tile's keys and of its values: a quarter of a
-  // token's codes; waves 0 and 1 chunk k's, 2 and 3 chunk k + 1's.  Keys: the
-  // pieces of a token side by side; values: tokens side by side (what the
-  // slots' xors want).
+  // token's codes; waves 0 and 1 chunk k's, 2 and 3 chunk k + 1's, 16 tokens
+  // each.  Which lane takes which piece is chosen so that eight lanes in turn,
+  // which a 16-byte write to LDS serves at once, meet eight different slots of
+  // the banks' 128 bytes (tokens or pieces in order: two-way conflicts, 13 % of
+  // the LDS' time).
   constexpr int PS = D / 32;                           // dwords, and slots, of a piece
-  const int half = wave >> 1, w128 = tid & 127;
-  const int tk = w128 >> 2, ck = w128 & 3, tv = w128 & 31, cv = w128 >> 5;
+  const int half = wave >> 1;
+  auto bit = [&](int x) { return (lane >> x) & 1; };
+  const int ck = D == 128 ? bit(0) + 2 * bit(3) : bit(0) + 2 * bit(1), cv = ck;
+  const int tk = 16 * (wave & 1) + 8 * bit(5) + 4 * bit(4) + (D == 128 ? 2 * bit(2) + bit(1) : 2 * bit(2) + bit(3));
+  const int tv = 16 * (wave & 1) + (D == 128 ? 8 * bit(2) + 4 * bit(1) + 2 * bit(5) + bit(4) : 8 * bit(5) + 4 * bit(2) + 2 * bit(4) + bit(3));
   const uint32_t kc_at = tk * (D / 2) + 4 * PS * ck, ks_at = T * D + (PS * ck / 4) * T + tk;
   const uint32_t vc_at = T * (D / 2) + tv * (D / 2) + 4 * PS * cv, vs_at = T * D + T * (D / 32) + (PS * cv / 4) * T + tv;
   const uint32_t k_put = 16 * k_slot<D>(32 * half + tk, PS * ck), v_put = 16 * v_slot<D>(32 * half + tv, PS * cv);
