@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <type_traits>
 #include <string.h>
 
 #include "stq.h"
@@ -574,18 +575,29 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, int64_t at, f16x8* q, 
   *c = q_factor(A.scale_log2, e);
 }
 
-// One chunk (32 cached tokens of one head) as a wave loads it.  Token 8G' + i
-// (i < 4) is row 4G' + i of key tile 0, token 8G' + 4 + i that row of tile 1:
-// the two tiles' products then leave lane group G with the eight tokens
-// 8G .. 8G+7 of its query row, which is the operand that the product with
-// the values wants.  Keys: lane (m, G) holds the channels (D/4) G .. of row m.
-// Values: lane (m, G) holds the channels (D/16) m .. of tokens 8G .. 8G+7.
+// One chunk (32 cached tokens of one head) as a wave loads it.  Element e of
+// lane group G stands for token token_of(G, e): row 4G + e % 4 of key tile e / 4,
+// so that the two tiles' products leave lane group G with the eight tokens of
+// its query row that the product with the values wants from it.  At D = 128
+// the tokens of a lane group are every other one, so that each load covers
+// whole 128-byte lines (two tokens' codes) and may pass the caches by: 8
+// requests of 32,768 to 131,072 tokens 164 us, 148 so, 161 past the caches with
+// half lines.  At D = 64 eight tokens in turn are faster (64 requests of 2,048
+// to 8,191 tokens: 51.6 us, 56 with four groups' tokens side by side).
+template <int D>
+__host__ __device__ constexpr int token_of(int G, int e) {
+  return D == 128 ? 16 * (G >> 1) + 2 * e + (G & 1) : 8 * G + e;
+}
+// Keys: lane (m, G) holds the channels (D/4) G .. of row m.  Values: lane (m,
+// G) holds the channels (D/16) m .. of its group's tokens.
 template <int D>
 struct Chunk {
   static constexpr int KD = D / 32;                    // dwords of keys per tile and lane
+  static constexpr int VS = D == 128 ? 4 : 2;          // dwords of scales from the group's first token on
+  static constexpr int STEP = token_of<D>(0, 1);       // tokens from one element to the next
   uint32_t k[2][KD], v[8];
-  uint32_t ks[2];                                      // scales of tokens 8 (m / 4) + 4u .., this lane's row is number m % 4
-  uint32_t vs[2];                                      // scales of tokens 8G ..
+  uint32_t ks[2];                                      // the scale of this lane's row is byte token_of % 4
+  uint32_t vs[VS];
 };
 
 // A lane's places in a chunk, the same for every chunk (bytes from the chunk's
@@ -594,41 +606,47 @@ template <int D>
 struct Places {
   uint32_t k, v, ks, vs;
   __device__ __forceinline__ explicit Places(int T) {
-    const int lane = threadIdx.x & 63, m = lane & 15, G = lane >> 4, r = 8 * (m >> 2) + (m & 3);
+    const int lane = threadIdx.x & 63, m = lane & 15, G = lane >> 4, r = token_of<D>(m >> 2, m & 3);
     k = r * (D / 2) + G * (D / 8);
-    ks = (G * (D / 4) / 32) * T + 8 * (m >> 2);
-    v = 8 * G * (D / 2) + m * (D / 32);
-    vs = (m * (D / 16) / 32) * T + 8 * G;
+    ks = (G * (D / 4) / 32) * T + (r & ~3);
+    v = token_of<D>(G, 0) * (D / 2) + m * (D / 32);
+    vs = (m * (D / 16) / 32) * T + (token_of<D>(G, 0) & ~7);
   }
 };
-template <int D>
+template <int D, bool ONCE>
 __device__ __forceinline__ void load_keys(Chunk<D>& C, const Places<D>& W, const uint8_t* codes, const uint8_t* scales) {
 #pragma unroll
   for (int u = 0; u < 2; u++) {
+    const int t = 4 * Chunk<D>::STEP * u;
     if constexpr (D == 128) {
-      const u32x4 w = *(const u32x4*)(codes + (W.k + 4 * u * (D / 2)));
+      const u32x4 w = load16<ONCE>((const u32x4*)(codes + (W.k + t * (D / 2))));
 #pragma unroll
       for (int i = 0; i < 4; i++) C.k[u][i] = w[i];
     } else {
-      const u32x2 w = *(const u32x2*)(codes + (W.k + 4 * u * (D / 2)));
+      const u32x2 w = load16<ONCE>((const u32x2*)(codes + (W.k + t * (D / 2))));
       C.k[u][0] = w[0];
       C.k[u][1] = w[1];
     }
+    C.ks[u] = *(const uint32_t*)(scales + (W.ks + t));
   }
-  const u32x2 s = *(const u32x2*)(scales + W.ks);
-  C.ks[0] = s[0];
-  C.ks[1] = s[1];
 }
-template <int D>
+template <int D, bool ONCE>
 __device__ __forceinline__ void load_values(Chunk<D>& C, const Places<D>& W, const uint8_t* codes, const uint8_t* scales) {
 #pragma unroll
   for (int j = 0; j < 8; j++) {
-    if constexpr (D == 128) C.v[j] = *(const uint32_t*)(codes + (W.v + j * (D / 2)));
-    else C.v[j] = *(const uint16_t*)(codes + (W.v + j * (D / 2)));
+    const uint8_t* p = codes + (W.v + Chunk<D>::STEP * j * (D / 2));
+    if constexpr (D == 128) C.v[j] = load16<ONCE>((const uint32_t*)p);
+    else C.v[j] = load16<ONCE>((const uint16_t*)p);
   }
-  const u32x2 s = *(const u32x2*)(scales + W.vs);
-  C.vs[0] = s[0];
-  C.vs[1] = s[1];
+  if constexpr (D == 128) {
+    const u32x4 s = *(const u32x4*)(scales + W.vs);
+#pragma unroll
+    for (int i = 0; i < 4; i++) C.vs[i] = s[i];
+  } else {
+    const u32x2 s = *(const u32x2*)(scales + W.vs);
+    C.vs[0] = s[0];
+    C.vs[1] = s[1];
+  }
 }
 
 // Scale byte j of a dword where v_cvt_scalef32_* takes a scale: in the
@@ -690,12 +708,12 @@ __device__ __forceinline__ f16x2 weights(float a, float b) {
   else return (f16x2){(f16)a, (f16)b};
 }
 
-// Keys of a chunk and queries -> products s (tile u: tokens 8G + 4u ..).
+// Keys of a chunk and queries -> products s (tile u: elements 4u ..).
 template <int D, int NT>
 __device__ __forceinline__ void key_products(const Chunk<D>& C, const f16x8 (*q)[D / 32], f32x4 (*s)[2]) {
 #pragma unroll
   for (int u = 0; u < 2; u++) {
-    const float sc = scale_of<0>(C.ks[u] >> (8 * (threadIdx.x & 3)));
+    const float sc = scale_of<0>(C.ks[u] >> (8 * (token_of<D>((threadIdx.x >> 2) & 3, threadIdx.x & 3) & 3)));
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) s[nt][u] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -713,8 +731,15 @@ __device__ __forceinline__ void key_products(const Chunk<D>& C, const f16x8 (*q)
 template <int D, int NT>
 __device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, const f16x8* P, f32x4 (*o)[D / 16]) {
   float vs[8];
-  vs[0] = scale_of<0>(C.vs[0]); vs[1] = scale_of<1>(C.vs[0]); vs[2] = scale_of<2>(C.vs[0]); vs[3] = scale_of<3>(C.vs[0]);
-  vs[4] = scale_of<0>(C.vs[1]); vs[5] = scale_of<1>(C.vs[1]); vs[6] = scale_of<2>(C.vs[1]); vs[7] = scale_of<3>(C.vs[1]);
+  if constexpr (D == 128) {                            // byte 2 (j % 2) + G % 2 to bits 23 .., by rotation
+    const uint32_t odd = (threadIdx.x >> 1) & 8;
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      vs[j] = bits_f(__builtin_amdgcn_alignbit(C.vs[j >> 1], C.vs[j >> 1], 9 + 16 * (j & 1) + odd));
+  } else {
+    vs[0] = scale_of<0>(C.vs[0]); vs[1] = scale_of<1>(C.vs[0]); vs[2] = scale_of<2>(C.vs[0]); vs[3] = scale_of<3>(C.vs[0]);
+    vs[4] = scale_of<0>(C.vs[1]); vs[5] = scale_of<1>(C.vs[1]); vs[6] = scale_of<2>(C.vs[1]); vs[7] = scale_of<3>(C.vs[1]);
+  }
   if (!full) {    // unwritten bytes behind the last token: any finite value, their weights are 0
 #pragma unroll
     for (int j = 0; j < 8; j++) vs[j] = bits_f(min(__float_as_uint(vs[j]) & 0x7F800000u, (uint32_t)(E_MAX + 127) << 23));
@@ -747,11 +772,12 @@ __device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, con
 // waves take every NWV-th chunk straight from memory into the operands'
 // registers and join their running softmaxes through LDS at the end.
 // Measured (32 heads over 8, d = 128, one token): 8 requests of 32,768 to
-// 131,072 tokens 164 us for 777 MB of codes and scales = 4.7 TB/s (loads alone
-// 161); 64 of 2,048 to 8,191 tokens 80 us = 4.6 TB/s (loads alone 74, work on
-// resident data 57: the two overlap but for the waits inside a wave); one of
-// 1,021 tokens 9.4 us.  Three tokens of 8 heads each over windows of 1,024 at d
-// = 64, 128 requests: 17.5 us, bound by the instructions of two waves a SIMD.
+// 131,072 tokens 147 us for 777 MB of codes and scales = 5.3 TB/s; 64 of 2,048 to
+// 8,191 tokens 73 us = 5.0 TB/s (a plain read past the caches runs at 7.0, a
+// copy at 5.16; the vector units are busy 40 % of the time, the rest is the
+// chain of a chunk: keys, products, weights, products); one of 1,021 tokens
+// 9.4 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
+// requests: 17.5 us, bound by the instructions and the chain of two waves a SIMD.
 // o *= f of tile nt where any lane of `far` is set (accumulators of 16 rows and
 // D channels: D/4 registers)
 template <int D, int NT>
@@ -773,7 +799,7 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
   }
 }
 
-template <int D, int TYPE, int NT, int NWV>
+template <int D, int TYPE, int NT, int NWV, bool ONCE>
 __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(AttnArgs A) {
   constexpr int NC = D / 16;
   __shared__ f32x4 so[NWV][NT * NC][64];
@@ -824,10 +850,10 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
     return x;
   };
   auto keys = [&](const Next& x) {
-    load_keys<D>(C, W, x.base + x.off * (D / 2), x.base + A.T * D + x.off);
+    load_keys<D, ONCE>(C, W, x.base + x.off * (D / 2), x.base + A.T * D + x.off);
   };
   auto values = [&](const Next& x) {
-    load_values<D>(C, W, x.base + A.T * (D / 2) + x.off * (D / 2), x.base + A.T * D + A.T * (D / 32) + x.off);
+    load_values<D, ONCE>(C, W, x.base + A.T * (D / 2) + x.off * (D / 2), x.base + A.T * D + A.T * (D / 32) + x.off);
   };
   Next at;
   at.dead = true;
@@ -860,7 +886,8 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
   }
   // One set of registers for the codes: the next chunk's keys are asked for as
   // soon as this one's are unpacked, its values likewise; the other waves of
-  // the SIMD cover what that does not (a second set measured the same or worse).
+  // the SIMD cover what that does not (a second set takes the registers of one or
+  // two waves: 147 -> 162 us and 73 -> 77 for the long and the ragged batch).
   while (k < c1) {
     const int ch = chunk_at(k), t0 = ch * 32, t1 = t0 + 31;
     const bool dead = at.dead, full = !dead && t1 <= p0 && (A.window == 0 || t0 > p1 - A.window || t1 < A.sink);
@@ -876,7 +903,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
         const int low = A.window == 0 ? -1 : pos[nt] - A.window, last = dead ? -1 : pos[nt];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const int t = t0 + 8 * G + e;
+          const int t = t0 + token_of<D>(G, e);
           const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < A.sink));
           s[nt][e >> 2][e & 3] = see ? s[nt][e >> 2][e & 3] : NEG_INF;
         }
@@ -1345,6 +1372,18 @@ __global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_rows) 
   const f32x2 none = {NEG_INF, 0.0f};
   const f32x2* ml = (const f32x2*)A.pml + row;
   const f32x2 m0 = lane < parts ? ml[lane * stride] : none, m1 = lane + 64 < parts ? ml[(lane + 64) * stride] : none;
+  // N parts from s on are under way at a time (the last one again where there
+  // are fewer, not added): the first eight along with the statistics
+  const float* po = A.po + row * D + lane * (D / 64);
+  constexpr int FIRST = 8, MORE = 24;
+  float y[MORE][D / 64];
+  auto ask = [&](auto N, int s) {
+#pragma unroll
+    for (int e = 0; e < N; e++)
+#pragma unroll
+      for (int u = 0; u < D / 64; u++) y[e][u] = po[min(s + e, parts - 1) * stride * D + u];
+  };
+  ask(std::integral_constant<int, FIRST>(), 0);
   float M = wave_max(__builtin_fmaxf(m0[0], m1[0]));
   if (M == NEG_INF) M = 0.0f;
   const float f0 = __builtin_amdgcn_exp2f(m0[0] - M), f1 = __builtin_amdgcn_exp2f(m1[0] - M);
@@ -1352,19 +1391,18 @@ __global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_rows) 
   float x[D / 64];
 #pragma unroll
   for (int u = 0; u < D / 64; u++) x[u] = 0.0f;
-  const float* po = A.po + row * D + lane * (D / 64);
-  for (int s = 0; s < parts; s += 8) {                 // eight loads under way at a time (the last ones twice, with weight 0)
-    float y[8][D / 64];
+  auto add = [&](auto N, int s) {
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-#pragma unroll
-      for (int u = 0; u < D / 64; u++) y[e][u] = po[min(s + e, parts - 1) * stride * D + u];
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const float f = s + e < parts ? bits_f(__builtin_amdgcn_readlane(__float_as_uint(s + e < 64 ? f0 : f1), (s + e) & 63)) : 0.0f;
+    for (int e = 0; e < N; e++) {
+      const float f = bits_f(__builtin_amdgcn_readlane(__float_as_uint(s + e < 64 ? f0 : f1), (s + e) & 63));
 #pragma unroll
       for (int u = 0; u < D / 64; u++) x[u] = s + e < parts ? __builtin_fmaf(f, y[e][u], x[u]) : x[u];
     }
+  };
+  add(std::integral_constant<int, FIRST>(), 0);
+  for (int s = FIRST; s < parts; s += MORE) {
+    ask(std::integral_constant<int, MORE>(), s);
+    add(std::integral_constant<int, MORE>(), s);
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   uint16_t* o = (uint16_t*)A.o + (int64_t)(R.first + j) * A.os + hd * D + lane * (D / 64);
@@ -1404,7 +1442,7 @@ bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
          (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
          a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
 }
-struct Split { int tiles, tile_rows, splits, per, waves; bool staged; };
+struct Split { int tiles, tile_rows, splits, per, waves; bool staged, once; };
 // Query rows per key/value head up to which each wave unpacks the cache for
 // itself, 32 rows at a time; above, it is staged through LDS for 128 rows (16
 // requests of up to 8,192 tokens, 8 heads: 36 rows 43 against 89 us staged, 64
@@ -1415,9 +1453,16 @@ constexpr int STAGED_ROWS = 64;
 // (the joins), about 5 us.  Few workgroups are split down to 8 chunks until
 // every CU holds three; many only into parts of 48 chunks and up, which even
 // out ragged lengths, and until every CU has eight of them (64 requests of 2,048
-// to 8,191 tokens, 8 heads: 83 us whole, 85 in parts of 128 chunks, 80 in parts
-// of 64, 80 of 48, 91 of 24; 8 requests of 32,768 to 131,072 tokens: 171 us at
-// six workgroups a CU, 164 at eight, 167 at ten, 169 at sixteen).
+// to 8,191 tokens, 8 heads: 78 us at four workgroups a CU, 73 to 74 at six to
+// sixteen; 83 whole and 91 in parts of 24 chunks before the loads past the
+// caches; 8 requests of 32,768 to 131,072 tokens: 156 us at four, 153 at six, 146
+// at eight, 150 at ten, 152 at sixteen).
+// A cache larger than the last-level cache is read past the caches at d = 128:
+// nothing of it would be there at the next call (rates at 32 heads over 8: 570
+// MB of pages 78 -> 73 us, 1.1 GB 161 -> 146, three times the rows per head 109
+// -> 106; 139 MB, which the next call finds again, 22.4 -> 23.1; d = 64, whose
+// loads cover half lines, 50 -> 54 and stays as it is).
+constexpr int64_t LAST_CACHE_BYTES = 256 << 20;
 constexpr int64_t CUS = 256, FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
@@ -1429,6 +1474,7 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   int64_t seen = a->max_len;
   if (a->window > 0) seen = seen < (int64_t)a->window + a->n_sink + 64 ? seen : (int64_t)a->window + a->n_sink + 64;
   const int64_t chunks = (seen + 31) / 32;
+  s.once = d->d == 128 && (double)chunks * 32 * 17 / 16 * d->d * d->n_kv_heads * a->n_req > (double)LAST_CACHE_BYTES;
   auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
   int64_t k = 1;
   if (base > 0) {
@@ -1450,13 +1496,18 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   return s;
 }
 
+template <int D, int TYPE, bool ONCE>
+void launch_rows(AttnArgs& A, const Split& s, unsigned grid, hipStream_t st) {
+  if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, ONCE>), dim3(grid), dim3(256), 0, st, A);
+  else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16, false>), dim3(grid), dim3(1024), 0, st, A);
+  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, ONCE>), dim3(grid), dim3(256), 0, st, A);
+}
 template <int D, int TYPE>
 void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
   if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
-  else if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4>), dim3(grid), dim3(256), 0, st, A);
-  else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16>), dim3(grid), dim3(1024), 0, st, A);
-  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4>), dim3(grid), dim3(256), 0, st, A);
+  else if (s.once) launch_rows<D, TYPE, D == 128>(A, s, grid, st);
+  else launch_rows<D, TYPE, false>(A, s, grid, st);
   if (A.splits > 1) {
     const int64_t rows = (int64_t)A.n_req * A.max_new * A.hq;
     hipLaunchKernelGGL((k_attend_join<D, TYPE>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, A, s.tile_rows);

@@ -722,3 +722,14 @@ def test_tensor_checks(stq):
                 dict(o=o[:2]), dict(q=q.cpu()), dict(q=q[:, :, :32]), dict(q=q[:1].expand(3, 4, 64)), dict(work=torch.zeros(8, device="cuda"))):
         with pytest.raises(stq.StqError):
             stq.stq_kv_attend(kv, **dict(ok, **bad), scale=1.0, max_new=3, max_len=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("news", [1, 7, 12])
+def test_attend_of_a_cache_said_to_be_large(stq, dtype, news):
+    """Stated lengths whose pages no cache holds: the loads that leave no trace, for one tile of rows, two
+    tiles' worth in one, and two tiles."""
+    lens = [1, 31, 33, 64, 129, 700, 1555]
+    B = Batch(stq, lens, [min(news, n) for n in lens], 8, 2, 128, 32, dtype, seed=news, spare=1)
+    for window, sink in ((0, 0), (100, 3)):
+        B.check(B.run(window=window, sink=sink, max_len=1 << 20), window, sink)
