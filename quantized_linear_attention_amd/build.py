@@ -4,6 +4,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,7 +15,7 @@ TENSOR_SRC, TENSOR_LIB = os.path.join(PKG, "csrc", "tensor.cpp"), os.path.join(P
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # every floating-point contraction in the kernels is an explicit fma
     "-ffp-contract=off",
     # no packed fp32 VALU ops (v_pk_{add,mul,fma}_f32) anywhere
@@ -39,15 +40,24 @@ def _current(out, deps):
 
 
 def build(force=True, verbose=False):
-    """Compile libstq.so and _tensor.so (always when force=True)."""
-    if force or not _current(TENSOR_LIB, [TENSOR_SRC]):
-        from torch.utils.cpp_extension import include_paths, library_paths
-        inc = include_paths() + [sysconfig.get_paths()["include"]]
-        _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared"] + ["-I" + d for d in inc] +
-             [TENSOR_SRC] + ["-L" + d for d in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"],
-             TENSOR_LIB, verbose)
-    if force or not _current(LIB, DEPS):
-        _run([HIPCC] + FLAGS + SRC, LIB, verbose)
+    """Compile libstq.so and _tensor.so (always when force=True), the sources side by side."""
+    from concurrent.futures import ThreadPoolExecutor
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor() as pool:
+        jobs, link = [], None
+        if force or not _current(LIB, DEPS):
+            objects = [os.path.join(tmp, os.path.basename(f) + ".o") for f in SRC]
+            jobs = [pool.submit(_run, [HIPCC] + FLAGS + ["-c", f], o, verbose) for f, o in zip(SRC, objects)]
+            link = [HIPCC] + FLAGS[:1] + ["-shared", "-fPIC"] + objects
+        if force or not _current(TENSOR_LIB, [TENSOR_SRC]):
+            from torch.utils.cpp_extension import include_paths, library_paths
+            inc = include_paths() + [sysconfig.get_paths()["include"]]
+            jobs.append(pool.submit(_run, [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared"] +
+                                    ["-I" + d for d in inc] + [TENSOR_SRC] + ["-L" + d for d in library_paths()] +
+                                    ["-ltorch_python", "-ltorch_cpu", "-lc10"], TENSOR_LIB, verbose))
+        for j in jobs:
+            j.result()
+        if link:
+            _run(link, LIB, verbose)
     return LIB
 
 
