@@ -21,6 +21,24 @@ constexpr int E_MIN = -23, E_MAX = 13;   // exponents of the cache's scales
 
 __device__ __forceinline__ float bits_f(uint32_t u) { return __uint_as_float(u); }
 
+// Division by an argument of the call, its reciprocal taken on the host: floor(2^32
+// / by) is at most one step short for every 32-bit x.  (The compiler's division
+// is a chain of some 40 instructions; five of them at a kernel's start and end
+// cost 0.7 us of the 9.6 of one short request.  k_attend_tiles keeps the
+// compiler's: they are nothing of its time, and its loop came out slower with
+// these, 239 us for 227.)
+struct Div { uint32_t by, inv; };
+Div div_of(int64_t by) {
+  Div d;
+  d.by = by < 1 ? 1u : (uint32_t)by;
+  d.inv = d.by == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / d.by);
+  return d;
+}
+__device__ __forceinline__ int quot(uint32_t x, Div d) {
+  const uint32_t q = __umulhi(x, d.inv);
+  return (int)(q + (x - q * d.by >= d.by ? 1u : 0u));
+}
+
 // A 16-byte load that leaves no trace in the caches (once = true: data that no
 // one reads again) or an ordinary one.
 template <bool ONCE, typename T>
@@ -200,6 +218,7 @@ struct NormArgs {
   const float *wq, *wk, *cs;
   const int32_t* pos;
   int n_tok, hq, hk, n_rot, n_pos, norm, adjacent, per_tok;
+  Div by_per_tok;
   float eps;
   int64_t qs, ks, qos, kos;
 };
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(256) k_qk_norm_rope(NormArgs A) {
   const int lane = threadIdx.x & 63;
   const int li = lane % LPR, c0 = 8 * li;
   const int gw = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
-  const int tok = gw / A.per_tok, part = gw - tok * A.per_tok;
+  const int tok = quot(gw, A.by_per_tok), part = gw - tok * A.per_tok;
   if (tok >= A.n_tok) return;
   const int64_t t = tok;
   const int rows = A.hq + A.hk, R = A.n_rot, step = A.per_tok * RPW;
@@ -333,6 +352,7 @@ struct StoreArgs {
   const void *k, *v;
   void *ko, *vo;
   int n_tok, heads, T;
+  Div by_heads;
   int64_t n_slots, ks, vs;
 };
 
@@ -377,7 +397,7 @@ template <int D>
 __device__ __forceinline__ StoreAt store_at(const StoreArgs& A) {
   constexpr int LPR = D / 8, RPB = 256 / LPR;
   StoreAt s;
-  const uint32_t tile = blockIdx.x / (uint32_t)A.heads;
+  const uint32_t tile = quot(blockIdx.x, A.by_heads);
   s.h = (int)(blockIdx.x - tile * (uint32_t)A.heads);
   s.li = threadIdx.x % LPR;
   s.t = (int64_t)tile * RPB + threadIdx.x / LPR;
@@ -476,6 +496,7 @@ struct AttnArgs {
   void* o;
   float *po, *pml;          // partial results: [split][row][D], [split][row][2]
   int n_req, n_tok, hq, hkv, group, T, n_blocks, cols, max_new, window, sink, splits, per, tiles;
+  Div by_hkv, by_group, by_max_new, by_per;
   int64_t qs, os;
   float scale_log2;
 };
@@ -508,7 +529,8 @@ __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
 // multiple of four: one per wave).  Shorter requests have fewer parts, all of
 // one size.
 __device__ __forceinline__ int split_chunks(const AttnArgs& A, int total) {
-  return max(((total + A.splits - 1) / A.splits + 3) & ~3, A.per);
+  if (total <= A.per * A.splits) return A.per;
+  return ((total + A.splits - 1) / A.splits + 3) & ~3;
 }
 
 __device__ __forceinline__ float max_quads(float x) {   // over the four 16-lane groups
@@ -773,11 +795,11 @@ __device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, con
 // registers and join their running softmaxes through LDS at the end.
 // Measured (32 heads over 8, d = 128, one token): 8 requests of 32,768 to
 // 131,072 tokens 147 us for 777 MB of codes and scales = 5.3 TB/s; 64 of 2,048 to
-// 8,191 tokens 73 us = 5.0 TB/s (a plain read past the caches runs at 7.0, a
+// 8,191 tokens 71 us = 5.1 TB/s (a plain read past the caches runs at 7.0, a
 // copy at 5.16; the vector units are busy 40 % of the time, the rest is the
 // chain of a chunk: keys, products, weights, products); one of 1,021 tokens
-// 9.4 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
-// requests: 17.5 us, bound by the instructions and the chain of two waves a SIMD.
+// 8.9 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
+// requests: 17.1 us, bound by the instructions and the chain of two waves a SIMD.
 // o *= f of tile nt where any lane of `far` is set (accumulators of 16 rows and
 // D channels: D/4 registers)
 template <int D, int NT>
@@ -808,20 +830,21 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   // the splits slowest: a short request has none of the last ones, and
   // neighbouring workgroups go to different XCDs
-  int b = blockIdx.x;
-  const int h = b % A.hkv; b /= A.hkv;
-  const int i = b % A.n_req; b /= A.n_req;
-  const int tile = b % A.tiles, sp = b / A.tiles;
+  const int i = quot(blockIdx.x, A.by_hkv), h = blockIdx.x - i * A.hkv;
+  const int tile = blockIdx.y, sp = blockIdx.z;
   const Req R = req_args(A, i);
-  const int row0 = tile * 16 * NT, rows = min(R.n_new, A.max_new) * A.group;
+  const int fresh = min(R.n_new, A.max_new), rows = fresh * A.group, row0 = tile * 16 * NT;
   if (row0 >= rows) return;
-  const int j1 = (min(row0 + 16 * NT, rows) - 1) / A.group;
-  const int p0 = R.base + row0 / A.group, p1 = R.base + j1;
+  int p0 = R.base, p1 = R.base + fresh - 1;             // positions of the tile's first and last row
+  if (A.tiles > 1) {
+    p0 = R.base + quot(row0, A.by_group);
+    p1 = R.base + quot(min(row0 + 16 * NT, rows) - 1, A.by_group);
+  }
   const Span sn = span_of(p0, p1, A.window, A.sink);
   const int per = split_chunks(A, sn.total);
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
   if (c0 >= c1 && sp > 0) return;
-  const int parts = (sn.total + per - 1) / per;
+  const bool whole = sn.total <= per;                   // one part: its result is the output's
 
   const int32_t* tab = A.table + (int64_t)i * A.cols;
   const int blk_shift = 31 - __builtin_clz(A.T) - 5;    // chunks of a block, as a power of two
@@ -869,7 +892,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
     // rows past the last compute the last one again and are not written
-    const int r = min(row0 + 16 * nt + n, rows - 1), j = r / A.group, g = r - j * A.group;
+    const int r = min(row0 + 16 * nt + n, rows - 1), j = quot(r, A.by_group), g = r - j * A.group;
     grow[nt] = row0 + 16 * nt + n < rows ? (int64_t)(R.first + j) * A.hq + h * A.group + g : -1;
     pos[nt] = R.base + j;
     load_q<D, TYPE>(A, (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + G * (D / 4), q[nt], &cf[nt]);
@@ -974,9 +997,9 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
       }
     }
     const int ch0 = NC * 4 * G + CW * wave;
-    if (parts <= 1) {
+    if (whole) {
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-      const int64_t t = R.first + (row0 + 16 * nt + n) / A.group;
+      const int64_t t = R.first + quot(row0 + 16 * nt + n, A.by_group);
       uint16_t* out = (uint16_t*)A.o + t * A.os + (grow[nt] - t * A.hq) * D + ch0;
 #pragma unroll
       for (int i4 = 0; i4 < 4; i4++) {
@@ -1012,7 +1035,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
 // address (lane 4t + c: channels 4c.. of token t).
 //
 // Measured (4 prompts of 1,078 to 2,048 tokens over up to 2,048 cached ones, 32
-// heads over 8, d = 128): 230 us = 930 TFLOP/s, where a library product of
+// heads over 8, d = 128): 228 us = 938 TFLOP/s (237 on a card that clocks lower), where a library product of
 // 8,192 x 8,192 x 8,192 in binary16 runs at 1,150.  A tile costs a wave about
 // 1,000 cycles of matrix instructions and as many of vector ones (32 exp2 at
 // half rate, the conversions, the sums), which share the SIMD's issue with the
@@ -1354,19 +1377,24 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
 // Join the splits of one row: one wave per row, its channels over the lanes,
 // the splits in order.
 template <int D, int TYPE>
-__global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_rows) {
+__global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_shift) {
   const int lane = threadIdx.x & 63;
-  int64_t b = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int hd = (int)(b % A.hq); b /= A.hq;
-  const int j = (int)(b % A.max_new), i = (int)(b / A.max_new);
-  if (i >= A.n_req) return;
+  const int hd = __builtin_amdgcn_readfirstlane((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
+  if (hd >= A.hq) return;
+  const int i = quot(blockIdx.x, A.by_max_new), j = blockIdx.x - i * A.max_new;
   const Req R = req_args(A, i);
-  if (j >= R.n_new) return;
-  const int row0 = (j * A.group + hd % A.group) / tile_rows * tile_rows, rows = min(R.n_new, A.max_new) * A.group;
-  const int j1 = (min(row0 + tile_rows, rows) - 1) / A.group;
-  const Span sn = span_of(R.base + row0 / A.group, R.base + j1, A.window, A.sink);
-  const int per = split_chunks(A, sn.total), parts = (sn.total + per - 1) / per;
-  if (parts <= 1) return;                              // written by its only part
+  const int fresh = min(R.n_new, A.max_new), rows = fresh * A.group;
+  if (j >= fresh) return;
+  int p0 = R.base, p1 = R.base + fresh - 1;             // as the tile's workgroups had them
+  if (A.tiles > 1) {
+    const int row0 = ((j * A.group + hd - quot(hd, A.by_group) * A.group) >> tile_shift) << tile_shift;
+    p0 = R.base + quot(row0, A.by_group);
+    p1 = R.base + quot(min(row0 + (1 << tile_shift), rows) - 1, A.by_group);
+  }
+  const Span sn = span_of(p0, p1, A.window, A.sink);
+  const int per = split_chunks(A, sn.total);
+  if (sn.total <= per) return;                              // written by its only part
+  const int parts = per == A.per ? quot(sn.total + per - 1, A.by_per) : (sn.total + per - 1) / per;
   const int64_t stride = (int64_t)A.n_tok * A.hq, row = (int64_t)(R.first + j) * A.hq + hd;
   // statistics: part s on lane s (and s + 64)
   const f32x2 none = {NEG_INF, 0.0f};
@@ -1497,20 +1525,21 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
 }
 
 template <int D, int TYPE, bool ONCE>
-void launch_rows(AttnArgs& A, const Split& s, unsigned grid, hipStream_t st) {
-  if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, ONCE>), dim3(grid), dim3(256), 0, st, A);
-  else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16, false>), dim3(grid), dim3(1024), 0, st, A);
-  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, ONCE>), dim3(grid), dim3(256), 0, st, A);
+void launch_rows(AttnArgs& A, const Split& s, hipStream_t st) {
+  const dim3 grid((unsigned)(A.n_req * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
+  if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, ONCE>), grid, dim3(256), 0, st, A);
+  else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16, false>), grid, dim3(1024), 0, st, A);
+  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, ONCE>), grid, dim3(256), 0, st, A);
 }
 template <int D, int TYPE>
 void launch_attend(AttnArgs& A, const Split& s, hipStream_t st) {
   const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
   if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
-  else if (s.once) launch_rows<D, TYPE, D == 128>(A, s, grid, st);
-  else launch_rows<D, TYPE, false>(A, s, grid, st);
+  else if (s.once) launch_rows<D, TYPE, D == 128>(A, s, st);
+  else launch_rows<D, TYPE, false>(A, s, st);
   if (A.splits > 1) {
-    const int64_t rows = (int64_t)A.n_req * A.max_new * A.hq;
-    hipLaunchKernelGGL((k_attend_join<D, TYPE>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, A, s.tile_rows);
+    const dim3 rows((unsigned)(A.n_req * A.max_new), (unsigned)((A.hq + 3) / 4));
+    hipLaunchKernelGGL((k_attend_join<D, TYPE>), rows, dim3(256), 0, st, A, __builtin_ctz(s.tile_rows));
   }
 }
 
@@ -1606,6 +1635,7 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   const int sets = (A.hq + A.hk + 512 / d->d - 1) / (512 / d->d);
   A.per_tok = (int)((NORM_WAVES + A.n_tok - 1) / A.n_tok);
   if (A.per_tok > (sets + 1) / 2) A.per_tok = (sets + 1) / 2;
+  A.by_per_tok = div_of(A.per_tok);
   if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, past, st);
   else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, past, st);
   else launch_norm_in<256>(A, d->in_type, d->out_type, past, st);
@@ -1624,7 +1654,7 @@ stq_status stq_kv_store(const stq_kv_desc* d, void* cache, size_t bytes, const i
   if (kv_grid(d, n_tok) > INT32_MAX) return STQ_ERR_UNSUPPORTED;
   StoreArgs A;
   memset(&A, 0, sizeof(A));
-  A.cache = (uint8_t*)cache; A.slot = slot; A.k = k; A.v = v; A.n_tok = n_tok; A.heads = d->n_kv_heads;
+  A.cache = (uint8_t*)cache; A.slot = slot; A.k = k; A.v = v; A.n_tok = n_tok; A.heads = d->n_kv_heads; A.by_heads = div_of(A.heads);
   A.T = d->block_tokens; A.n_slots = (int64_t)d->n_blocks * d->block_tokens; A.ks = k_stride; A.vs = v_stride;
   if (d->d == 64) launch_kv<64>(A, type, true, st);
   else launch_kv<128>(A, type, true, st);
@@ -1642,7 +1672,7 @@ stq_status stq_kv_fetch(const stq_kv_desc* d, const void* cache, size_t bytes, c
   if (kv_grid(d, n_tok) > INT32_MAX) return STQ_ERR_UNSUPPORTED;
   StoreArgs A;
   memset(&A, 0, sizeof(A));
-  A.cache = (uint8_t*)cache; A.slot = slot; A.ko = k_out; A.vo = v_out; A.n_tok = n_tok; A.heads = d->n_kv_heads;
+  A.cache = (uint8_t*)cache; A.slot = slot; A.ko = k_out; A.vo = v_out; A.n_tok = n_tok; A.heads = d->n_kv_heads; A.by_heads = div_of(A.heads);
   A.T = d->block_tokens; A.n_slots = (int64_t)d->n_blocks * d->block_tokens;
   if (d->d == 64) launch_kv<64>(A, type, false, st);
   else launch_kv<128>(A, type, false, st);
@@ -1677,7 +1707,9 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.q = q; A.o = o;
   A.n_req = a->n_req; A.n_tok = a->n_tok; A.hq = a->n_heads; A.hkv = d->n_kv_heads; A.group = a->n_heads / d->n_kv_heads;
   A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = a->table_cols; A.max_new = a->max_new; A.window = a->window;
-  A.sink = a->n_sink; A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles; A.qs = a->q_stride; A.os = a->o_stride;
+  A.sink = a->n_sink; A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles;
+  A.by_hkv = div_of(A.hkv); A.by_group = div_of(A.group); A.by_max_new = div_of(A.max_new); A.by_per = div_of(A.per);
+  A.qs = a->q_stride; A.os = a->o_stride;
   A.scale_log2 = a->scale * 1.44269504088896340736f;
   A.po = (float*)work;
   A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
