@@ -454,7 +454,8 @@ size_t stq_kv_bytes(const stq_kv_desc* desc);
  *   used_dev [1]         blocks wanted; above n_free, the free list was short.
  * blocks(c) = ceil(c / block_tokens).  Entries of pos and slot from
  * tok_start[n] on (a padded batch) become -1; new tokens past n_tok get no
- * entry.  n in [1, 4096]; token and block sums must stay below 2^31. */
+ * entry.  n in [1, 4096]; token and block sums must stay below 2^31.  No
+ * output may overlap the counts or the free list (STQ_ERR_ARG). */
 stq_status stq_kv_plan(int32_t n, const int32_t* cached_dev, const int32_t* new_dev, const int32_t* free_dev,
                        int32_t n_free, int32_t n_blocks, int32_t block_tokens, int32_t* table_dev,
                        int32_t table_cols, int32_t n_tok, int32_t* tok_start_dev, int32_t* len_dev,

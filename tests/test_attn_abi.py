@@ -255,3 +255,18 @@ def test_binding_passes_short_strides_on(stq, monkeypatch):
             with pytest.raises(stq.StqError) as e:
                 call(x, y)
             assert e.value.status in (-1, -2)       # before any launch
+
+
+def test_plan_refuses_outputs_over_inputs(L):
+    """Lengths written over the counts they come from, and any other output that reaches into an input."""
+    at = {k: 0x100000 * (i + 1) for i, k in enumerate(("cached", "new", "free", "table", "tok", "len", "pos", "slot", "used"))}
+    size = dict(cached=12, new=12, free=8, table=48, tok=16, len=12, pos=20, slot=40, used=4)
+
+    def call(**over):
+        p = {k: P(v) for k, v in dict(at, **over).items()}
+        return L.stq_kv_plan(3, p["cached"], p["new"], p["free"], 2, 10, 64, p["table"], 4, 5, p["tok"], p["len"], p["pos"],
+                             p["slot"], p["used"], None)
+    for i in ("cached", "new", "free"):
+        for o in ("table", "tok", "len", "pos", "slot", "used"):
+            for a in (at[i], at[i] + size[i] - 4, at[i] - size[o] + 4):
+                assert call(**{o: a}) == -1, (i, o)

@@ -733,3 +733,33 @@ def test_attend_of_a_cache_said_to_be_large(stq, dtype, news):
     B = Batch(stq, lens, [min(news, n) for n in lens], 8, 2, 128, 32, dtype, seed=news, spare=1)
     for window, sink in ((0, 0), (100, 3)):
         B.check(B.run(window=window, sink=sink, max_len=1 << 20), window, sink)
+
+
+def test_plan_of_one_buffer(stq):
+    """All tensors side by side in one buffer, none reaching into another."""
+    import torch
+    n, T, cols, tok = 5, 32, 7, 77
+    cached, new = [0, 31, 64, 100, 5], [40, 2, 0, 30, 1]
+    buf = torch.full((64 + 3 * n + cols * n + 20 + 4 * tok,), -7, dtype=torch.int32, device="cuda")
+    at = 0
+
+    def part(m, values=None):
+        nonlocal at
+        x = buf[at:at + m]
+        at += m
+        if values is not None:
+            x.copy_(cu(np.array(values), torch.int32))
+        return x
+    used, a, b, f = part(1), part(n, cached), part(n, new), part(20, range(20))
+    table, start, lens, pos = part(n * cols).view(n, cols), part(n + 1), part(n), part(tok)
+    table.copy_(cu(np.arange(100, 100 + n * cols).reshape(n, cols), torch.int32))
+    at += at % 2
+    slots = part(2 * tok).view(torch.int64)
+    want = R.plan(cached, new, np.arange(20), np.arange(100, 100 + n * cols).reshape(n, cols), T, 200, tok)
+    stq.stq_kv_plan(a, b, f, table, T, 200, start, lens, pos, slots, used)
+    torch.cuda.synchronize()
+    for got, k in ((start, "tok_start"), (lens, "lens"), (pos, "pos"), (slots, "slots"), (table, "table"), (used, "used")):
+        assert np.array_equal(got.cpu().numpy(), want[k]), k
+    assert a.tolist() == cached and b.tolist() == new and f.tolist() == list(range(20))
+    with pytest.raises(stq.StqError):
+        stq.stq_kv_plan(a, b, f, table, T, 200, start, a, pos, slots, used)
