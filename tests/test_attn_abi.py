@@ -270,3 +270,33 @@ def test_plan_refuses_outputs_over_inputs(L):
         for o in ("table", "tok", "len", "pos", "slot", "used"):
             for a in (at[i], at[i] + size[i] - 4, at[i] - size[o] + 4):
                 assert call(**{o: a}) == -1, (i, o)
+
+
+def test_binding_refuses_values_a_descriptor_cannot_hold(stq, monkeypatch):
+    import torch
+    b, i = torch.bfloat16, torch.int32
+    kv = stq.make_kv(Fake([10 * 2 * 64 * 136], torch.uint8), 64, 2, 128)
+    q, o = Fake([4, 2, 128], b), Fake([4, 2, 128], b, ptr=0x20000)
+    args = (kv, Fake([2, 5], i), Fake([3], i), Fake([2], i), q, o)
+    for scale, max_new, window in (("1", 2, 0), (None, 2, 0), (0.1, 2.5, 0), (0.1, 2, 1.0)):
+        with pytest.raises(stq.StqError, match="descriptor"):
+            stq.stq_kv_attend(*args, scale, max_new, 100, window=window, stream=0)
+    with pytest.raises(stq.StqError, match="descriptor"):
+        stq.stq_qk_norm_rope(q, None, o, None, eps=None, stream=0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)   # an infinite scale is the library's to refuse
+    for scale in (1e39, -1e39, float("nan")):
+        with pytest.raises(stq.StqError) as e:
+            stq.stq_kv_attend(*args, scale, 2, 100, stream=0)
+        assert e.value.status == -1
+    with pytest.raises(stq.StqError, match="descriptor"):
+        stq.stq_kv_attend_bytes(kv, 2, 4, 2, 2, 100, window=3.5)
+
+
+def test_packed_descriptors_are_the_structures():
+    """The packed bytes lie as the structures' fields do."""
+    import ctypes
+    from quantized_linear_attention_amd import _lib
+    for pack, desc in ((_lib._norm_desc, _lib._NormDesc), (_lib._attend_desc, _lib._AttendDesc)):
+        values = [0.5 + i if t is ctypes.c_float else (i + 1) * (2 ** 33 if t is ctypes.c_int64 else 3) for i, (_, t) in enumerate(desc._fields_)]
+        d = desc.from_buffer_copy(pack(*values))
+        assert [getattr(d, n) for n, _ in desc._fields_] == values
