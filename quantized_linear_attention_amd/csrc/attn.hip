@@ -1481,8 +1481,10 @@ struct Split { int tiles, tile_rows, splits, per, waves; bool staged, once; };
 // 64 rows 54 against 63, 96 rows 67 against 62, 128 rows 84 against 67).
 constexpr int STAGED_ROWS = 64;
 // A part of a request's work has its own start (three dependent loads) and end
-// (the joins), about 5 us.  Few workgroups are split down to 8 chunks until
-// every CU holds three; many only into parts of 48 chunks and up, which even
+// (the joins), about 5 us.  Few workgroups are split down to 12 chunks, three a
+// wave, until every CU holds two (1 x 16,000 tokens of 8 heads 13.9 us in parts of
+// 8 chunks, 11.4 of 12, 12.0 of 16; 8 x 2,000 11.0, 9.9, 10.9; 1 x 2,000 8.0,
+// 8.7, 9.8; 8 x 6,000 14.7 at two workgroups a CU, 16.1 at three); many only into parts of 48 chunks and up, which even
 // out ragged lengths, and until every CU has eight of them (64 requests of 2,048
 // to 8,191 tokens, 8 heads: 78 us at four workgroups a CU, 73 to 74 at six to
 // sixteen; 83 whole and 91 in parts of 24 chunks before the loads past the
@@ -1494,7 +1496,7 @@ constexpr int STAGED_ROWS = 64;
 // -> 106; 139 MB, which the next call finds again, 22.4 -> 23.1; d = 64, whose
 // loads cover half lines, 50 -> 54 and stays as it is).
 constexpr int64_t LAST_CACHE_BYTES = 256 << 20;
-constexpr int64_t CUS = 256, FEW_GROUPS = 768, FEW_CHUNKS = 8, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
+constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
   const int64_t rows = (int64_t)a->max_new * (a->n_heads / d->n_kv_heads);
