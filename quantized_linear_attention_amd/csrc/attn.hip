@@ -501,7 +501,7 @@ struct AttnArgs {
   int n_req, n_tok, hq, hkv, group, T, n_blocks, cols, max_new, window, sink, splits, per, tiles;
   Div by_hkv, by_group, by_max_new, by_per;
   int64_t qs, os;
-  float scale_log2;
+  float scale;
 };
 
 // Chunks of 32 positions that some row of positions [p0, p1] sees: the first
@@ -572,8 +572,11 @@ constexpr float NEG_INF = -__builtin_inff();
 __device__ __forceinline__ int q_shift(float m) {
   return m > 0.0f && m < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;
 }
-__device__ __forceinline__ float q_factor(float scale_log2, int e) {
-  return __builtin_fmaxf(__builtin_ldexpf(__builtin_fabsf(scale_log2), -e), 1.17549435e-38f);
+// (Kept normal, and at most 2^80: two products that differ are 2^-48 apart at
+// least, which is 2^32 logits then, and products of 2^38 stay finite.)
+__device__ __forceinline__ float q_factor(float scale, int e) {
+  const float c = __builtin_ldexpf(__builtin_fabsf(scale), -e) * 1.44269504088896340736f;
+  return __builtin_fminf(__builtin_fmaxf(c, 1.17549435e-38f), 0x1p80f);
 }
 
 // A wave's query rows as matrix operands: row n = lane % 16 of tile nt, the
@@ -592,12 +595,12 @@ __device__ __forceinline__ void load_q(const AttnArgs& A, int64_t at, f16x8* q, 
   for (int i = 0; i < D / 4; i++) m = __builtin_fmaxf(m, __builtin_fabsf(x[i]));
   m = max_quads(m);
   const int e = q_shift(m);
-  const float sign = A.scale_log2 < 0.0f ? -1.0f : 1.0f;
+  const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
   for (int i = 0; i < D / 32; i++)
 #pragma unroll
     for (int j = 0; j < 8; j++) q[i][j] = (f16)(sign * __builtin_ldexpf(x[8 * i + j], e));
-  *c = q_factor(A.scale_log2, e);
+  *c = q_factor(A.scale, e);
 }
 
 // One chunk (32 cached tokens of one head) as a wave loads it.  Element e of
@@ -698,16 +701,21 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 struct Ref {
   float m, mc, over;       // the product it stands at, times c; products above `over` move it
   __device__ __forceinline__ void init() { m = over = NEG_INF; mc = 0.0f; }
-  // to the product x; the factor of what was summed so far.  (Nothing seen yet:
-  // any finite reference will do, every weight is 2^-inf.)
+  // Nothing seen yet: any finite reference will do, every weight is 2^-inf.
+  __device__ __forceinline__ float at() const { return m == NEG_INF ? 0.0f : m; }
+  // to the product x; the factor of what was summed so far
   __device__ __forceinline__ float move(float x, float c) {
-    const float xc = x == NEG_INF ? 0.0f : x * c;
-    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(m, c, -xc));
+    const float from = m;
     m = x;
-    mc = xc;
+    mc = at() * c;
     over = x + 8.0f * __builtin_amdgcn_rcpf(c);
-    return f;
+    return __builtin_amdgcn_exp2f((from - at()) * c);
   }
+  // mc is off by half a step of its own, the same for all of a row's weights,
+  // which their quotient does not mind; but past 2^22 that begins to leave the
+  // weights' range (2^27 logits: by 2^8).  Such rows' waves take the reference from
+  // the products before they are multiplied.
+  __device__ __forceinline__ bool steep() const { return __builtin_fabsf(mc) >= 0x1p22f; }
 };
 
 // x *= f for `count` registers from V`first` on, where any lane of `far` is set.
@@ -901,11 +909,13 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
     load_q<D, TYPE>(A, (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + G * (D / 4), q[nt], &cf[nt]);
   }
   Ref ref[NT];
+  uint64_t steep[NT];
   float l[NT];             // this lane group's part of the sum
   f32x4 o[NT][NC];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
     ref[nt].init();
+    steep[nt] = 0;
     l[nt] = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; c++) o[nt][c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -939,16 +949,25 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
       for (int e = 1; e < 8; e++) m = __builtin_fmaxf(m, s[nt][e >> 2][e & 3]);
       const uint64_t far = __builtin_amdgcn_ballot_w64(m > ref[nt].over);
       float f = 1.0f;
-      if (far) f = ref[nt].move(__builtin_fmaxf(ref[nt].m, max_quads(m)), cf[nt]);
+      if (far) {
+        f = ref[nt].move(__builtin_fmaxf(ref[nt].m, max_quads(m)), cf[nt]);
+        steep[nt] = __builtin_amdgcn_ballot_w64(ref[nt].steep());
+      }
       l[nt] *= f;
       scale_rows<D, NT>(far, f, o, nt);
+      float mc = ref[nt].mc;
+      if (steep[nt]) {
+        mc = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; e++) s[nt][e >> 2][e & 3] -= ref[nt].at();
+      }
       // Weights to binary16 in pairs; the sum takes the same rounded weights, so
       // that a weight's rounding moves o by its own part only.
       uint32_t pk[4];
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1)], cf[nt], -ref[nt].mc));
-        const float b2 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1) + 1], cf[nt], -ref[nt].mc));
+        const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1)], cf[nt], -mc));
+        const float b2 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nt][e >> 1][2 * (e & 1) + 1], cf[nt], -mc));
         const f16x2 hh = weights<TYPE>(a, b2);
         pk[e] = h2_bits(hh);
         l[nt] = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, l[nt], false);
@@ -978,11 +997,11 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
       ml[w] = sml[w][nt][n];
       M = __builtin_fmaxf(M, ml[w][0]);
     }
-    const float mc = M == NEG_INF ? 0.0f : M * cf[nt];
+    const float M0 = M == NEG_INF ? 0.0f : M;
     float L = 0.0f, f[NWV];
 #pragma unroll
     for (int w = 0; w < NWV; w++) {
-      f[w] = __builtin_amdgcn_exp2f(__builtin_fmaf(ml[w][0], cf[nt], -mc));
+      f[w] = __builtin_amdgcn_exp2f((ml[w][0] - M0) * cf[nt]);
       L = __builtin_fmaf(ml[w][1], f[w], L);
     }
     // tiles CW * wave ..: channels (D/16)(4G + i) + c
@@ -1011,7 +1030,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
       }
     } else {
       const int64_t row = (int64_t)sp * A.n_tok * A.hq + grow[nt];
-      if (G == 0 && wave == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){M == NEG_INF ? NEG_INF : mc, L};
+      if (G == 0 && wave == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){M * cf[nt], L};
       float* out = A.po + row * D + ch0;
 #pragma unroll
       for (int i4 = 0; i4 < 4; i4++) {
@@ -1151,12 +1170,12 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
     for (int u = 0; u < D / 2; u++) m = __builtin_fmaxf(m, __builtin_fabsf(x[u]));
     m = max_halves(m);
     const int e = q_shift(m);
-    const float sign = A.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
     for (int s = 0; s < KSTEP; s++)
 #pragma unroll
       for (int u = 0; u < 8; u++) q[s][u] = (f16)(sign * __builtin_ldexpf(x[8 * s + u], e));
-    cf = q_factor(A.scale_log2, e);
+    cf = q_factor(A.scale, e);
   }
   f32x16 o[NC];
 #pragma unroll
@@ -1165,6 +1184,7 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
     for (int u = 0; u < 16; u++) o[c][u] = 0.0f;
   Ref ref;
   ref.init();
+  uint64_t steep = 0;
   float L = 0.0f;
 
   const int32_t* tab = A.table + (int64_t)i * A.cols;
@@ -1279,12 +1299,21 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
     for (int e = 1; e < 32; e++) m = __builtin_fmaxf(m, s[e >> 4][e & 15]);
     const uint64_t far = __builtin_amdgcn_ballot_w64(m > ref.over);
     float f = 1.0f;
-    if (far) f = ref.move(__builtin_fmaxf(ref.m, max_halves(m)), cf);
+    if (far) {
+      f = ref.move(__builtin_fmaxf(ref.m, max_halves(m)), cf);
+      steep = __builtin_amdgcn_ballot_w64(ref.steep());
+    }
     L *= f;
     if constexpr (NC == 4)
       SCALE_WHERE(far, f, 192, 64, AT(192:207)(o[0]), AT(208:223)(o[1]), AT(224:239)(o[2]), AT(240:255)(o[3]));
     else
       SCALE_WHERE(far, f, 128, 32, AT(128:143)(o[0]), AT(144:159)(o[1]));
+    float mc = ref.mc;
+    if (steep) {
+      mc = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 32; e++) s[e >> 4][e & 15] -= ref.at();
+    }
     // (the wave that has matrix work goes first: 234 -> 229 us)
     __builtin_amdgcn_s_setprio(1);
     key_tile(next_k, sn);
@@ -1296,8 +1325,8 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e], cf, -ref.mc));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e + 1], cf, -ref.mc));
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e], cf, -mc));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * y + 2 * e + 1], cf, -mc));
           const f16x2 hh = weights<TYPE>(e0, e1);
           pk[e] = h2_bits(hh);
           L = __builtin_amdgcn_fdot2(hh, (f16x2){(f16)1.0f, (f16)1.0f}, L, false);
@@ -1722,7 +1751,7 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   A.sink = a->n_sink; A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles;
   A.by_hkv = div_of(A.hkv); A.by_group = div_of(A.group); A.by_max_new = div_of(A.max_new); A.by_per = div_of(A.per);
   A.qs = a->q_stride; A.os = a->o_stride;
-  A.scale_log2 = a->scale * 1.44269504088896340736f;
+  A.scale = a->scale;
   A.po = (float*)work;
   A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
   if (d->d == 64) {
