@@ -544,7 +544,9 @@ size_t stq_kv_attend_bytes(const stq_kv_desc* desc, const stq_attend_desc* a);
  * else STQ_ERR_LAYOUT.  A workspace serves one call at a time.  o must not
  * overlap q.  Products run on the matrix cores in binary16 (cached values and
  * queries exact, the queries scaled by a power of two per row; softmax
- * weights rounded to binary16), sums and statistics in binary32. */
+ * weights rounded to binary16, for bfloat16 outputs cut to it: off by 2^-10
+ * of themselves, or by 2^-31 of the row's largest where they are below 2^-21
+ * of it), sums and statistics in binary32. */
 stq_status stq_kv_attend(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, const stq_attend_desc* a,
                          const int32_t* table_dev, const int32_t* tok_start_dev, const int32_t* len_dev,
                          const void* q_dev, void* o_dev, void* work_dev, size_t work_bytes, hipStream_t stream);

@@ -693,11 +693,17 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
   return __builtin_bit_cast(f16x8, (u32x4){a, b, c, d});
 }
 
-// What a row's weights are relative to, 2^(product * c - mc).  It follows the
-// row's largest product only when a weight would pass 2^8: until then it stays
-// (binary16 holds weights to 2^15, the sums are binary32, and a quotient does
-// not mind), which spares most steps the exchange between lanes and the
-// rescaling of the sums.
+// What a row's weights are relative to, 2^(product * c - mc).  A weight at the
+// reference is 2^LIFT, and the reference follows the row's largest product only
+// when a weight would pass 2^(LIFT + 8) = 2^15, which binary16 still holds (the
+// sums are binary32, and a quotient does not mind): that spares most steps the
+// exchange between lanes and the rescaling of the sums.  The lift is for the small
+// weights: binary16 is subnormal below 2^-14, with steps of 2^-24, so without it
+// thousands of tokens at 2^-20 of a dominant one (16 nats) lose much of their sum
+// (16,390 tokens 14 nats below four: outputs off by 3.7 %, by 48 % at 16.6 nats).
+// With it weights are normal down to 2^-21 of the largest, and below that off by
+// 2^-31 of it at most.
+constexpr float LIFT = 7.0f, MOVE = 8.0f;
 struct Ref {
   float m, mc, over;       // the product it stands at, times c; products above `over` move it
   __device__ __forceinline__ void init() { m = over = NEG_INF; mc = 0.0f; }
@@ -707,13 +713,13 @@ struct Ref {
   __device__ __forceinline__ float move(float x, float c) {
     const float from = m;
     m = x;
-    mc = at() * c;
-    over = x + 8.0f * __builtin_amdgcn_rcpf(c);
+    mc = __builtin_fmaf(at(), c, -LIFT);
+    over = x + MOVE * __builtin_amdgcn_rcpf(c);
     return __builtin_amdgcn_exp2f((from - at()) * c);
   }
   // mc is off by half a step of its own, the same for all of a row's weights,
   // which their quotient does not mind; but past 2^22 that begins to leave the
-  // weights' range (2^27 logits: by 2^8).  Such rows' waves take the reference from
+  // weights' range (at 2^24 by 2^1).  Such rows' waves take the reference from
   // the products before they are multiplied.
   __device__ __forceinline__ bool steep() const { return __builtin_fabsf(mc) >= 0x1p22f; }
 };
@@ -734,7 +740,8 @@ struct Ref {
 // Two weights as a binary16 pair.  Outputs of binary16: to nearest.  bfloat16
 // outputs take the truncating conversion (one instruction at full rate against
 // one at half): off by 2^-10 of a weight at most where the output's own
-// rounding is 2^-8, and the weights' sum takes the same truncated values.
+// rounding is 2^-8 (and by 2^-31 of the row's largest below 2^-21 of it: see
+// Ref), and the weights' sum takes the same truncated values.
 template <int TYPE>
 __device__ __forceinline__ f16x2 weights(float a, float b) {
   if constexpr (TYPE == STQ_BF16) return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b));
@@ -957,7 +964,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
       scale_rows<D, NT>(far, f, o, nt);
       float mc = ref[nt].mc;
       if (steep[nt]) {
-        mc = 0.0f;
+        mc = -LIFT;
 #pragma unroll
         for (int e = 0; e < 8; e++) s[nt][e >> 2][e & 3] -= ref[nt].at();
       }
@@ -1310,7 +1317,7 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
       SCALE_WHERE(far, f, 128, 32, AT(128:143)(o[0]), AT(144:159)(o[1]));
     float mc = ref.mc;
     if (steep) {
-      mc = 0.0f;
+      mc = -LIFT;
 #pragma unroll
       for (int e = 0; e < 32; e++) s[e >> 4][e & 15] -= ref.at();
     }
