@@ -1531,6 +1531,7 @@ constexpr int STAGED_ROWS = 64;
 // MB of pages 78 -> 73 us, 1.1 GB 161 -> 146, three times the rows per head 109
 // -> 106; 139 MB, which the next call finds again, 22.4 -> 23.1; d = 64, whose
 // loads cover half lines, 50 -> 54 and stays as it is).
+constexpr int32_t MOST_WINDOW = 1 << 30;
 constexpr int64_t LAST_CACHE_BYTES = 256 << 20;
 constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
@@ -1754,8 +1755,11 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   AttnArgs A;
   A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.q = q; A.o = o;
   A.n_req = a->n_req; A.n_tok = a->n_tok; A.hq = a->n_heads; A.hkv = d->n_kv_heads; A.group = a->n_heads / d->n_kv_heads;
-  A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = a->table_cols; A.max_new = a->max_new; A.window = a->window;
-  A.sink = a->n_sink; A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles;
+  A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = a->table_cols; A.max_new = a->max_new;
+  // positions lie in (-2^28, 2^30): a window past that is no limit, and the kernels' differences of the two stay in 32 bits
+  A.window = a->window < MOST_WINDOW ? a->window : MOST_WINDOW;
+  A.sink = a->n_sink < MOST_WINDOW ? a->n_sink : MOST_WINDOW;
+  A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles;
   A.by_hkv = div_of(A.hkv); A.by_group = div_of(A.group); A.by_max_new = div_of(A.max_new); A.by_per = div_of(A.per);
   A.qs = a->q_stride; A.os = a->o_stride;
   A.scale = a->scale;

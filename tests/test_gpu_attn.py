@@ -763,3 +763,14 @@ def test_plan_of_one_buffer(stq):
     assert a.tolist() == cached and b.tolist() == new and f.tolist() == list(range(20))
     with pytest.raises(stq.StqError):
         stq.stq_kv_plan(a, b, f, table, T, 200, start, a, pos, slots, used)
+
+
+@pytest.mark.parametrize("news", [[9, 4, 40], [90, 4, 130]])
+def test_attend_windows_without_end(stq, news):
+    """The largest windows and counts of first tokens are no limit at all, for
+    rows at negative positions too."""
+    B = Batch(stq, [3, 0, 100], news, 4, 2, 64, 32, "bf16")
+    want = B.run()
+    B.check(want)
+    for window, sink in ((2 ** 31 - 1, 0), (2 ** 31 - 2, 2 ** 31 - 1), (1 << 30, 1), (1, 2 ** 31 - 1)):
+        assert np.array_equal(host(B.run(window, sink)), host(want)), (window, sink)
