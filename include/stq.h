@@ -522,7 +522,9 @@ stq_status stq_kv_fetch(const stq_kv_desc* desc, const void* cache_dev, size_t b
 typedef struct stq_attend_desc {
   int32_t n_req;            /* requests (>= 0)                                */
   int32_t n_tok;            /* rows of q and o, 0 .. 2^28 (a padded batch may   */
-                            /* have more than tok_start[n_req]: left alone)   */
+                            /* have more than tok_start[n_req]: left alone;   */
+                            /* query tokens past n_tok have no row, but count */
+                            /* for the others' positions)                     */
   int32_t n_heads;          /* a multiple of n_kv_heads                       */
   int32_t type;             /* of q and o: STQ_BF16 or STQ_FP16               */
   int32_t table_cols;       /* columns of the block table                     */

@@ -516,15 +516,21 @@ __device__ __forceinline__ Span span_of(int p0, int p1, int window, int sink) {
   s.total = s.n_low + (p1 >> 5) + 1 - s.lo;
   return s;
 }
-struct Req { int first, n_new, len, base; };   // first row, query tokens, cached tokens, position of query 0
-__device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
+// First row, rows, position of query 0.  Query tokens behind the last row of q
+// count for the positions (no row lies before -2^28: there are at most 2^28).
+struct Req { int first, n_new, base; };
+__device__ __forceinline__ Req req_of(const AttnArgs& A, int start, int end, int len) {
+  start = max(start, 0);
+  end = max(end, start);
+  len = (int)min((int64_t)max(len, 0), (int64_t)A.cols * A.T);
   Req r;
-  r.first = min(max(ld_const(A.tok_start + i), 0), A.n_tok);
-  const int end = min(max(ld_const(A.tok_start + i + 1), r.first), A.n_tok);
-  r.n_new = end - r.first;
-  r.len = (int)min((int64_t)max(ld_const(A.len + i), 0), (int64_t)A.cols * A.T);
-  r.base = r.len - r.n_new;
+  r.first = min(start, A.n_tok);
+  r.n_new = min(end, A.n_tok) - r.first;
+  r.base = max(len - (end - start), -(1 << 28));
   return r;
+}
+__device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
+  return req_of(A, ld_const(A.tok_start + i), ld_const(A.tok_start + i + 1), ld_const(A.len + i));
 }
 
 // Chunks of one part of a request's work: the host's size for a request of the
@@ -1114,11 +1120,10 @@ __device__ __forceinline__ bool tile_of(const AttnArgs& A, int rows_of_tile, int
     return *row0 >= 0;
   }
   const int lane = threadIdx.x & 63, i = min(lane, A.n_req - 1);
-  const int first = min(max(A.tok_start[i], 0), A.n_tok), end = min(max(A.tok_start[i + 1], first), A.n_tok);
-  const int len = (int)min((int64_t)max(A.len[i], 0), (int64_t)A.cols * A.T);
-  const int fresh = min(end - first, A.max_new);
+  const Req R = req_of(A, A.tok_start[i], A.tok_start[i + 1], A.len[i]);
+  const int fresh = min(R.n_new, A.max_new);
   const int tiles = lane < A.n_req ? (fresh * A.group + rows_of_tile - 1) / rows_of_tile : 0;
-  const int last = tiles > 0 ? len - (end - first) + fresh : -(1 << 30);    // behind the last query's position
+  const int last = tiles > 0 ? R.base + fresh : -(1 << 30);    // behind the last query's position
   const int band = max(rows_of_tile / A.group, 1);
   const int top = wave_max_i(last);                      // (by all lanes)
   const int skip = tiles > 0 ? (top - last) / band : 0;  // bands above the request's first

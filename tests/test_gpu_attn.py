@@ -774,3 +774,18 @@ def test_attend_windows_without_end(stq, news):
     B.check(want)
     for window, sink in ((2 ** 31 - 1, 0), (2 ** 31 - 2, 2 ** 31 - 1), (1 << 30, 1), (1, 2 ** 31 - 1)):
         assert np.array_equal(host(B.run(window, sink)), host(want)), (window, sink)
+
+
+@pytest.mark.parametrize("news,kept", [([3, 6, 2], 5), ([3, 6, 2], 2), ([70, 5, 90], 130), ([4, 300, 7], 150)])
+def test_attend_start_offsets_past_the_rows(stq, news, kept):
+    """A batch whose offsets go on behind the last row of q (a plan with room for fewer tokens than the
+    requests bring): the rows that are there keep their positions."""
+    import torch
+    B = Batch(stq, [40, 320, 95], news, 4, 2, 64, 32, "bf16")
+    whole = B.run()
+    B.check(whole)
+    for window, sink in ((0, 0), (20, 3)):
+        whole = B.run(window, sink)
+        o = B.run(window, sink, q=B.q[:kept].clone())
+        assert o.shape[0] == kept
+        B.check(torch.cat([o, whole[kept:]]), window, sink)
