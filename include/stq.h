@@ -543,7 +543,9 @@ size_t stq_kv_attend_bytes(const stq_kv_desc* desc, const stq_attend_desc* a);
 /* Lengths are taken as at most table_cols * block_tokens; blocks whose table
  * entry lies outside [0, n_blocks) hold no visible token.  q and o 16-byte
  * aligned with strides a multiple of 16 bytes, the workspace 16-byte aligned,
- * else STQ_ERR_LAYOUT.  A workspace serves one call at a time.  o must not
+ * else STQ_ERR_LAYOUT.  STQ_ERR_UNSUPPORTED for calls larger than a launch:
+ * n_req * max_new * n_heads from 2^31 on, or n_req * n_kv_heads (times the
+ * query rows' tiles and the splits) from 2^24 on.  A workspace serves one call at a time.  o must not
  * overlap q.  Products run on the matrix cores in binary16 (cached values and
  * queries exact, the queries scaled by a power of two per row; softmax
  * weights rounded to binary16, for bfloat16 outputs cut to it: off by 2^-10

@@ -1495,7 +1495,8 @@ stq_status kv_check(const stq_kv_desc* d, const void* cache, size_t bytes) {
   if (!cache || ((uintptr_t)cache & 15u) || bytes < kv_size(d)) return STQ_ERR_LAYOUT;
   return STQ_OK;
 }
-int64_t kv_grid(const stq_kv_desc* d, int64_t n_tok) { return (n_tok + 2048 / d->d - 1) / (2048 / d->d) * d->n_kv_heads; }
+// A launch takes fewer than 2^32 threads in one direction; calls on more tokens go in slices.
+constexpr int64_t MOST_THREADS = (1ll << 32) - 1, MOST_GROUPS = 1 << 23;
 // The L2s of the eight dies together: a larger output cannot stay there for its
 // reader, and stored past them it leaves room and saves their write-back
 // (16,381 tokens of 40 heads normed 74.8 -> 67.8 us with loads past them as
@@ -1610,12 +1611,26 @@ void launch_norm_in(const NormArgs& A, int in, int out, bool past, hipStream_t s
 }
 
 template <int D, int TYPE>
-void launch_kv_type(const StoreArgs& A, bool store, hipStream_t st) {
+void launch_kv_type(StoreArgs A, bool store, hipStream_t st) {
   constexpr int RPB = 256 / (D / 8);
-  const dim3 g((unsigned)(((int64_t)A.n_tok + RPB - 1) / RPB * A.heads)), b(256);
-  if (store) hipLaunchKernelGGL((k_kv_store<D, TYPE>), g, b, 0, st, A);
-  else if (2 * (int64_t)A.n_tok * A.heads * D * elem_bytes(TYPE) > CACHE_BYTES) hipLaunchKernelGGL((k_kv_fetch<D, TYPE, true>), g, b, 0, st, A);
-  else hipLaunchKernelGGL((k_kv_fetch<D, TYPE, false>), g, b, 0, st, A);
+  const int64_t all = A.n_tok, slice = MOST_GROUPS / A.heads * RPB, w = (int64_t)A.heads * D;
+  const bool past = 2 * all * w * elem_bytes(TYPE) > CACHE_BYTES;
+  const StoreArgs F = A;
+  for (int64_t t = 0; t < all; t += slice) {
+    A.n_tok = (int)(all - t < slice ? all - t : slice);
+    A.slot = F.slot + t;
+    const dim3 g((unsigned)(((int64_t)A.n_tok + RPB - 1) / RPB * A.heads)), b(256);
+    if (store) {
+      A.k = (const char*)F.k + t * A.ks * elem_bytes(TYPE);
+      A.v = (const char*)F.v + t * A.vs * elem_bytes(TYPE);
+      hipLaunchKernelGGL((k_kv_store<D, TYPE>), g, b, 0, st, A);
+    } else {
+      A.ko = (char*)F.ko + t * w * elem_bytes(TYPE);
+      A.vo = (char*)F.vo + t * w * elem_bytes(TYPE);
+      if (past) hipLaunchKernelGGL((k_kv_fetch<D, TYPE, true>), g, b, 0, st, A);
+      else hipLaunchKernelGGL((k_kv_fetch<D, TYPE, false>), g, b, 0, st, A);
+    }
+  }
 }
 template <int D>
 void launch_kv(const StoreArgs& A, int type, bool store, hipStream_t st) {
@@ -1690,9 +1705,19 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   A.per_tok = (int)((NORM_WAVES + A.n_tok - 1) / A.n_tok);
   if (A.per_tok > (sets + 1) / 2) A.per_tok = (sets + 1) / 2;
   A.by_per_tok = div_of(A.per_tok);
-  if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, past, st);
-  else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, past, st);
-  else launch_norm_in<256>(A, d->in_type, d->out_type, past, st);
+  const int ib = elem_bytes(d->in_type), ob = elem_bytes(d->out_type);
+  const int64_t slice = A.per_tok > 1 ? d->n_tok : 4 * MOST_GROUPS;     // (several waves a token: 16,384 waves at most)
+  for (int64_t t = 0; t < d->n_tok; t += slice) {
+    A.n_tok = (int)(d->n_tok - t < slice ? d->n_tok - t : slice);
+    A.q = (const char*)q + t * d->q_stride * ib;
+    A.qo = (char*)qo + t * d->q_out_stride * ob;
+    if (k) A.k = (const char*)k + t * d->k_stride * ib;
+    if (ko) A.ko = (char*)ko + t * d->k_out_stride * ob;
+    if (pos) A.pos = pos + t;
+    if (d->d == 64) launch_norm_in<64>(A, d->in_type, d->out_type, past, st);
+    else if (d->d == 128) launch_norm_in<128>(A, d->in_type, d->out_type, past, st);
+    else launch_norm_in<256>(A, d->in_type, d->out_type, past, st);
+  }
   return launched();
 }
 
@@ -1705,7 +1730,6 @@ stq_status stq_kv_store(const stq_kv_desc* d, void* cache, size_t bytes, const i
   if (!slot || !k || !v) return STQ_ERR_ARG;
   const int64_t w = (int64_t)d->n_kv_heads * d->d;
   if (!aligned(k) || !aligned(v) || !stride_ok(k_stride, w, type) || !stride_ok(v_stride, w, type)) return STQ_ERR_LAYOUT;
-  if (kv_grid(d, n_tok) > INT32_MAX) return STQ_ERR_UNSUPPORTED;
   StoreArgs A;
   memset(&A, 0, sizeof(A));
   A.cache = (uint8_t*)cache; A.slot = slot; A.k = k; A.v = v; A.n_tok = n_tok; A.heads = d->n_kv_heads; A.by_heads = div_of(A.heads);
@@ -1723,7 +1747,6 @@ stq_status stq_kv_fetch(const stq_kv_desc* d, const void* cache, size_t bytes, c
   if (n_tok == 0) return STQ_OK;
   if (!slot || !k_out || !v_out) return STQ_ERR_ARG;
   if (!aligned(k_out) || !aligned(v_out)) return STQ_ERR_LAYOUT;
-  if (kv_grid(d, n_tok) > INT32_MAX) return STQ_ERR_UNSUPPORTED;
   StoreArgs A;
   memset(&A, 0, sizeof(A));
   A.cache = (uint8_t*)cache; A.slot = slot; A.ko = k_out; A.vo = v_out; A.n_tok = n_tok; A.heads = d->n_kv_heads; A.by_heads = div_of(A.heads);
@@ -1754,8 +1777,10 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   const Split sp = split_of(d, a);
   const size_t need = stq_kv_attend_bytes(d, a);
   if (need > 0 && (!work || !aligned(work) || work_bytes < need)) return STQ_ERR_LAYOUT;
-  if ((int64_t)a->n_req * d->n_kv_heads * sp.tiles * sp.splits > INT32_MAX ||
-      (int64_t)a->n_req * a->max_new * a->n_heads > INT32_MAX)
+  const int64_t groups = (int64_t)a->n_req * d->n_kv_heads;
+  if ((int64_t)a->n_req * a->max_new * a->n_heads > INT32_MAX ||
+      (sp.staged ? groups * sp.tiles * sp.splits * 64 * TILE_WAVES : groups * 64 * sp.waves) > MOST_THREADS ||
+      (sp.splits > 1 && (int64_t)a->n_req * a->max_new * 256 > MOST_THREADS))
     return STQ_ERR_UNSUPPORTED;
   AttnArgs A;
   A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.q = q; A.o = o;

@@ -300,3 +300,12 @@ def test_packed_descriptors_are_the_structures():
         values = [0.5 + i if t is ctypes.c_float else (i + 1) * (2 ** 33 if t is ctypes.c_int64 else 3) for i, (_, t) in enumerate(desc._fields_)]
         d = desc.from_buffer_copy(pack(*values))
         assert [getattr(d, n) for n, _ in desc._fields_] == values
+
+
+def test_attend_refuses_more_threads_than_a_launch_takes(L):
+    """2^32 threads and more in one direction: a refusal, not the runtime's error."""
+    one = kvd(n_kv_heads=1)
+    full = L.stq_kv_bytes(ctypes.byref(one))
+    for kw in (dict(n_heads=1, q_stride=128, o_stride=128), dict(n_heads=65, q_stride=65 * 128, o_stride=65 * 128)):
+        a = ad(n_req=1 << 24, **kw)
+        assert L.stq_kv_attend(ctypes.byref(one), D, full, ctypes.byref(a), D, D, D, D, P(0x20000), None, 0, None) == -5, kw

@@ -789,3 +789,53 @@ def test_attend_start_offsets_past_the_rows(stq, news, kept):
         o = B.run(window, sink, q=B.q[:kept].clone())
         assert o.shape[0] == kept
         B.check(torch.cat([o, whole[kept:]]), window, sink)
+
+
+def test_norm_of_more_tokens_than_a_grid_holds(stq):
+    """2^26 tokens and a few: as many blocks of 2^20 that all get what one gets alone."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(6)
+    m, times, d = 1 << 20, 64, 64
+    n = m * times + 5
+    one = torch.randn(m, 1, d, device="cuda", generator=g).bfloat16()
+    at = torch.randint(0, 300, (m,), device="cuda", generator=g).to(torch.int32)
+    table = cu(cos_sin(300, 16))
+    want = torch.empty_like(one)
+    stq.stq_qk_norm_rope(one, None, want, None, pos=at, cos_sin=table)
+    q, pos = torch.empty(n, 1, d, dtype=one.dtype, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
+    for x, y in ((q, one), (pos, at)):
+        x[:m * times].view(times, m, *x.shape[1:]).copy_(y)
+        x[m * times:] = y[:5]
+    stq.stq_qk_norm_rope(q, None, q, None, pos=pos, cos_sin=table)
+    for i in range(times):
+        assert torch.equal(q[i * m:(i + 1) * m], want), i
+    assert torch.equal(q[m * times:], want[:5])
+
+
+def test_store_and_fetch_of_more_tokens_than_a_grid_holds(stq):
+    """2^29 and a few (token, head) pairs: the tokens that have a slot, some all
+    over the call and the last ones, are written and read back, no other."""
+    import torch
+    heads, d, T = 2048, 64, 32
+    n = (1 << 18) + 33
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 130 GiB")
+    k, v = (torch.empty(n, heads, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    live = torch.tensor([0, 31, 32, 1 << 16, (1 << 17) - 1, 1 << 17, (1 << 17) + 1, (1 << 18) - 1, 1 << 18, n - 2, n - 1], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    a, b = (torch.randn(len(live), heads, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    k[live], v[live] = a, b
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    slots[live] = torch.arange(len(live), device="cuda") + 3
+    kv = stq.make_kv(torch.zeros(stq.stq_kv_bytes(1, T, heads, d), dtype=torch.uint8, device="cuda"), T, heads, d)
+    few = stq.make_kv(torch.zeros_like(kv.pages), T, heads, d)
+    stq.stq_kv_store(few, slots[live], a, b)
+    stq.stq_kv_store(kv, slots, k, v)
+    assert torch.equal(kv.pages, few.pages)
+    want = [torch.empty_like(a) for _ in range(2)]
+    stq.stq_kv_fetch(kv, slots[live], *want)
+    k[live], v[live] = 7, 7
+    k[5], v[n - 9] = 3, 3
+    stq.stq_kv_fetch(kv, slots, k, v)
+    assert torch.equal(k[live], want[0]) and torch.equal(v[live], want[1])
+    assert (k[5] == 3).all() and (v[n - 9] == 3).all()
