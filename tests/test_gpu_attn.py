@@ -839,3 +839,22 @@ def test_store_and_fetch_of_more_tokens_than_a_grid_holds(stq):
     stq.stq_kv_fetch(kv, slots, k, v)
     assert torch.equal(k[live], want[0]) and torch.equal(v[live], want[1])
     assert (k[5] == 3).all() and (v[n - 9] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,d,new,L", [(4, 128, 1, 20011), (3, 64, 8, 20011), (2, 128, 40, 33000), (4, 64, 1, 33000)])
+def test_attend_long_requests(stq, dtype, heads, d, new, L):
+    """Parts of more than 64 chunks a wave, whose table entries are asked for again, and more than 64 parts of one
+    row; blocks outside the cache on both sides of the places where either happens."""
+    T = 32
+    B = Batch(stq, [L], [new], heads, 1, d, T, dtype, seed=new)
+    for at in (3, 63, 64, 65, 255, 256, 257, 320, 511, 512, L // T - 3):
+        B.table[0, at] = -1
+    i = B.stq
+    parts = i.stq_kv_attend_bytes(B.kvc, 1, B.tok, heads, new, L) // (B.tok * heads * (d + 2) * 4)
+    assert i.stq_kv_attend_bytes(B.kvc, 1, B.tok, heads, new, 1) == 0
+    if L > 30000:
+        assert parts > 64
+    for hint in (1, L):
+        B.check(B.run(max_len=hint))
+    B.check(B.run(window=L - 5000, sink=100, max_len=1), L - 5000, 100)
