@@ -1,10 +1,14 @@
-"""ctypes marshalling for libstq.so (no computation happens here); _tensor.so checks tensor arguments."""
+"""ctypes marshalling for libstq.so (no computation happens here); _tensor.so, where it is there, checks tensor arguments."""
 import ctypes
 import os
 import struct
 
 import numpy as np
-import torch    # before the library: see _load
+
+try:
+    import torch    # before the library: see _load
+except ImportError:
+    torch = None    # the host-only calls need none
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _PATH = os.path.join(_PKG, "libstq.so")
@@ -120,7 +124,23 @@ def _load():
 
 
 _L = _load()
-from . import _tensor    # noqa: E402  (built with the library; links against torch)
+
+
+class _PythonChecks:
+    """In the place of the compiled checks: they pass nothing, so every argument takes the steps in Python."""
+    address = rows = staticmethod(lambda *a: None)
+
+
+def _compiled_checks():
+    """_tensor.so links against torch's C++ interface: it serves the torch that it was compiled with, and no other."""
+    try:
+        from . import _tensor as t
+    except ImportError:
+        return _PythonChecks
+    return t if str(torch.__version__).split("+")[0] == t.torch_version else _PythonChecks
+
+
+_tensor = _PythonChecks if torch is None else _compiled_checks()
 
 
 def stq_status_str(status):
@@ -331,7 +351,7 @@ def stq_requant_fixed_scales(pool, slots, stream=None):
 
 # ------------------------------------------- the softmax layers' operators
 
-_TYPES = {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}
+_TYPES = {} if torch is None else {torch.bfloat16: STQ_BF16, torch.float16: STQ_FP16, torch.float32: STQ_FP32}
 
 
 def _type(t, what, allowed=(STQ_BF16, STQ_FP16, STQ_FP32)):

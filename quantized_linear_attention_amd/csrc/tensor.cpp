@@ -7,6 +7,7 @@
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 namespace {
 
@@ -63,4 +64,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor", "checks of tensor argume
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor(void) { return PyModule_Create(&module); }
+// (nothing of torch is called here: the binding compares the version first)
+PyMODINIT_FUNC PyInit__tensor(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -309,3 +309,70 @@ def test_attend_refuses_more_threads_than_a_launch_takes(L):
     for kw in (dict(n_heads=1, q_stride=128, o_stride=128), dict(n_heads=65, q_stride=65 * 128, o_stride=65 * 128)):
         a = ad(n_req=1 << 24, **kw)
         assert L.stq_kv_attend(ctypes.byref(one), D, full, ctypes.byref(a), D, D, D, D, P(0x20000), None, 0, None) == -5, kw
+
+
+def _import_alone(tmp_path, code, keep=("libstq.so",)):
+    """Runs `code` where the package has its sources and the files of `keep` only."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    import quantized_linear_attention_amd as q
+    src = os.path.dirname(q.library_path())
+    pkg = tmp_path / os.path.basename(src)
+    pkg.mkdir()
+    for f in os.listdir(src):
+        if f.endswith(".py"):
+            shutil.copy(os.path.join(src, f), pkg / f)
+        elif f in keep:
+            os.symlink(os.path.join(src, f), pkg / f)
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=240,
+                       env=dict(os.environ, PYTHONPATH=str(tmp_path)))
+    assert r.returncode == 0, r.stderr
+    return r.stdout
+
+
+ALLOCATE = """
+import numpy as np, quantized_linear_attention_amd as stq
+e = np.array([[4.0, 2.0, 1.0], [8.0, 1.0, 0.5]])
+bits, obj = stq.stq_allocate_bits(e, np.array([1.0, 1.0]), 1, 12)
+print(bits.tolist(), stq.stq_kv_bytes(10, 64, 2, 128))
+"""
+
+
+def test_import_without_the_compiled_checks(tmp_path):
+    """The package's host side without _tensor.so: every check is Python's then."""
+    want = _import_alone(tmp_path, ALLOCATE, ("libstq.so", "_tensor.so"))
+    (tmp_path / "b").mkdir()
+    assert _import_alone(tmp_path / "b", ALLOCATE) == want
+    (tmp_path / "c").mkdir()
+    _import_alone(tmp_path / "c", """
+import torch, quantized_linear_attention_amd as stq
+try:
+    stq.make_kv(torch.zeros(1 << 20, dtype=torch.uint8), 64, 2, 128)
+    raise SystemExit("taken")
+except stq.StqError as e:
+    assert "pages" in str(e)
+x = torch.zeros(3, 2, 64)
+try:
+    stq.stq_qk_norm_rope(x, None, x, None)
+    raise SystemExit("taken")
+except stq.StqError as e:
+    assert "q is on cpu" in str(e), e
+""")
+
+
+def test_import_with_checks_of_another_torch(tmp_path):
+    """A _tensor.so that does not load, or that was compiled against another torch, is left aside."""
+    want = _import_alone(tmp_path, ALLOCATE, ("libstq.so", "_tensor.so"))
+    (tmp_path / "b").mkdir()
+    assert _import_alone(tmp_path / "b", "open('quantized_linear_attention_amd/_tensor.so', 'w').write('no library')\n" + ALLOCATE) == want
+    (tmp_path / "c").mkdir()
+    code = "import torch\ntorch.__version__ = '1.0.0'\n" + ALLOCATE + "\nassert not hasattr(stq._lib._tensor, 'torch_version')\n"
+    assert _import_alone(tmp_path / "c", code, ("libstq.so", "_tensor.so")) == want
+
+
+def test_import_without_torch(tmp_path):
+    want = _import_alone(tmp_path, ALLOCATE, ("libstq.so", "_tensor.so"))
+    (tmp_path / "b").mkdir()
+    assert _import_alone(tmp_path / "b", "import sys\nsys.modules['torch'] = None\n" + ALLOCATE, ("libstq.so", "_tensor.so")) == want
