@@ -396,6 +396,13 @@ def _heads(t, what, n, heads, d, index):
     return t.data_ptr(), st if a > 1 else b * c     # one shorter than a token is the library's to refuse
 
 
+def _there(**tensors):
+    """Refuses arguments whose sizes a call reads but that were left out."""
+    for what, t in tensors.items():
+        if t is None:
+            raise StqError(-1, "%s is missing" % what)
+
+
 def _i32(*sizes):
     """Sizes that C takes in 32 bits (ctypes would drop the rest in silence)."""
     for x in sizes:
@@ -450,6 +457,8 @@ def stq_kv_plan(cached, new, free, table, block_tokens, n_blocks, tok_start, len
     """cached, new int32 [n]; free int32; table int32 [n][cols], updated in place;
     outputs tok_start int32 [n+1], lens int32 [n], pos int32 [tokens], slots int64
     [tokens], used int32 [1]."""
+    if table is None or pos is None or free is None:
+        _there(table=table, pos=pos, free=free)
     i, dev = torch.int32, table.get_device()
     if table.dim() != 2:
         raise StqError(-1, "table must be [requests][columns]")
@@ -500,6 +509,8 @@ def stq_qk_norm_rope(q, k, q_out, k_out, norm=STQ_NORM_RMS, eps=1e-6, q_weight=N
 
 def stq_kv_store(kv, slots, k, v, stream=None):
     """slots int64 [tokens]; k, v [tokens][n_kv_heads][d] of one element type."""
+    if slots is None:
+        _there(slots=slots)
     n, dev = slots.numel(), kv.index
     _i32(n)
     kp, ks = _heads(k, "k", n, kv.n_kv_heads, kv.d, dev)
@@ -512,6 +523,8 @@ def stq_kv_store(kv, slots, k, v, stream=None):
 
 def stq_kv_fetch(kv, slots, k_out, v_out, stream=None):
     """slots int64 [tokens]; k_out, v_out contiguous [tokens][n_kv_heads][d] of one element type."""
+    if slots is None or k_out is None:
+        _there(slots=slots, k_out=k_out)
     n, dev = slots.numel(), kv.index
     _i32(n)
     want, ty = n * kv.n_kv_heads * kv.d, k_out.dtype
@@ -531,7 +544,7 @@ def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, win
     [requests]; q, o [tokens][n_heads][d], bfloat16 or float16; work: uint8
     tensor of at least stq_kv_attend_bytes(...) bytes (None where that is 0)."""
     i, dev = torch.int32, kv.index
-    if table.dim() != 2:
+    if table is None or table.dim() != 2:
         raise StqError(-1, "table must be [requests][columns]")
     n, cols = table.shape
     qp, qs = _heads(q, "q", None, None, kv.d, dev)

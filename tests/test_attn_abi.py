@@ -376,3 +376,27 @@ def test_import_without_torch(tmp_path):
     want = _import_alone(tmp_path, ALLOCATE, ("libstq.so", "_tensor.so"))
     (tmp_path / "b").mkdir()
     assert _import_alone(tmp_path / "b", "import sys\nsys.modules['torch'] = None\n" + ALLOCATE, ("libstq.so", "_tensor.so")) == want
+
+
+def test_binding_refuses_what_was_left_out(stq, monkeypatch):
+    """None for any tensor that a call has to have is a StqError."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    b, i, l = torch.bfloat16, torch.int32, torch.int64
+    kv = stq.make_kv(Fake([10 * 2 * 64 * 136], torch.uint8), 64, 2, 128)
+    x, y = Fake([4, 2, 128], b), Fake([4, 2, 128], b, ptr=0x20000)
+    calls = ((stq.stq_kv_plan, dict(cached=Fake([2], i), new=Fake([2], i), free=Fake([9], i), table=Fake([2, 5], i), block_tokens=48,
+                                    n_blocks=10, tok_start=Fake([3], i), lens=Fake([2], i), pos=Fake([7], i), slots=Fake([7], l),
+                                    used=Fake([1], i)), ("block_tokens", "n_blocks")),
+             (stq.stq_kv_store, dict(kv=kv, slots=Fake([4], l), k=x, v=x), ("kv",)),
+             (stq.stq_kv_fetch, dict(kv=kv, slots=Fake([4], l), k_out=x, v_out=y), ("kv",)),
+             (stq.stq_kv_attend, dict(kv=kv, table=Fake([2, 5], i), tok_start=Fake([3], i), lens=Fake([2], i), q=x, o=y, scale=0.1,
+                                      max_new=2, max_len=100), ("kv", "max_new", "max_len", "scale")),
+             (stq.stq_qk_norm_rope, dict(q=x, k=x, q_out=y, k_out=y, pos=Fake([4], i), cos_sin=Fake([9, 64], torch.float32)), ("k",)))
+    for call, args, skip in calls:
+        for name in args:
+            if name not in skip:
+                with pytest.raises(stq.StqError):
+                    call(**dict(args, **{name: None}), stream=0)
+    with pytest.raises(stq.StqError):
+        stq.make_kv(None, 64, 2, 128)
