@@ -1558,12 +1558,16 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
     k = least(few > many ? few : many, MOST_SPLITS);
     if (k < 1) k = 1;
   }
-  // One workgroup a CU or fewer, and not much for each: sixteen waves and no
-  // second launch (1 x 500 tokens 8.5 -> 7.9 us, 32 x 1,000 14.1 -> 11.8; 1 x
-  // 1,021 8.6 -> 9.5 but 2.5 us less on the host; 8 x 2,000 would lose, 12.1 ->
-  // 13.4, and so would up to 8 chunks, 5.4 -> 6.2).
+  // One workgroup a CU or fewer, and requests that would be split in two (in up to
+  // five where the workgroups are half the CUs and more): sixteen waves and no
+  // second launch.  Below that four waves need none either.  Four waves against
+  // sixteen, us on the GPU, 8 heads, d = 128: 1 request of 640 tokens 6.9, 7.7;
+  // 736 7.6, 8.0; 768 8.1, 8.0; 960 8.7, 8.8 (a call 9.9, 8.8); 1,100 9.3, 9.1;
+  // 1,216 8.7, 9.4; 1,500 8.9, 10.6.  32 requests of 736 9.1, 9.7; 768 11.6, 9.8; 2,000
+  // 16.9, 14.1; 16 of 640 7.3, 8.1; 1,100 10.5, 10.1; 1,900 12.7, 12.5; 2,048 12.9,
+  // 13.1.  (d = 64 gains from 640 on: 20 requests of 640 6.3, 6.2, of 2,048 11.9, 10.3.)
   s.waves = 4;
-  if (s.tile_rows == 16 && base <= CUS && chunks > 8 && chunks <= (2 * base >= CUS ? 64 : 32)) {
+  if (s.tile_rows == 16 && base <= CUS && chunks >= 2 * FEW_CHUNKS && chunks < (2 * base >= CUS ? 65 : 3 * FEW_CHUNKS)) {
     s.waves = 16;
     k = 1;
   }

@@ -858,3 +858,26 @@ def test_attend_long_requests(stq, dtype, heads, d, new, L):
     for hint in (1, L):
         B.check(B.run(max_len=hint))
     B.check(B.run(window=L - 5000, sink=100, max_len=1), L - 5000, 100)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,kv,d,T,longest,new", [(8, 2, 128, 64, 768, 1), (6, 2, 64, 32, 1120, 1), (16, 1, 128, 256, 1021, 1),
+                                                      (8, 2, 64, 128, 1100, 4), (3, 3, 128, 32, 900, 5), (64, 16, 128, 64, 2048, 1)])
+def test_attend_sixteen_waves(stq, dtype, heads, kv, d, T, longest, new):
+    """Requests that one workgroup of sixteen waves takes whole: no workspace; lengths from nothing to the
+    longest, windows, a block outside the cache, a token that holds a NaN."""
+    import torch
+    lens = [longest, 0, 1, 33, 700, 511, longest - 1, 95]
+    B = Batch(stq, lens, [min(new, n) for n in lens], heads, kv, d, T, dtype, seed=longest, pad=2)
+    assert stq.stq_kv_attend_bytes(B.kvc, len(lens), B.tok, heads, new, longest) == 0
+    B.check(B.run())
+    B.check(B.run(window=longest - 9, sink=2), longest - 9, 2)
+    B.table[4, 1] = -1
+    slot = np.array([B.table[0, 600 // T] * T + 600 % T], np.int64)
+    k, v = torch.ones(1, kv, d, device="cuda"), torch.ones(1, kv, d, device="cuda")
+    k[0, kv - 1, 3] = float("nan")
+    stq.stq_kv_store(B.kvc, cu(slot), k, v)
+    o = B.run()
+    B.check(o)
+    g = heads // kv
+    assert np.isnan(host(o)[0, -g:]).all() and not np.isnan(host(o)[0, :-g]).any() and not np.isnan(host(o)[B.start[1]:]).any()
