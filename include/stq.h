@@ -492,8 +492,10 @@ typedef struct stq_norm_desc {
  * cosines, then the n_rot/2 sines; pair (x, y) becomes (x cos - y sin,
  * y cos + x sin).  Rows of a token whose position lies outside [0, n_pos)
  * (a padded batch) are left as they were.  Outputs may be the inputs
- * themselves (same pointer, type and stride), else they must not overlap them.  Pointers 16-byte aligned,
- * strides a multiple of 16 bytes, else STQ_ERR_LAYOUT. */
+ * themselves (same pointer, type and stride), else they must not overlap them
+ * or each other (STQ_ERR_ARG; rows side by side in one buffer do not).
+ * Pointers 16-byte aligned, strides a multiple of 16 bytes, else
+ * STQ_ERR_LAYOUT. */
 stq_status stq_qk_norm_rope(const stq_norm_desc* desc, const void* q_dev, const void* k_dev,
                             const float* q_weight_dev, const float* k_weight_dev, const int32_t* pos_dev,
                             const float* cos_sin_dev, void* q_out_dev, void* k_out_dev, hipStream_t stream);
@@ -545,8 +547,9 @@ size_t stq_kv_attend_bytes(const stq_kv_desc* desc, const stq_attend_desc* a);
  * aligned with strides a multiple of 16 bytes, the workspace 16-byte aligned,
  * else STQ_ERR_LAYOUT.  STQ_ERR_UNSUPPORTED for calls larger than a launch:
  * n_req * max_new * n_heads from 2^31 on, or n_req * n_kv_heads (times the
- * query rows' tiles and the splits) from 2^24 on.  A workspace serves one call at a time.  o must not
- * overlap q.  Products run on the matrix cores in binary16 (cached values and
+ * query rows' tiles and the splits) from 2^24 on.  A workspace serves one call
+ * at a time.  o may be q itself (same pointer and stride), else it must not
+ * overlap q (STQ_ERR_ARG).  Products run on the matrix cores in binary16 (cached values and
  * queries exact, the queries scaled by a power of two per row; softmax
  * weights rounded to binary16, for bfloat16 outputs cut to it: off by 2^-10
  * of themselves, or by 2^-31 of the row's largest where they are below 2^-21

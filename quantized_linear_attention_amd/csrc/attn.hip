@@ -812,18 +812,6 @@ __device__ __forceinline__ void value_products(const Chunk<D>& C, bool full, con
   }
 }
 
-// Few query rows per key/value head (a token's head group, drafted tokens):
-// the cache's bytes bound the work, so nothing is staged.  One workgroup =
-// one (request, head, tile of 16 NT rows, split of the cache); its NWV
-// waves take every NWV-th chunk straight from memory into the operands'
-// registers and join their running softmaxes through LDS at the end.
-// Measured (32 heads over 8, d = 128, one token): 8 requests of 32,768 to
-// 131,072 tokens 147 us for 777 MB of codes and scales = 5.3 TB/s; 64 of 2,048 to
-// 8,191 tokens 71 us = 5.1 TB/s (a plain read past the caches runs at 7.0, a
-// copy at 5.16; the vector units are busy 40 % of the time, the rest is the
-// chain of a chunk: keys, products, weights, products); one of 1,021 tokens
-// 8.9 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
-// requests: 17.1 us, bound by the instructions and the chain of two waves a SIMD.
 // o *= f of tile nt where any lane of `far` is set (accumulators of 16 rows and
 // D channels: D/4 registers)
 template <int D, int NT>
@@ -845,6 +833,18 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
   }
 }
 
+// Few query rows per key/value head (a token's head group, drafted tokens):
+// the cache's bytes bound the work, so nothing is staged.  One workgroup =
+// one (request, head, tile of 16 NT rows, split of the cache); its NWV
+// waves take every NWV-th chunk straight from memory into the operands'
+// registers and join their running softmaxes through LDS at the end.
+// Measured (32 heads over 8, d = 128, one token): 8 requests of 32,768 to
+// 131,072 tokens 147 us for 777 MB of codes and scales = 5.3 TB/s; 64 of 2,048 to
+// 8,191 tokens 71 us = 5.1 TB/s (a plain read past the caches runs at 7.0, a
+// copy at 5.16; the vector units are busy 40 % of the time, the rest is the
+// chain of a chunk: keys, products, weights, products); one of 1,021 tokens
+// 8.9 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
+// requests: 17.1 us, bound by the instructions and the chain of two waves a SIMD.
 template <int D, int TYPE, int NT, int NWV, bool ONCE>
 __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(AttnArgs A) {
   constexpr int NC = D / 16;
@@ -1507,6 +1507,18 @@ int elem_bytes(int type) { return type == STQ_FP32 ? 4 : 2; }
 bool stride_ok(int64_t stride, int64_t least, int type) {
   return stride >= least && stride < (1ll << 40) && (stride * elem_bytes(type)) % 16 == 0;
 }
+// n rows of `bytes` bytes each, `step` bytes apart
+struct Rows { const void* p; int64_t step, bytes; };
+// Whether two tensors of n rows share a byte.  Rows of one buffer side by side
+// (one step) are told apart exactly; with two steps, ranges that meet count.
+bool meet(const Rows& a, const Rows& b, int64_t n) {
+  const int64_t x = (int64_t)(uintptr_t)a.p, y = (int64_t)(uintptr_t)b.p;
+  if (x + (n - 1) * a.step + a.bytes <= y || y + (n - 1) * b.step + b.bytes <= x) return false;
+  if (a.step != b.step) return true;
+  const int64_t gap = ((y - x) % a.step + a.step) % a.step;      // from a row of a to the next of b
+  return gap < a.bytes || gap > a.step - b.bytes;
+}
+bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.step == b.step && a.bytes == b.bytes; }
 stq_status launched() { return hipGetLastError() == hipSuccess ? STQ_OK : STQ_ERR_HIP; }
 
 bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
@@ -1695,8 +1707,12 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   if (d->n_k_heads > 0 && (!aligned(k) || !aligned(ko) || !stride_ok(d->k_stride, kw, d->in_type) ||
                            !stride_ok(d->k_out_stride, kw, d->out_type)))
     return STQ_ERR_LAYOUT;
-  if ((q == qo && (d->q_stride != d->q_out_stride || d->in_type != d->out_type)) ||
-      (d->n_k_heads > 0 && k == ko && (d->k_stride != d->k_out_stride || d->in_type != d->out_type)))
+  const int ib = elem_bytes(d->in_type), ob = elem_bytes(d->out_type);
+  const Rows rq = {q, d->q_stride * ib, qw * ib}, rqo = {qo, d->q_out_stride * ob, qw * ob}, rk = {k, d->k_stride * ib, kw * ib},
+             rko = {ko, d->k_out_stride * ob, kw * ob};
+  if (!same(rq, rqo) && meet(rq, rqo, d->n_tok)) return STQ_ERR_ARG;
+  if (d->n_k_heads > 0 && ((!same(rk, rko) && meet(rk, rko, d->n_tok)) || meet(rk, rqo, d->n_tok) || meet(rq, rko, d->n_tok) ||
+                           meet(rqo, rko, d->n_tok)))
     return STQ_ERR_ARG;
   NormArgs A;
   A.q = q; A.k = k; A.qo = qo; A.ko = ko; A.wq = wq; A.wk = wk; A.cs = cos_sin; A.pos = pos;
@@ -1709,7 +1725,6 @@ stq_status stq_qk_norm_rope(const stq_norm_desc* d, const void* q, const void* k
   A.per_tok = (int)((NORM_WAVES + A.n_tok - 1) / A.n_tok);
   if (A.per_tok > (sets + 1) / 2) A.per_tok = (sets + 1) / 2;
   A.by_per_tok = div_of(A.per_tok);
-  const int ib = elem_bytes(d->in_type), ob = elem_bytes(d->out_type);
   const int64_t slice = A.per_tok > 1 ? d->n_tok : 4 * MOST_GROUPS;     // (several waves a token: 16,384 waves at most)
   for (int64_t t = 0; t < d->n_tok; t += slice) {
     A.n_tok = (int)(d->n_tok - t < slice ? d->n_tok - t : slice);
@@ -1778,6 +1793,8 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   const int64_t w = (int64_t)a->n_heads * d->d;
   if (!aligned(q) || !aligned(o) || !stride_ok(a->q_stride, w, a->type) || !stride_ok(a->o_stride, w, a->type))
     return STQ_ERR_LAYOUT;
+  const Rows rq = {q, a->q_stride * 2, w * 2}, ro = {o, a->o_stride * 2, w * 2};
+  if (!same(rq, ro) && meet(rq, ro, a->n_tok)) return STQ_ERR_ARG;
   const Split sp = split_of(d, a);
   const size_t need = stq_kv_attend_bytes(d, a);
   if (need > 0 && (!work || !aligned(work) || work_bytes < need)) return STQ_ERR_LAYOUT;

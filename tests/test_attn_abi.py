@@ -400,3 +400,25 @@ def test_binding_refuses_what_was_left_out(stq, monkeypatch):
                     call(**dict(args, **{name: None}), stream=0)
     with pytest.raises(stq.StqError):
         stq.make_kv(None, 64, 2, 128)
+
+
+def test_calls_refuse_outputs_over_inputs(L):
+    """Outputs that share bytes with an input, or with each other, and are not the input itself."""
+    kv = kvd(n_kv_heads=2)
+    full = L.stq_kv_bytes(ctypes.byref(kv))
+    w = 4 * 128 * 2                                       # bytes of a token's four heads
+
+    def attend(q, o, **kw):
+        return L.stq_kv_attend(ctypes.byref(kv), D, full, ctypes.byref(ad(**kw)), D, D, D, P(q), P(o), None, 0, None)
+    q = 0x100000
+    for o, kw in ((q + 16, {}), (q - 16, {}), (q + w, {}), (q + 2 * w + 16, {}), (q, dict(o_stride=1024)), (q + w - 16, dict(q_stride=1024, o_stride=1024)),
+                  (q + 3 * w + 16, dict(q_stride=1024, o_stride=1024)), (q + w, dict(q_stride=1024))):
+        assert attend(q, o, **kw) == -1, (hex(o), kw)
+
+    def norm(kw, q=0x100000, k=0x200000, qo=0x300000, ko=0x400000):
+        return L.stq_qk_norm_rope(ctypes.byref(nd(**kw)), P(q), P(k), None, None, D, D, P(qo), P(ko), None)
+    for kw, at in (({}, dict(qo=0x100010)), ({}, dict(qo=0x100000 - 16)), ({}, dict(ko=0x200000 + 512)), ({}, dict(ko=0x100000)),
+                   ({}, dict(qo=0x200000)), ({}, dict(ko=0x300000 + 2 * w)), (dict(out_type=2, q_out_stride=512), dict(qo=0x100000)),
+                   (dict(q_out_stride=520), dict(qo=0x100000)), (dict(n_tok=1), dict(qo=0x100000 + w - 16)),
+                   (dict(out_type=2), dict(qo=0x100000 + 3 * w - 16))):
+        assert norm(kw, **at) == -1, (kw, at)

@@ -881,3 +881,24 @@ def test_attend_sixteen_waves(stq, dtype, heads, kv, d, T, longest, new):
     B.check(o)
     g = heads // kv
     assert np.isnan(host(o)[0, -g:]).all() and not np.isnan(host(o)[0, :-g]).any() and not np.isnan(host(o)[B.start[1]:]).any()
+
+
+@pytest.mark.parametrize("lens,news", [([100, 64, 7], [3, 1, 9]), ([5000, 31], [1, 2]), ([300, 200], [70, 130]), ([5000, 40], [40, 1])])
+def test_attend_in_place(stq, lens, news):
+    """Output rows in the place of the queries, also as views of one wider buffer; next to them in the
+    same rows; any other overlap is refused."""
+    import torch
+    B = Batch(stq, lens, news, 4, 2, 64, 32, "bf16", seed=len(lens), pad=1)
+    want = B.run()
+    wide = torch.full((B.tok, 9, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    for first in (1, 5):
+        wide[:, 1:5] = B.q
+        wide[:, 5:] = 5
+        q, o = wide[:, 1:5], wide[:, first:first + 4]
+        B.run(q=q, o=o)
+        n = int(B.start[-1])
+        assert torch.equal(o[:n], want[:n]) and torch.equal(o[n:], B.q[n:] if first == 1 else want[n:])
+        assert (wide[:, 0] == 5).all() and (first == 5 or (wide[:, 5:] == 5).all())
+    for bad in (wide[:, 2:6], wide[:, :4]):
+        with pytest.raises(stq.StqError):
+            B.run(q=wide[:, 1:5], o=bad)
