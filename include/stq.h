@@ -520,7 +520,15 @@ stq_status stq_kv_fetch(const stq_kv_desc* desc, const void* cache_dev, size_t b
  * at position p = len[i] - (tok_start[i+1] - tok_start[i]) + j.  It sees cached
  * position s when s <= p and (window == 0, or s > p - window, or s < n_sink).
  *   o = sum_s softmax_s(scale * q . k_s) v_s, query head h reading key/value
- *   head h / (n_heads / n_kv_heads); a query that sees nothing gets 0. */
+ *   head h / (n_heads / n_kv_heads); a query that sees nothing gets 0.
+ *
+ * One kernel and one split of the work serve a whole call, by max_new and
+ * max_len.  Requests of one or a few new tokens therefore belong in a call of
+ * their own, apart from prompts: with requests a .. b-1 side by side, the call
+ * takes table + a * table_cols, tok_start + a, len + a, n_req = b - a and the
+ * same q, o and n_tok.  (32 heads over 8, d = 128, a prompt of 2,048 tokens with
+ * 63 requests of 2,048 to 8,191: 136 us in two calls, 270 in one; with 8 of
+ * 32,768 to 131,072: 212 us, 2,690 in one.) */
 typedef struct stq_attend_desc {
   int32_t n_req;            /* requests (>= 0)                                */
   int32_t n_tok;            /* rows of q and o, 0 .. 2^28 (a padded batch may   */

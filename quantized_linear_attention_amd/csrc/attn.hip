@@ -707,8 +707,8 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
 // weights: binary16 is subnormal below 2^-14, with steps of 2^-24, so without it
 // thousands of tokens at 2^-20 of a dominant one (16 nats) lose much of their sum
 // (16,390 tokens 14 nats below four: outputs off by 3.7 %, by 48 % at 16.6 nats).
-// With it weights are normal down to 2^-21 of the largest, and below that off by
-// 2^-31 of it at most.
+// With it weights are normal down to 2^-21 of the largest at least, and below that
+// off by 2^-31 of it at most.
 constexpr float LIFT = 7.0f, MOVE = 8.0f;
 struct Ref {
   float m, mc, over;       // the product it stands at, times c; products above `over` move it
@@ -844,7 +844,11 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
 // copy at 5.16; the vector units are busy 40 % of the time, the rest is the
 // chain of a chunk: keys, products, weights, products); one of 1,021 tokens
 // 8.9 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
-// requests: 17.1 us, bound by the instructions and the chain of two waves a SIMD.
+// requests: 17.1 us, of which the vector units are busy 31 %: two waves a SIMD, and
+// each chunk of a wave waits for its own loads.  Rows from 17 on: 16 requests of
+// up to 8,192 tokens 24 rows 40 us, 36 rows 41, 64 rows 60 (the bytes take 17 to 20):
+// at 191 registers two workgroups a CU, and each tile of 32 rows reads and
+// unpacks the cache for itself.
 template <int D, int TYPE, int NT, int NWV, bool ONCE>
 __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(AttnArgs A) {
   constexpr int NC = D / 16;
@@ -1070,7 +1074,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
 // address (lane 4t + c: channels 4c.. of token t).
 //
 // Measured (4 prompts of 1,078 to 2,048 tokens over up to 2,048 cached ones, 32
-// heads over 8, d = 128): 228 us = 938 TFLOP/s (237 on a card that clocks lower), where a library product of
+// heads over 8, d = 128): 236 us = 905 TFLOP/s (226 to 238 by the card's clocks), where a library product of
 // 8,192 x 8,192 x 8,192 in binary16 runs at 1,150.  A tile costs a wave about
 // 1,000 cycles of matrix instructions and as many of vector ones (32 exp2 at
 // half rate, the conversions, the sums), which share the SIMD's issue with the
@@ -1521,6 +1525,9 @@ bool meet(const Rows& a, const Rows& b, int64_t n) {
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.step == b.step && a.bytes == b.bytes; }
 stq_status launched() { return hipGetLastError() == hipSuccess ? STQ_OK : STQ_ERR_HIP; }
 
+// Positions lie in [-2^28, 2^30): a window of 2^30 is no limit, and the kernels'
+// differences of the two stay in 32 bits.
+constexpr int32_t MOST_WINDOW = 1 << 30;
 bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
   return a && a->n_req >= 0 && a->n_tok >= 0 && a->n_tok <= (1 << 28) && a->n_heads >= 1 && a->n_heads % d->n_kv_heads == 0 &&
          a->n_heads <= 65536 && (a->type == STQ_BF16 || a->type == STQ_FP16) && a->table_cols >= 1 &&
@@ -1530,9 +1537,10 @@ bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
 struct Split { int tiles, tile_rows, splits, per, waves; bool staged, once; };
 // Query rows per key/value head up to which each wave unpacks the cache for
 // itself, 32 rows at a time; above, it is staged through LDS for 128 rows (16
-// requests of up to 8,192 tokens, 8 heads: 36 rows 43 against 89 us staged, 64
-// rows 62 against 95, 128 rows 99 staged alike; 64 requests of up to 2,048:
-// 64 rows 54 against 63, 96 rows 67 against 62, 128 rows 84 against 67).
+// requests of up to 8,192 tokens, 8 heads, d = 128: 36 rows 41 against 63 us
+// staged, 64 rows 60 against 67, 96 rows 76 against 70, 128 rows 90 against 76;
+// 64 requests of up to 2,048: 64 rows 54 against 62, 96 rows 67 against 63; d = 64,
+// 16 requests: 64 rows 45 against 58, 96 rows 56 against 60, 128 rows 68 against 63).
 constexpr int STAGED_ROWS = 64;
 // A part of a request's work has its own start (three dependent loads) and end
 // (the joins), about 5 us.  Few workgroups are split down to 12 chunks, three a
@@ -1549,7 +1557,6 @@ constexpr int STAGED_ROWS = 64;
 // MB of pages 78 -> 73 us, 1.1 GB 161 -> 146, three times the rows per head 109
 // -> 106; 139 MB, which the next call finds again, 22.4 -> 23.1; d = 64, whose
 // loads cover half lines, 50 -> 54 and stays as it is).
-constexpr int32_t MOST_WINDOW = 1 << 30;
 constexpr int64_t LAST_CACHE_BYTES = 256 << 20;
 constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
@@ -1807,7 +1814,6 @@ stq_status stq_kv_attend(const stq_kv_desc* d, const void* cache, size_t bytes, 
   A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.q = q; A.o = o;
   A.n_req = a->n_req; A.n_tok = a->n_tok; A.hq = a->n_heads; A.hkv = d->n_kv_heads; A.group = a->n_heads / d->n_kv_heads;
   A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = a->table_cols; A.max_new = a->max_new;
-  // positions lie in (-2^28, 2^30): a window past that is no limit, and the kernels' differences of the two stay in 32 bits
   A.window = a->window < MOST_WINDOW ? a->window : MOST_WINDOW;
   A.sink = a->n_sink < MOST_WINDOW ? a->n_sink : MOST_WINDOW;
   A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles;

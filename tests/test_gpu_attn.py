@@ -902,3 +902,23 @@ def test_attend_in_place(stq, lens, news):
     for bad in (wide[:, 2:6], wide[:, :4]):
         with pytest.raises(stq.StqError):
             B.run(q=wide[:, 1:5], o=bad)
+
+
+def test_attend_parts_of_a_batch(stq):
+    """Running requests and prompts in calls of their own on slices of one plan: every row as the reference has
+    it, and no row of the other part touched."""
+    import torch
+    news = [1, 3, 1, 2, 140, 60]
+    B = Batch(stq, [700, 33, 1, 95, 140, 333], news, 4, 2, 64, 32, "bf16", seed=3, pad=2)
+    i = torch.int32
+    table, start, lens = cu(B.table, i), cu(B.start, i), cu(B.lens, i)
+    B.check(B.run())
+    o = torch.full_like(B.q, 5.0)
+    for a, b in ((4, 6), (0, 4)):
+        most, longest = int(B.news[a:b].max()), int(B.lens[a:b].max())
+        size = stq.stq_kv_attend_bytes(B.kvc, b - a, B.tok, 4, most, longest)
+        stq.stq_kv_attend(B.kvc, table[a:b], start[a:b + 1], lens[a:b], B.q, o, B.scale, most, longest,
+                          work=torch.empty(size, dtype=torch.uint8, device="cuda") if size else None)
+        if a:
+            assert (o[:B.start[a]] == 5).all()
+    B.check(o)
