@@ -844,7 +844,7 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
 // copy at 5.16; the vector units are busy 40 % of the time, the rest is the
 // chain of a chunk: keys, products, weights, products); one of 1,021 tokens
 // 8.9 us.  Three tokens of 8 heads each over windows of 1,024 at d = 64, 128
-// requests: 17.1 us, of which the vector units are busy 31 %: two waves a SIMD, and
+// requests: 17.1 us, the vector units busy 29 % of them: two waves a SIMD, and
 // each chunk of a wave waits for its own loads.  Rows from 17 on: 16 requests of
 // up to 8,192 tokens 24 rows 40 us, 36 rows 41, 64 rows 60 (the bytes take 17 to 20):
 // at 191 registers two workgroups a CU, and each tile of 32 rows reads and
