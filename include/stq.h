@@ -566,6 +566,115 @@ stq_status stq_kv_attend(const stq_kv_desc* desc, const void* cache_dev, size_t 
                          const int32_t* table_dev, const int32_t* tok_start_dev, const int32_t* len_dev,
                          const void* q_dev, void* o_dev, void* work_dev, size_t work_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * LONG CONTEXTS.  Two ways to read less of a long cache than all of it once
+ * per request: attention over the blocks that a cheap score selects for each
+ * query (stq_kv_bounds, stq_kv_score, stq_kv_select, stq_kv_attend_blocks), and
+ * attention of requests that share a prefix, which is read once for all of
+ * them (stq_kv_attend_shared).  All take a ragged batch as stq_kv_attend does:
+ * table, tok_start, len, max_new and rows of q mean the same, and query j of
+ * request i sits at p = len[i] - (tok_start[i+1] - tok_start[i]) + j; rows and
+ * tokens outside of any request, and queries past max_new, are left alone.
+ * Their stq_attend_desc has window = n_sink = 0 (else STQ_ERR_ARG).
+ *
+ * BOUNDS: per block b, key/value head h and channel c the least and the largest
+ * key of the block, as E5M2 (the upper byte of a binary16; 0x7F for NaN),
+ * rounded down and up; bytes of block b, head h at (b * n_kv_heads + h) * 2d:
+ * the d lower bounds, then the d upper ones.  Cached keys need two of E5M2's
+ * three significant bits, so bounds of 2^-14 and more are keys of the block
+ * exactly; smaller ones round to a multiple of 2^-16.  */
+
+/* Bytes of the bounds' device buffer (16-byte aligned); 0 for an invalid
+ * description.  Needs no initialisation: a block's bounds are written when its
+ * tokens are. */
+size_t stq_kv_bounds_bytes(const stq_kv_desc* desc);
+
+/* Bounds of the blocks that hold new tokens, after stq_kv_store: of request i
+ * those that hold positions len[i] - (tok_start[i+1] - tok_start[i]) .. len[i] - 1
+ * (of the first max_new of them), from all tokens of the block below len[i].
+ * Every other block's bounds are left as they were, and blocks whose table entry
+ * lies outside [0, n_blocks) have none.  A block that holds new tokens must
+ * belong to one request.  A block with a poisoned key (one stored with NaN
+ * scales) gets NaN bounds.  STQ_ERR_UNSUPPORTED from 2^24 (request, block)
+ * pairs on that max_new makes possible: n_req * min((max_new - 1) /
+ * block_tokens + 2, table_cols). */
+stq_status stq_kv_bounds(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, int32_t n_req, int32_t max_new,
+                         const int32_t* table_dev, int32_t table_cols, const int32_t* tok_start_dev,
+                         const int32_t* len_dev, void* bounds_dev, hipStream_t stream);
+
+/* Scores of the blocks that a query sees (those with block_tokens * b <= p):
+ *   score[t][h][b] = max over the query heads g of key/value head h of
+ *                    sum_c max(x_c lo_c, x_c hi_c),  x = scale * q[t][g],
+ * which no logit of the block exceeds.  score_dev: fp32 [n_tok][n_kv_heads][table_cols];
+ * blocks outside the cache get -inf, blocks with NaN bounds NaN, columns behind
+ * p's block are left as they were.  max_len sets the split of the work, never the
+ * result; o_stride is not used.  Products are exact (queries scaled by a power
+ * of two per row), sums binary32.  score may overlap neither q nor the bounds
+ * (STQ_ERR_ARG).  STQ_ERR_UNSUPPORTED from n_req * n_kv_heads = 2^24 on and from
+ * 65,536 tiles of a request's tokens on (16 query rows each, 64 where max_new
+ * needs more than one). */
+stq_status stq_kv_score(const stq_kv_desc* desc, const stq_attend_desc* a, const void* bounds_dev,
+                        const int32_t* table_dev, const int32_t* tok_start_dev, const int32_t* len_dev,
+                        const void* q_dev, float* score_dev, hipStream_t stream);
+
+typedef struct stq_select_desc {
+  int32_t n_req;            /* requests (>= 0)                                */
+  int32_t n_tok;            /* rows of score and sel, 0 .. 2^28               */
+  int32_t n_kv_heads;       /* >= 1                                           */
+  int32_t block_tokens;     /* 32, 64, 128 or 256                             */
+  int32_t table_cols;       /* columns of score, 1 .. 32,768                  */
+  int32_t n_sel;            /* columns of sel (>= 1)                          */
+  int32_t n_first, n_last;  /* blocks always taken; their sum at most n_sel   */
+  int32_t max_new;          /* as in stq_attend_desc                          */
+} stq_select_desc;
+
+/* Selection: of each token and head the first n_first and the last n_last blocks
+ * that the token sees, and of the others those with the highest scores, up to
+ * n_sel together; equal scores by the lower index, NaN above all numbers, -inf
+ * never taken.  sel_dev int32 [n_tok][n_kv_heads][n_sel]: their columns in
+ * ascending order, then -1.  Whole numbers from comparisons: the same scores give
+ * the same selection.  sel must not overlap score (STQ_ERR_ARG).
+ * STQ_ERR_UNSUPPORTED past 32,768 columns, from n_req * max_new * n_kv_heads =
+ * 2^31 on and from 2^32 threads on (a row takes 64, 256 past 512 columns and
+ * 1,024 past 2,048). */
+stq_status stq_kv_select(const stq_select_desc* c, const int32_t* tok_start_dev, const int32_t* len_dev,
+                         const float* score_dev, int32_t* sel_dev, hipStream_t stream);
+
+/* Attention over listed blocks: as stq_kv_attend, but query t sees, through key/
+ * value head h, cached position s only where column s / block_tokens of its
+ * request's table is one of sel[t][h][0 .. n_sel-1].  Entries outside [0,
+ * table_cols), and blocks wholly behind p, stand for nothing; one that is listed
+ * twice counts twice.  max_len is not used.  Errors, overlap and roundings as
+ * stq_kv_attend; o must not overlap sel (STQ_ERR_ARG); sel 16-byte aligned. */
+size_t stq_kv_attend_blocks_bytes(const stq_kv_desc* desc, const stq_attend_desc* a, int32_t n_sel);
+stq_status stq_kv_attend_blocks(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, const stq_attend_desc* a,
+                                int32_t n_sel, const int32_t* table_dev, const int32_t* tok_start_dev,
+                                const int32_t* len_dev, const int32_t* sel_dev, const void* q_dev, void* o_dev,
+                                void* work_dev, size_t work_bytes, hipStream_t stream);
+
+typedef struct stq_shared_desc {
+  int32_t n_groups;         /* >= 0                                           */
+  int32_t max_prefix;       /* about the longest prefix: sets the split of the */
+                            /* work, never the result                         */
+} stq_shared_desc;
+
+/* Attention of requests that share prefixes: the result of stq_kv_attend (without
+ * a window).  Requests group_start[g] .. group_start[g+1]-1 share their first
+ * prefix[g] tokens: the leading entries of their table rows are the same blocks,
+ * of which the group's first row is read.  Only whole blocks are shared (prefix
+ * is cut to a multiple of block_tokens), and none behind the first new token of
+ * any of the group's requests: what lies there counts as each request's own.
+ * group_start int32 [n_groups + 1], non-decreasing; requests before
+ * group_start[0] or from group_start[n_groups] on are in no group.  In the
+ * descriptor max_len is about the longest own part (len minus prefix): it sets
+ * the split of the work, never the result.  The workspace is always needed.
+ * Errors, overlap and roundings as stq_kv_attend. */
+size_t stq_kv_attend_shared_bytes(const stq_kv_desc* desc, const stq_attend_desc* a, const stq_shared_desc* g);
+stq_status stq_kv_attend_shared(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, const stq_attend_desc* a,
+                                const stq_shared_desc* g, const int32_t* table_dev, const int32_t* tok_start_dev,
+                                const int32_t* len_dev, const int32_t* group_start_dev, const int32_t* prefix_dev,
+                                const void* q_dev, void* o_dev, void* work_dev, size_t work_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

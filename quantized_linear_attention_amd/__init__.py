@@ -13,4 +13,6 @@ from ._lib import (  # noqa: F401
     STQ_BF16, STQ_FP16, STQ_FP32, STQ_NORM_L2, STQ_NORM_NONE, STQ_NORM_RMS, STQ_ROT_ADJACENT, STQ_ROT_HALVES,
     make_kv, stq_kv_attend, stq_kv_attend_bytes, stq_kv_bytes, stq_kv_fetch, stq_kv_plan, stq_kv_store,
     stq_qk_norm_rope,
+    stq_kv_attend_blocks, stq_kv_attend_blocks_bytes, stq_kv_attend_shared, stq_kv_attend_shared_bytes,
+    stq_kv_bounds, stq_kv_bounds_bytes, stq_kv_score, stq_kv_select,
 )

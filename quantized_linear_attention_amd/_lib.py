@@ -1,5 +1,6 @@
 """ctypes marshalling for libstq.so (no computation happens here); _tensor.so, where it is there, checks tensor arguments."""
 import ctypes
+import operator
 import os
 import struct
 
@@ -52,6 +53,15 @@ class _AttendDesc(ctypes.Structure):
                 [("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("q_stride", "o_stride")])
 
 
+class _SelectDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_req", "n_tok", "n_kv_heads", "block_tokens", "table_cols", "n_sel", "n_first",
+                                              "n_last", "max_new")]
+
+
+class _SharedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_groups", "max_prefix")]
+
+
 def _packer(desc):
     """The bytes of a descriptor from its fields' values (a call's host time is 0.4 us less than with a ctypes structure)."""
     f = struct.Struct("@" + "".join({ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_int64: "q"}[t] for _, t in desc._fields_))
@@ -66,6 +76,7 @@ def _packer(desc):
 
 
 _norm_desc, _attend_desc = _packer(_NormDesc), _packer(_AttendDesc)
+_select_desc, _shared_desc = _packer(_SelectDesc), _packer(_SharedDesc)
 
 
 def library_path():
@@ -114,10 +125,16 @@ def _load():
                        ("stq_qk_norm_rope", [NP, P, P, P, P, P, P, P, P, St]),
                        ("stq_kv_store", [KP, P, Z, P, I, P, P, I64, I64, I, St]),
                        ("stq_kv_fetch", [KP, P, Z, P, I, P, P, I, St]),
-                       ("stq_kv_attend", [KP, P, Z, AP, P, P, P, P, P, P, Z, St])):
+                       ("stq_kv_attend", [KP, P, Z, AP, P, P, P, P, P, P, Z, St]),
+                       ("stq_kv_bounds", [KP, P, Z, I, I, P, I, P, P, P, St]),
+                       ("stq_kv_score", [KP, AP, P, P, P, P, P, P, St]),
+                       ("stq_kv_select", [P, P, P, P, P, St]),
+                       ("stq_kv_attend_blocks", [KP, P, Z, AP, I, P, P, P, P, P, P, P, Z, St]),
+                       ("stq_kv_attend_shared", [KP, P, Z, AP, P, P, P, P, P, P, P, P, P, Z, St])):
         getattr(L, name).restype = I
         getattr(L, name).argtypes = args
-    for name, args in (("stq_kv_bytes", [KP]), ("stq_kv_attend_bytes", [KP, AP])):
+    for name, args in (("stq_kv_bytes", [KP]), ("stq_kv_attend_bytes", [KP, AP]), ("stq_kv_bounds_bytes", [KP]),
+                       ("stq_kv_attend_blocks_bytes", [KP, AP, I]), ("stq_kv_attend_shared_bytes", [KP, AP, P])):
         getattr(L, name).restype = Z
         getattr(L, name).argtypes = args
     return L
@@ -411,6 +428,14 @@ def _i32(*sizes):
         raise StqError(-1, "one of the sizes %s does not fit 32 bits" % (sizes,))
 
 
+def _int(x, what):
+    """A size that goes to C as an argument of its own."""
+    try:
+        return operator.index(x)
+    except TypeError:
+        raise StqError(-1, "%s must be a whole number" % what) from None
+
+
 def _call(name, index, stream, *args):
     """One library call on device `index` and its current stream (or the given one)."""
     if stream is None:
@@ -561,3 +586,126 @@ def stq_kv_attend(kv, table, tok_start, lens, q, o, scale, max_new, max_len, win
     desc = _attend_desc(n, tok, heads, ty, cols, max_new, max_len, window, n_sink, scale, qs, os_)
     _call("stq_kv_attend", dev, stream, kv.ref, kv.ptr, kv.bytes, desc, _ptr(table, i, "table", n * cols, dev),
           _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), qp, op, wp, wn)
+
+
+# ----------------------------------------------------------- long contexts
+
+def _table(table, what="table"):
+    if table is None or table.dim() != 2:
+        raise StqError(-1, "%s must be [requests][columns]" % what)
+    return table.shape
+
+
+def _q_and_o(kv, q, o, dev):
+    """(address, stride) of q and of o, rows of q, its heads and element type."""
+    qp, qs = _heads(q, "q", None, None, kv.d, dev)
+    tok, heads, d = q.shape
+    op, os_ = _heads(o, "o", tok, heads, d, dev)
+    ty = _type(q, "q", (STQ_BF16, STQ_FP16))
+    if o.dtype is not q.dtype:
+        raise StqError(-1, "o must have the type of q")
+    return qp, qs, op, os_, tok, heads, ty
+
+
+def _workspace(work, dev):
+    if work is None:
+        return None, 0
+    n = work.numel()
+    return _ptr(work, torch.uint8, "work", n, dev), n
+
+
+def _bounds(bounds, kv, dev):
+    return _ptr(bounds, torch.float8_e5m2, "bounds", kv.desc.n_blocks * kv.n_kv_heads * 2 * kv.d, dev)
+
+
+def stq_kv_bounds_bytes(kv):
+    """Bytes of the bounds of all blocks: those of a float8_e5m2 tensor [n_blocks][n_kv_heads][2][d]."""
+    return _L.stq_kv_bounds_bytes(kv.ref)
+
+
+def stq_kv_bounds(kv, table, tok_start, lens, bounds, max_new, stream=None):
+    """Bounds of the keys of the blocks that hold new tokens.  table int32 [requests][cols];
+    tok_start int32 [requests + 1]; lens int32 [requests]; bounds float8_e5m2
+    [n_blocks][n_kv_heads][2][d], the least values, then the largest."""
+    i, dev = torch.int32, kv.index
+    n, cols = _table(table)
+    _i32(n, cols, max_new)
+    _call("stq_kv_bounds", dev, stream, kv.ref, kv.ptr, kv.bytes, n, _int(max_new, "max_new"), _ptr(table, i, "table", n * cols, dev), cols,
+          _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), _bounds(bounds, kv, dev))
+
+
+def stq_kv_score(kv, bounds, table, tok_start, lens, q, score, scale, max_new, max_len, stream=None):
+    """q [tokens][n_heads][d], bfloat16 or float16; score float32 [tokens][n_kv_heads][cols]: of the blocks
+    that a token sees, the largest logit that its head group's queries can have there."""
+    i, dev = torch.int32, kv.index
+    n, cols = _table(table)
+    qp, qs = _heads(q, "q", None, None, kv.d, dev)
+    tok, heads, _ = q.shape
+    _i32(n, tok, cols, max_new, max_len)
+    desc = _attend_desc(n, tok, heads, _type(q, "q", (STQ_BF16, STQ_FP16)), cols, max_new, max_len, 0, 0, scale, qs, 0)
+    _call("stq_kv_score", dev, stream, kv.ref, desc, _bounds(bounds, kv, dev), _ptr(table, i, "table", n * cols, dev),
+          _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev), qp,
+          _ptr(score, torch.float32, "score", tok * kv.n_kv_heads * cols, dev))
+
+
+def stq_kv_select(score, tok_start, lens, sel, block_tokens, max_new, n_first=1, n_last=1, stream=None):
+    """score float32 [tokens][n_kv_heads][cols]; sel int32 [tokens][n_kv_heads][n_sel]: the columns of the
+    first n_first and the last n_last blocks that the token sees and of the best others, ascending, then -1."""
+    _there(score=score, sel=sel, lens=lens)
+    if score.dim() != 3 or sel.dim() != 3 or sel.shape[:2] != score.shape[:2]:
+        raise StqError(-1, "score must be [tokens][n_kv_heads][cols] and sel [tokens][n_kv_heads][n_sel]")
+    i, dev = torch.int32, score.get_device()
+    tok, heads, cols = score.shape
+    k, n = sel.shape[2], lens.numel()
+    _i32(n, tok, cols, k, block_tokens, max_new, n_first, n_last)
+    desc = _select_desc(n, tok, heads, block_tokens, cols, k, n_first, n_last, max_new)
+    _call("stq_kv_select", dev, stream, desc, _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev),
+          _ptr(score, torch.float32, "score", tok * heads * cols, dev), _ptr(sel, i, "sel", tok * heads * k, dev))
+
+
+def stq_kv_attend_blocks_bytes(kv, n_req, n_tok, n_heads, n_sel, max_new):
+    """Bytes of the workspace that stq_kv_attend_blocks takes for these sizes (0: none)."""
+    _i32(n_req, n_tok, n_heads, n_sel, max_new)
+    return _L.stq_kv_attend_blocks_bytes(kv.ref, _attend_desc(n_req, n_tok, n_heads, STQ_BF16, 1, max_new, 1, 0, 0, 1.0, 0, 0),
+                                         _int(n_sel, "n_sel"))
+
+
+def stq_kv_attend_blocks(kv, table, tok_start, lens, sel, q, o, scale, max_new, work=None, stream=None):
+    """Attention over the blocks of sel int32 [tokens][n_kv_heads][n_sel] alone; the rest as stq_kv_attend."""
+    i, dev = torch.int32, kv.index
+    n, cols = _table(table)
+    qp, qs, op, os_, tok, heads, ty = _q_and_o(kv, q, o, dev)
+    if sel is None or sel.dim() != 3 or sel.shape[0] != tok or sel.shape[1] != kv.n_kv_heads:
+        raise StqError(-1, "sel must be [%s][%s][n_sel]" % (tok, kv.n_kv_heads))
+    k = sel.shape[2]
+    wp, wn = _workspace(work, dev)
+    _i32(n, tok, cols, k, max_new)
+    desc = _attend_desc(n, tok, heads, ty, cols, max_new, 1, 0, 0, scale, qs, os_)
+    _call("stq_kv_attend_blocks", dev, stream, kv.ref, kv.ptr, kv.bytes, desc, k, _ptr(table, i, "table", n * cols, dev),
+          _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev),
+          _ptr(sel, i, "sel", tok * kv.n_kv_heads * k, dev), qp, op, wp, wn)
+
+
+def stq_kv_attend_shared_bytes(kv, n_req, n_tok, n_heads, n_groups, max_new, max_own, max_prefix):
+    """Bytes of the workspace that stq_kv_attend_shared takes for these sizes."""
+    _i32(n_req, n_tok, n_heads, n_groups, max_new, max_own, max_prefix)
+    return _L.stq_kv_attend_shared_bytes(kv.ref, _attend_desc(n_req, n_tok, n_heads, STQ_BF16, 1, max_new, max_own, 0, 0, 1.0, 0, 0),
+                                         _shared_desc(n_groups, max_prefix))
+
+
+def stq_kv_attend_shared(kv, table, tok_start, lens, group_start, prefix, q, o, scale, max_new, max_own, max_prefix,
+                         work, stream=None):
+    """As stq_kv_attend, for requests of which group_start[g] .. group_start[g+1]-1 share their first prefix[g]
+    tokens: group_start int32 [groups + 1], prefix int32 [groups]; max_own, max_prefix: about the longest
+    own part and the longest prefix; work: uint8 tensor of stq_kv_attend_shared_bytes(...) bytes."""
+    _there(prefix=prefix)
+    i, dev = torch.int32, kv.index
+    n, cols = _table(table)
+    qp, qs, op, os_, tok, heads, ty = _q_and_o(kv, q, o, dev)
+    g = prefix.numel()
+    wp, wn = _workspace(work, dev)
+    _i32(n, tok, cols, g, max_new, max_own, max_prefix)
+    desc = _attend_desc(n, tok, heads, ty, cols, max_new, max_own, 0, 0, scale, qs, os_)
+    _call("stq_kv_attend_shared", dev, stream, kv.ref, kv.ptr, kv.bytes, desc, _shared_desc(g, max_prefix),
+          _ptr(table, i, "table", n * cols, dev), _ptr(tok_start, i, "tok_start", n + 1, dev), _ptr(lens, i, "lens", n, dev),
+          _ptr(group_start, i, "group_start", g + 1, dev), _ptr(prefix, i, "prefix", g, dev), qp, op, wp, wn)

@@ -8,7 +8,7 @@ import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = [os.path.join(PKG, "csrc", f) for f in ("stq.hip", "attn.hip", "alloc.cpp")]
+SRC = [os.path.join(PKG, "csrc", f) for f in ("stq.hip", "attn.hip", "attn_long.hip", "alloc.cpp")]
 DEPS = SRC + [os.path.join(PKG, "csrc", f) for f in ("stq_device.h", "attn_device.h")] + [os.path.join(ROOT, "include", "stq.h")]
 LIB = os.path.join(PKG, "libstq.so")
 TENSOR_SRC, TENSOR_LIB = os.path.join(PKG, "csrc", "tensor.cpp"), os.path.join(PKG, "_tensor.so")

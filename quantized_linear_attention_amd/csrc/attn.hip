@@ -399,40 +399,12 @@ __global__ void __launch_bounds__(256) k_kv_fetch(StoreArgs A) {
 
 // ------------------------------------------------------------------ host
 
-// Positions lie in [-2^28, 2^30): a window of 2^30 is no limit, and the kernels'
-// differences of the two stay in 32 bits.
-constexpr int32_t MOST_WINDOW = 1 << 30;
-bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
-  return a && a->n_req >= 0 && a->n_tok >= 0 && a->n_tok <= (1 << 28) && a->n_heads >= 1 && a->n_heads % d->n_kv_heads == 0 &&
-         a->n_heads <= 65536 && (a->type == STQ_BF16 || a->type == STQ_FP16) && a->table_cols >= 1 &&
-         (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
-         a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
-}
-struct Split { int tiles, tile_rows, splits, per, waves; bool staged, once; };
-// Query rows per key/value head up to which each wave unpacks the cache for
-// itself, 32 rows at a time; above, it is staged through LDS for 128 rows (16
-// requests of up to 8,192 tokens, 8 heads, d = 128: 36 rows 41 against 63 us
-// staged, 64 rows 60 against 67, 96 rows 76 against 70, 128 rows 90 against 76;
-// 64 requests of up to 2,048: 64 rows 54 against 62, 96 rows 67 against 63; d = 64,
-// 16 requests: 64 rows 45 against 58, 96 rows 56 against 60, 128 rows 68 against 63).
-constexpr int STAGED_ROWS = 64;
-// A part of a request's work has its own start (three dependent loads) and end
-// (the joins), about 5 us.  Few workgroups are split down to 12 chunks, three a
-// wave, until every CU holds two (1 x 16,000 tokens of 8 heads 13.9 us in parts of
-// 8 chunks, 11.4 of 12, 12.0 of 16; 8 x 2,000 11.0, 9.9, 10.9; 1 x 2,000 8.0,
-// 8.7, 9.8; 8 x 6,000 14.7 at two workgroups a CU, 16.1 at three); many only into parts of 48 chunks and up, which even
-// out ragged lengths, and until every CU has eight of them (64 requests of 2,048
-// to 8,191 tokens, 8 heads: 78 us at four workgroups a CU, 73 to 74 at six to
-// sixteen; 83 whole and 91 in parts of 24 chunks before the loads past the
-// caches; 8 requests of 32,768 to 131,072 tokens: 156 us at four, 153 at six, 146
-// at eight, 150 at ten, 152 at sixteen).
 // A cache larger than the last-level cache is read past the caches at d = 128:
 // nothing of it would be there at the next call (rates at 32 heads over 8: 570
 // MB of pages 78 -> 73 us, 1.1 GB 161 -> 146, three times the rows per head 109
 // -> 106; 139 MB, which the next call finds again, 22.4 -> 23.1; d = 64, whose
 // loads cover half lines, 50 -> 54 and stays as it is).
 constexpr int64_t LAST_CACHE_BYTES = 256 << 20;
-constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
 Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   Split s;
   const int64_t rows = (int64_t)a->max_new * (a->n_heads / d->n_kv_heads);
@@ -444,28 +416,7 @@ Split split_of(const stq_kv_desc* d, const stq_attend_desc* a) {
   if (a->window > 0) seen = seen < (int64_t)a->window + a->n_sink + 64 ? seen : (int64_t)a->window + a->n_sink + 64;
   const int64_t chunks = (seen + 31) / 32;
   s.once = d->d == 128 && (double)chunks * 32 * 17 / 16 * d->d * d->n_kv_heads * a->n_req > (double)LAST_CACHE_BYTES;
-  auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-  int64_t k = 1;
-  if (base > 0) {
-    const int64_t few = least(FEW_GROUPS / base, chunks / FEW_CHUNKS), many = least(MANY_GROUPS / base, chunks / MANY_CHUNKS);
-    k = least(few > many ? few : many, MOST_SPLITS);
-    if (k < 1) k = 1;
-  }
-  // One workgroup a CU or fewer, and requests that would be split in two (in up to
-  // five where the workgroups are half the CUs and more): sixteen waves and no
-  // second launch.  Below that four waves need none either.  Four waves against
-  // sixteen, us on the GPU, 8 heads, d = 128: 1 request of 640 tokens 6.9, 7.7;
-  // 736 7.6, 8.0; 768 8.1, 8.0; 960 8.7, 8.8 (a call 9.9, 8.8); 1,100 9.3, 9.1;
-  // 1,216 8.7, 9.4; 1,500 8.9, 10.6.  32 requests of 736 9.1, 9.7; 768 11.6, 9.8; 2,000
-  // 16.9, 14.1; 16 of 640 7.3, 8.1; 1,100 10.5, 10.1; 1,900 12.7, 12.5; 2,048 12.9,
-  // 13.1.  (d = 64 gains from 640 on: 20 requests of 640 6.3, 6.2, of 2,048 11.9, 10.3.)
-  s.waves = 4;
-  if (s.tile_rows == 16 && base <= CUS && chunks >= 2 * FEW_CHUNKS && chunks < (2 * base >= CUS ? 65 : 3 * FEW_CHUNKS)) {
-    s.waves = 16;
-    k = 1;
-  }
-  s.per = (int)(((chunks + k - 1) / k + 3) & ~3ll);
-  s.splits = (int)((chunks + s.per - 1) / s.per);
+  cut(&s, base, chunks);
   return s;
 }
 

@@ -114,6 +114,21 @@ struct AttnArgs {
   float scale;
 };
 
+// What a call's chunks are: SPAN all that a request's rows see; LIST the blocks
+// that a token's and head's list names (one query token a workgroup); PREFIX the
+// tokens that a group of requests shares, for the rows of all of them; SUFFIX
+// those of a request behind what its group shares.
+enum Mode { SPAN, LIST, PREFIX, SUFFIX };
+
+struct LongArgs : AttnArgs {
+  const int32_t* sel;                    // LIST: [n_tok][hkv][n_sel] block columns
+  int n_sel;
+  const int32_t *group_start, *prefix;   // PREFIX and SUFFIX: [n_groups + 1], [n_groups]
+  int n_groups, pre_splits, pre_per;     // parts of a prefix at most, chunks of one
+  int32_t* shared;                       // [n_req] tokens that the request's group shares
+};
+template <int MODE> using ArgsOf = std::conditional_t<MODE == SPAN, AttnArgs, LongArgs>;
+
 // Chunks of 32 positions that some row of positions [p0, p1] sees: the first
 // n_low chunks (always-visible tokens), then chunks from lo on, `total` in all.
 struct Span { int n_low, lo, total; };
@@ -143,14 +158,98 @@ __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
   return req_of(A, ld_const(A.tok_start + i), ld_const(A.tok_start + i + 1), ld_const(A.len + i));
 }
 
+// The member requests [s, e) of a group and the tokens that they share: whole
+// blocks, and none behind the first new token of any member that has one, so that
+// every row sees all of them.  By all lanes of a wave.
+struct Group { int s, e, len; };
+__device__ __forceinline__ int wave_max_i(int x);
+__device__ __forceinline__ Group group_at(const LongArgs& A, int g) {
+  Group r;
+  r.s = min(max(ld_const(A.group_start + g), 0), A.n_req);
+  r.e = min(max(ld_const(A.group_start + g + 1), r.s), A.n_req);
+  int last = (int)min((int64_t)max(ld_const(A.prefix + g), 0), (int64_t)A.cols * A.T);
+  for (int b = r.s; b < r.e; b += 64) {
+    const int i = min(b + (int)(threadIdx.x & 63), r.e - 1);
+    const int start = A.tok_start[i], end = A.tok_start[i + 1];
+    if (end > start) last = min(last, req_of(A, start, end, A.len[i]).base);
+  }
+  r.len = max(-wave_max_i(-last), 0) & ~(A.T - 1);
+  return r;
+}
+// What request i shares (0 in no group).  The group that holds it is the last
+// one that starts at or before it.
+__device__ __forceinline__ int shared_of(const LongArgs& A, int i) {
+  int g = -1;
+  for (int b = 0; b < A.n_groups; b += 64) {
+    const int x = b + (int)(threadIdx.x & 63);
+    const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(x < A.n_groups && A.group_start[min(x, A.n_groups - 1)] <= i));
+    if (n > 0) g = b + n - 1;
+  }
+  if (g < 0) return 0;
+  const Group r = group_at(A, g);
+  return i < r.e ? r.len : 0;
+}
+// First and last query token's row of a group, in q and o.
+__device__ __forceinline__ void group_tokens(const LongArgs& A, int s, int e, int* first, int* last) {
+  *first = min(max(A.tok_start[s], 0), A.n_tok);
+  *last = min(max(A.tok_start[e], *first), A.n_tok);
+}
+// The x-th tile of rows of all groups that share anything: group and tile of it.
+__device__ __forceinline__ bool group_tile(const LongArgs& A, int rows_of_tile, int x, int* group, int* tile) {
+  const int lane = threadIdx.x & 63;
+  for (int b = 0; b < A.n_groups; b += 64) {
+    const int g = min(b + lane, A.n_groups - 1);
+    const int s = min(max(A.group_start[g], 0), A.n_req), e = min(max(A.group_start[g + 1], s), A.n_req);
+    int first, last;
+    group_tokens(A, s, e, &first, &last);
+    const int mine = b + lane < A.n_groups && A.prefix[g] >= A.T
+                         ? (int)(((int64_t)(last - first) * A.group + rows_of_tile - 1) / rows_of_tile) : 0;
+    int sum = mine;                                      // inclusive
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += y;
+    }
+    const int all = __builtin_amdgcn_readlane(sum, 63);
+    if (x < all) {
+      const int k = __builtin_ctzll(__builtin_amdgcn_ballot_w64(sum > x));
+      *group = b + k;
+      *tile = x - (__builtin_amdgcn_readlane(sum, k) - __builtin_amdgcn_readlane(mine, k));
+      return true;
+    }
+    x -= all;
+  }
+  return false;
+}
+// Entries of a list up to its last one that names a block the token at position
+// p may see.  By all lanes of a wave.
+__device__ __forceinline__ bool listed(const LongArgs& A, int col, int p) { return col >= 0 && col < A.cols && (int64_t)col * A.T <= p; }
+__device__ __forceinline__ int entries_of(const LongArgs& A, const int32_t* list, int p) {
+  int n = 0;
+  for (int b = 0; b < A.n_sel; b += 64) {
+    const int x = b + (int)(threadIdx.x & 63);
+    const uint64_t on = __builtin_amdgcn_ballot_w64(x < A.n_sel && listed(A, list[min(x, A.n_sel - 1)], p));
+    if (on) n = b + 64 - __builtin_clzll(on);
+  }
+  return n;
+}
+
+// Where part sp of a row lies in the workspace: a prefix' parts, then the request's own.
+template <int MODE>
+__device__ __forceinline__ int slot_of(const ArgsOf<MODE>& A, int sp) {
+  if constexpr (MODE == SUFFIX) return A.pre_splits + sp;
+  else return sp;
+}
+
 // Chunks of one part of a request's work: the host's size for a request of the
 // stated longest length, more for a request that is longer than that (a
 // multiple of four: one per wave).  Shorter requests have fewer parts, all of
 // one size.
-__device__ __forceinline__ int split_chunks(const AttnArgs& A, int total) {
-  if (total <= A.per * A.splits) return A.per;
-  return ((total + A.splits - 1) / A.splits + 3) & ~3;
+__device__ __forceinline__ int split_into(int total, int per, int splits) {
+  if (total <= per * splits) return per;
+  return ((total + splits - 1) / splits + 3) & ~3;
 }
+__device__ __forceinline__ int split_chunks(const AttnArgs& A, int total) { return split_into(total, A.per, A.splits); }
 
 __device__ __forceinline__ float max_quads(float x) {   // over the four 16-lane groups
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -459,8 +558,8 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
 // up to 8,192 tokens 24 rows 40 us, 36 rows 41, 64 rows 60 (the bytes take 17 to 20):
 // at 191 registers two workgroups a CU, and each tile of 32 rows reads and
 // unpacks the cache for itself.
-template <int D, int TYPE, int NT, int NWV, bool ONCE>
-__global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(AttnArgs A) {
+template <int D, int TYPE, int NT, int NWV, bool ONCE, int MODE = SPAN>
+__global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(ArgsOf<MODE> A) {
   constexpr int NC = D / 16;
   __shared__ f32x4 so[NWV][NT * NC][64];
   __shared__ f32x2 sml[NWV][NT][16];
@@ -468,21 +567,63 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   // the splits slowest: a short request has none of the last ones, and
   // neighbouring workgroups go to different XCDs
-  const int i = quot(blockIdx.x, A.by_hkv), h = blockIdx.x - i * A.hkv;
-  const int tile = blockIdx.y, sp = blockIdx.z;
-  const Req R = req_args(A, i);
-  const int fresh = min(R.n_new, A.max_new), rows = fresh * A.group, row0 = tile * 16 * NT;
+  int i = quot(blockIdx.x, A.by_hkv), tile = blockIdx.y;
+  const int h = blockIdx.x - i * A.hkv, sp = blockIdx.z;
+  Req R;
+  if constexpr (MODE == PREFIX) {
+    int g;
+    if (!group_tile(A, 16 * NT, i, &g, &tile)) return;
+    const Group r = group_at(A, g);
+    int last;
+    group_tokens(A, r.s, r.e, &R.first, &last);
+    R.n_new = last - R.first;
+    R.base = r.len;                                      // (no row lies before what is shared)
+    i = r.s;                                             // by the table of the first
+  } else if constexpr (MODE == LIST) {
+    const int x = i;
+    i = quot(x, A.by_max_new);
+    const int j = x - i * A.max_new;
+    R = req_args(A, i);
+    if (j >= R.n_new) return;
+    R.first += j;
+    R.base += j;
+    R.n_new = 1;
+  } else {
+    R = req_args(A, i);
+  }
+  const int fresh = MODE == PREFIX ? R.n_new : min(R.n_new, A.max_new), rows = fresh * A.group, row0 = tile * 16 * NT;
   if (row0 >= rows) return;
   int p0 = R.base, p1 = R.base + fresh - 1;             // positions of the tile's first and last row
-  if (A.tiles > 1) {
-    p0 = R.base + quot(row0, A.by_group);
-    p1 = R.base + quot(min(row0 + 16 * NT, rows) - 1, A.by_group);
+  if (MODE == SPAN || MODE == SUFFIX)
+    if (A.tiles > 1) {
+      p0 = R.base + quot(row0, A.by_group);
+      p1 = R.base + quot(min(row0 + 16 * NT, rows) - 1, A.by_group);
+    }
+  Span sn = {0, 0, 0};
+  int per = A.per;
+  const int32_t* list = nullptr;
+  if constexpr (MODE == SPAN) {
+    sn = span_of(p0, p1, A.window, A.sink);
+    per = split_chunks(A, sn.total);
+  } else if constexpr (MODE == LIST) {
+    list = A.sel + ((int64_t)R.first * A.hkv + h) * A.n_sel;
+    sn.total = entries_of(A, list, p0) * (A.T >> 5);
+    per = split_chunks(A, sn.total);
+  } else if constexpr (MODE == PREFIX) {
+    sn.total = R.base >> 5;
+    per = split_into(sn.total, A.pre_per, A.pre_splits);
+  } else {
+    const int shared = shared_of(A, i);
+    if (h == 0 && tile == 0 && sp == 0 && threadIdx.x == 0) A.shared[i] = shared;
+    sn.lo = shared >> 5;
+    sn.total = max((p1 >> 5) + 1 - sn.lo, 0);
+    per = split_chunks(A, sn.total);
   }
-  const Span sn = span_of(p0, p1, A.window, A.sink);
-  const int per = split_chunks(A, sn.total);
+  const int window = MODE == SPAN ? A.window : 0, sink = MODE == SPAN ? A.sink : 0;
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
-  if (c0 >= c1 && sp > 0) return;
-  const bool whole = sn.total <= per;                   // one part: its result is the output's
+  if (c0 >= c1 && (sp > 0 || MODE == PREFIX)) return;
+  // one part: its result is the output's
+  const bool whole = MODE != PREFIX && sn.total <= per && (MODE != SUFFIX || sn.lo == 0);
 
   const int32_t* tab = A.table + (int64_t)i * A.cols;
   const int blk_shift = 31 - __builtin_clz(A.T) - 5;    // chunks of a block, as a power of two
@@ -492,20 +633,34 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
   Chunk<D> C;
   const Places<D> W(A.T);
   const uint32_t block_bytes = (uint32_t)A.T * D / 16 * 17;
-  int k = c0 + wave, ahead = 0, entry = 0;
-  struct Next { const uint8_t* base; uint32_t off; bool dead; };
+  int k = c0 + wave, ahead = 0, entry = 0, first_of = 0;
+  struct Next { const uint8_t* base; uint32_t off; bool dead; int t; };
   // Where chunk kf lies.  Past the end the last chunk once more: the loads are
   // always made (from the cache then); with a branch around them the compiler has to
   // wait for all of them at the first use of any.
   auto locate = [&](int kf) {
     if ((ahead & 63) == 0) {
-      entry = tab[chunk_at(min(kf + NWV * lane, c1 - 1)) >> blk_shift];
+      if constexpr (MODE == LIST) {
+        const int kk = min(kf + NWV * lane, c1 - 1), col = list[kk >> blk_shift];
+        const bool on = listed(A, col, p0);
+        entry = tab[on ? col : 0];
+        if (!on) entry = -1;
+        first_of = (on ? col * A.T : 0) + 32 * (kk & ((1 << blk_shift) - 1));
+        asm volatile("" : "+v"(first_of));
+      } else {
+        entry = tab[chunk_at(min(kf + NWV * lane, c1 - 1)) >> blk_shift];
+      }
       asm volatile("" : "+v"(entry));     // (waited for here, not behind the branch, where it would hold up every step)
     }
     Next x;
     const int blk = __builtin_amdgcn_readlane(entry, ahead & 63);
     x.dead = (uint32_t)blk >= (uint32_t)A.n_blocks;    // no block: no visible token (block 0 is read in its place)
-    x.off = (chunk_at(min(kf, c1 - 1)) * 32) & (A.T - 1);
+    if constexpr (MODE == LIST) {
+      x.t = __builtin_amdgcn_readlane(first_of, ahead & 63);
+      x.off = x.t & (A.T - 1);
+    } else {
+      x.off = (chunk_at(min(kf, c1 - 1)) * 32) & (A.T - 1);
+    }
     x.base = A.cache + ((uint64_t)(uint32_t)(x.dead ? 0 : blk) * A.hkv + h) * block_bytes;
     ahead++;
     return x;
@@ -552,8 +707,8 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
   // the SIMD cover what that does not (a second set takes the registers of one or
   // two waves: 147 -> 162 us and 73 -> 77 for the long and the ragged batch).
   while (k < c1) {
-    const int ch = chunk_at(k), t0 = ch * 32, t1 = t0 + 31;
-    const bool dead = at.dead, full = !dead && t1 <= p0 && (A.window == 0 || t0 > p1 - A.window || t1 < A.sink);
+    const int t0 = MODE == LIST ? at.t : chunk_at(k) * 32, t1 = t0 + 31;
+    const bool dead = at.dead, full = !dead && (MODE == PREFIX || t1 <= p0) && (window == 0 || t0 > p1 - window || t1 < sink);
     k += NWV;
     f32x4 s[NT][2];
     key_products<D, NT>(C, q, s);
@@ -563,11 +718,11 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
       if (!full) {
-        const int low = A.window == 0 ? -1 : pos[nt] - A.window, last = dead ? -1 : pos[nt];
+        const int low = window == 0 ? -1 : pos[nt] - window, last = dead ? -1 : pos[nt];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           const int t = t0 + token_of<D>(G, e);
-          const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < A.sink));
+          const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < sink));
           s[nt][e >> 2][e & 3] = see ? s[nt][e >> 2][e & 3] : NEG_INF;
         }
       }
@@ -656,8 +811,10 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Att
         else out[NC * i4] = (uint16_t)pack2<TYPE>(x[0][i4] * inv, 0.0f);
       }
     } else {
-      const int64_t row = (int64_t)sp * A.n_tok * A.hq + grow[nt];
-      if (G == 0 && wave == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){M * cf[nt], L};
+      const int64_t row = (int64_t)slot_of<MODE>(A, sp) * A.n_tok * A.hq + grow[nt];
+      // (parts of a shared prefix may come from k_attend_tiles, whose sums count from the reference's lift)
+      const float at_m = MODE == SPAN ? M * cf[nt] : M == NEG_INF ? NEG_INF : __builtin_fmaf(M, cf[nt], -LIFT);
+      if (G == 0 && wave == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){at_m, L};
       float* out = A.po + row * D + ch0;
 #pragma unroll
       for (int i4 = 0; i4 < 4; i4++) {
@@ -755,8 +912,8 @@ __device__ __forceinline__ bool tile_of(const AttnArgs& A, int rows_of_tile, int
 }
 
 constexpr int TILE_WAVES = 4;
-template <int D, int TYPE>
-__global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A) {
+template <int D, int TYPE, int MODE = SPAN>
+__global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE> A) {
   constexpr int ROWS = 32 * TILE_WAVES;
   constexpr int KSTEP = D / 16, NC = D / 32;
   __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][64 * D * 2], lds_v[2][64 * D * 2];
@@ -766,18 +923,47 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
   // multiple of 8
   int b = blockIdx.x;
   const int h = b % A.hkv; b /= A.hkv;
-  const int sp = b % A.splits;
+  int most = A.splits;
+  if constexpr (MODE == PREFIX) most = A.pre_splits;
+  const int sp = b % most;
   int i, row0;
-  if (!tile_of(A, ROWS, b / A.splits, &i, &row0)) return;
-  const Req R = req_args(A, i);
-  const int rows = min(R.n_new, A.max_new) * A.group;
+  Req R;
+  if constexpr (MODE == PREFIX) {
+    int g;
+    if (!group_tile(A, ROWS, b / most, &g, &row0)) return;
+    row0 *= ROWS;
+    const Group r = group_at(A, g);
+    int last;
+    group_tokens(A, r.s, r.e, &R.first, &last);
+    R.n_new = last - R.first;
+    R.base = r.len;                                      // (no row lies before what is shared)
+    i = r.s;                                             // by the table of the first
+  } else {
+    if (!tile_of(A, ROWS, b / A.splits, &i, &row0)) return;
+    R = req_args(A, i);
+  }
+  const int rows = (MODE == PREFIX ? R.n_new : min(R.n_new, A.max_new)) * A.group;
   if (row0 < 0 || row0 >= rows) return;
   const int p0 = R.base + row0 / A.group, p1 = R.base + (min(row0 + ROWS, rows) - 1) / A.group;
-  const Span sn = span_of(p0, p1, A.window, A.sink);
-  const int per = split_chunks(A, sn.total);
+  Span sn = {0, 0, 0};
+  int per;
+  if constexpr (MODE == SPAN) {
+    sn = span_of(p0, p1, A.window, A.sink);
+    per = split_chunks(A, sn.total);
+  } else if constexpr (MODE == PREFIX) {
+    sn.total = R.base >> 5;
+    per = split_into(sn.total, A.pre_per, A.pre_splits);
+  } else {
+    const int shared = shared_of(A, i);
+    if (h == 0 && row0 == 0 && sp == 0 && tid == 0) A.shared[i] = shared;
+    sn.lo = shared >> 5;
+    sn.total = max((p1 >> 5) + 1 - sn.lo, 0);
+    per = split_chunks(A, sn.total);
+  }
+  const int window = MODE == SPAN ? A.window : 0, sink = MODE == SPAN ? A.sink : 0;
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
-  if (c0 >= c1 && sp > 0) return;
-  const int parts = (sn.total + per - 1) / per;
+  if (c0 >= c1 && (sp > 0 || MODE == PREFIX)) return;
+  const int parts = MODE == PREFIX || (MODE == SUFFIX && sn.lo > 0) ? 2 : (sn.total + per - 1) / per;
 
   // the wave's rows
   const bool on = row0 + 32 * wave + n < rows;         // rows past the last compute the last one again and are not written
@@ -905,17 +1091,17 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
   // other, so the compiler interleaves them).
   auto work = [&](const Tile& x, f32x16* s, f32x16* sn, const uint8_t* next_k, const uint8_t* v, auto&& move_on) {
     const int ta = chunk_at(x.k) * 32, tb = chunk_at(min(x.k + 1, c1 - 1)) * 32;
-    const bool in_a = A.window == 0 || ta > pw1 - A.window || ta + 31 < A.sink;
-    const bool in_b = A.window == 0 || tb > pw1 - A.window || tb + 31 < A.sink;
-    if (x.gone || tb + 31 > pw0 || !in_a || !in_b) {
+    const bool in_a = window == 0 || ta > pw1 - window || ta + 31 < sink;
+    const bool in_b = window == 0 || tb > pw1 - window || tb + 31 < sink;
+    if (x.gone || (MODE != PREFIX && tb + 31 > pw0) || !in_a || !in_b) {
 #pragma unroll
       for (int u = 0; u < 2; u++) {
-        const int t0 = (u ? tb : ta) + 4 * G, low = A.window == 0 ? -1 : pos - A.window;
+        const int t0 = (u ? tb : ta) + 4 * G, low = window == 0 ? -1 : pos - window;
         const int last = x.gone & (1 << u) ? -1 : pos;
 #pragma unroll
         for (int e = 0; e < 16; e++) {
           const int t = t0 + 8 * (e >> 2) + (e & 3);
-          const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < A.sink));
+          const int see = (int)(t <= last) & ((int)(t > low) | (int)(t < sink));
           s[u][e] = see ? s[u][e] : NEG_INF;
         }
       }
@@ -1018,7 +1204,7 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
         *(u32x2*)(out + 32 * c + 8 * a) = (u32x2){pack2<TYPE>(o[c][4 * a] * inv, o[c][4 * a + 1] * inv),
                                                   pack2<TYPE>(o[c][4 * a + 2] * inv, o[c][4 * a + 3] * inv)};
   } else {
-    const int64_t row = (int64_t)sp * A.n_tok * A.hq + (int64_t)(R.first + j) * A.hq + h * A.group + g;
+    const int64_t row = (int64_t)slot_of<MODE>(A, sp) * A.n_tok * A.hq + (int64_t)(R.first + j) * A.hq + h * A.group + g;
     if (G == 0) {
       A.pml[2 * row] = ref.m == NEG_INF ? NEG_INF : ref.mc;
       A.pml[2 * row + 1] = L;
@@ -1034,8 +1220,8 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(AttnArgs A)
 
 // Join the splits of one row: one wave per row, its channels over the lanes,
 // the splits in order.
-template <int D, int TYPE>
-__global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_shift) {
+template <int D, int TYPE, int MODE = SPAN>
+__global__ void __launch_bounds__(256) k_attend_join(ArgsOf<MODE> A, int tile_shift) {
   const int lane = threadIdx.x & 63;
   const int hd = __builtin_amdgcn_readfirstlane((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
   if (hd >= A.hq) return;
@@ -1044,20 +1230,35 @@ __global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_shift)
   const int fresh = min(R.n_new, A.max_new), rows = fresh * A.group;
   if (j >= fresh) return;
   int p0 = R.base, p1 = R.base + fresh - 1;             // as the tile's workgroups had them
-  if (A.tiles > 1) {
+  if (MODE != LIST && A.tiles > 1) {
     const int row0 = ((j * A.group + hd - quot(hd, A.by_group) * A.group) >> tile_shift) << tile_shift;
     p0 = R.base + quot(row0, A.by_group);
     p1 = R.base + quot(min(row0 + (1 << tile_shift), rows) - 1, A.by_group);
   }
-  const Span sn = span_of(p0, p1, A.window, A.sink);
+  Span sn = {0, 0, 0};
+  if constexpr (MODE == SPAN) {
+    sn = span_of(p0, p1, A.window, A.sink);
+  } else if constexpr (MODE == LIST) {
+    sn.total = entries_of(A, A.sel + ((int64_t)(R.first + j) * A.hkv + quot(hd, A.by_group)) * A.n_sel, R.base + j) * (A.T >> 5);
+  } else {
+    sn.lo = ld_const(A.shared + i) >> 5;
+    sn.total = max((p1 >> 5) + 1 - sn.lo, 0);
+  }
   const int per = split_chunks(A, sn.total);
-  if (sn.total <= per) return;                              // written by its only part
-  const int parts = per == A.per ? quot(sn.total + per - 1, A.by_per) : (sn.total + per - 1) / per;
+  if (sn.total <= per && (MODE != SUFFIX || sn.lo == 0)) return;   // written by its only part
+  int parts = per == A.per ? quot(sn.total + per - 1, A.by_per) : (sn.total + per - 1) / per, shared_parts = 0, gap = 0;
+  if constexpr (MODE == SUFFIX) {
+    const int pre = split_into(sn.lo, A.pre_per, A.pre_splits);
+    shared_parts = (sn.lo + pre - 1) / pre;
+    parts += shared_parts;
+    gap = A.pre_splits - shared_parts;
+  }
+  auto at = [&](int s) { return MODE == SUFFIX && s >= shared_parts ? s + gap : s; };
   const int64_t stride = (int64_t)A.n_tok * A.hq, row = (int64_t)(R.first + j) * A.hq + hd;
   // statistics: part s on lane s (and s + 64)
   const f32x2 none = {NEG_INF, 0.0f};
   const f32x2* ml = (const f32x2*)A.pml + row;
-  const f32x2 m0 = lane < parts ? ml[lane * stride] : none, m1 = lane + 64 < parts ? ml[(lane + 64) * stride] : none;
+  const f32x2 m0 = lane < parts ? ml[at(lane) * stride] : none, m1 = lane + 64 < parts ? ml[at(lane + 64) * stride] : none;
   // N parts from s on are under way at a time (the last one again where there
   // are fewer, not added): the first eight along with the statistics
   const float* po = A.po + row * D + lane * (D / 64);
@@ -1067,7 +1268,7 @@ __global__ void __launch_bounds__(256) k_attend_join(AttnArgs A, int tile_shift)
 #pragma unroll
     for (int e = 0; e < N; e++)
 #pragma unroll
-      for (int u = 0; u < D / 64; u++) y[e][u] = po[min(s + e, parts - 1) * stride * D + u];
+      for (int u = 0; u < D / 64; u++) y[e][u] = po[at(min(s + e, parts - 1)) * stride * D + u];
   };
   ask(std::integral_constant<int, FIRST>(), 0);
   float M = wave_max(__builtin_fmaxf(m0[0], m1[0]));
@@ -1134,5 +1335,59 @@ bool meet(const Rows& a, const Rows& b, int64_t n) {
 }
 bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.step == b.step && a.bytes == b.bytes; }
 stq_status launched() { return hipGetLastError() == hipSuccess ? STQ_OK : STQ_ERR_HIP; }
+
+// Positions lie in [-2^28, 2^30): a window of 2^30 is no limit, and the kernels'
+// differences of the two stay in 32 bits.
+constexpr int32_t MOST_WINDOW = 1 << 30;
+bool attend_ok(const stq_kv_desc* d, const stq_attend_desc* a) {
+  return a && a->n_req >= 0 && a->n_tok >= 0 && a->n_tok <= (1 << 28) && a->n_heads >= 1 && a->n_heads % d->n_kv_heads == 0 &&
+         a->n_heads <= 65536 && (a->type == STQ_BF16 || a->type == STQ_FP16) && a->table_cols >= 1 &&
+         (int64_t)a->table_cols * d->block_tokens <= (1ll << 30) && a->max_new >= 1 && a->max_len >= 1 &&
+         a->window >= 0 && a->n_sink >= 0 && isfinite(a->scale);
+}
+struct Split { int tiles, tile_rows, splits, per, waves; bool staged, once; };
+// Query rows per key/value head up to which each wave unpacks the cache for
+// itself, 32 rows at a time; above, it is staged through LDS for 128 rows (16
+// requests of up to 8,192 tokens, 8 heads, d = 128: 36 rows 41 against 63 us
+// staged, 64 rows 60 against 67, 96 rows 76 against 70, 128 rows 90 against 76;
+// 64 requests of up to 2,048: 64 rows 54 against 62, 96 rows 67 against 63; d = 64,
+// 16 requests: 64 rows 45 against 58, 96 rows 56 against 60, 128 rows 68 against 63).
+constexpr int STAGED_ROWS = 64;
+// A part of a request's work has its own start (three dependent loads) and end
+// (the joins), about 5 us.  Few workgroups are split down to 12 chunks, three a
+// wave, until every CU holds two (1 x 16,000 tokens of 8 heads 13.9 us in parts of
+// 8 chunks, 11.4 of 12, 12.0 of 16; 8 x 2,000 11.0, 9.9, 10.9; 1 x 2,000 8.0,
+// 8.7, 9.8; 8 x 6,000 14.7 at two workgroups a CU, 16.1 at three); many only into parts of 48 chunks and up, which even
+// out ragged lengths, and until every CU has eight of them (64 requests of 2,048
+// to 8,191 tokens, 8 heads: 78 us at four workgroups a CU, 73 to 74 at six to
+// sixteen; 83 whole and 91 in parts of 24 chunks before the loads past the
+// caches; 8 requests of 32,768 to 131,072 tokens: 156 us at four, 153 at six, 146
+// at eight, 150 at ten, 152 at sixteen).
+constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
+void cut(Split* x, int64_t base, int64_t chunks) {
+  Split& s = *x;
+  auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  int64_t k = 1;
+  if (base > 0) {
+    const int64_t few = least(FEW_GROUPS / base, chunks / FEW_CHUNKS), many = least(MANY_GROUPS / base, chunks / MANY_CHUNKS);
+    k = least(few > many ? few : many, MOST_SPLITS);
+    if (k < 1) k = 1;
+  }
+  // One workgroup a CU or fewer, and requests that would be split in two (in up to
+  // five where the workgroups are half the CUs and more): sixteen waves and no
+  // second launch.  Below that four waves need none either.  Four waves against
+  // sixteen, us on the GPU, 8 heads, d = 128: 1 request of 640 tokens 6.9, 7.7;
+  // 736 7.6, 8.0; 768 8.1, 8.0; 960 8.7, 8.8 (a call 9.9, 8.8); 1,100 9.3, 9.1;
+  // 1,216 8.7, 9.4; 1,500 8.9, 10.6.  32 requests of 736 9.1, 9.7; 768 11.6, 9.8; 2,000
+  // 16.9, 14.1; 16 of 640 7.3, 8.1; 1,100 10.5, 10.1; 1,900 12.7, 12.5; 2,048 12.9,
+  // 13.1.  (d = 64 gains from 640 on: 20 requests of 640 6.3, 6.2, of 2,048 11.9, 10.3.)
+  s.waves = 4;
+  if (s.tile_rows == 16 && base <= CUS && chunks >= 2 * FEW_CHUNKS && chunks < (2 * base >= CUS ? 65 : 3 * FEW_CHUNKS)) {
+    s.waves = 16;
+    k = 1;
+  }
+  s.per = (int)(((chunks + k - 1) / k + 3) & ~3ll);
+  s.splits = (int)((chunks + s.per - 1) / s.per);
+}
 
 }  // namespace

@@ -1,0 +1,699 @@
+// attn_long.hip — gfx950 kernels and C ABI of the softmax layers' operators for
+// long contexts (contract: include/stq.h, "LONG CONTEXTS"): bounds of a block's
+// keys, scores of the blocks for a query, their selection, attention over the
+// selected blocks, and attention of requests that share a prefix.
+#include "attn_device.h"
+
+namespace {
+
+// ------------------------------------------------------- bounds of keys
+//
+// Per channel the least and the largest of a block's keys, as the upper byte
+// of binary16 (E5M2), rounded outward: cached keys are exact in binary16 and
+// have two significant bits of E5M2's three, so a bound is the key itself from
+// 2^-14 on.  A block with a poisoned key gets NaN.
+//
+// One wave takes one (block, head).  A lane reads the 16 bytes of one token's
+// 32 channels of a scale; tokens of a pass lie on lane bits 0, 1, 4, 5 (and 3
+// at d = 64), channel groups on bit 2 (and 3), so that the joins over tokens
+// are register swaps (permlane32 and 16, each halving what a lane holds) and
+// DPP steps.  Lanes past the last token read the last one again.
+struct BoundsArgs {
+  const uint8_t* cache;
+  const int32_t *table, *tok_start, *len;
+  uint8_t* bounds;
+  int n_req, hkv, T, n_blocks, cols, max_new, span;
+  Div by_span;
+};
+
+__device__ __forceinline__ f16x2 min2(f16x2 a, f16x2 b) { return __builtin_elementwise_min(a, b); }
+__device__ __forceinline__ f16x2 max2(f16x2 a, f16x2 b) { return __builtin_elementwise_max(a, b); }
+template <bool MAX>
+__device__ __forceinline__ f16x2 best2(f16x2 a, f16x2 b) {
+  if constexpr (MAX) return max2(a, b);
+  else return min2(a, b);
+}
+// N pairs of every lane -> N / 2: the two halves of the wave (rows of 16 lanes)
+// join theirs, the lower lanes keep the first half of the pairs, the upper the second
+template <bool MAX, int N>
+__device__ __forceinline__ void halve32(f16x2* x) {
+#pragma unroll
+  for (int i = 0; i < N / 2; i++) {
+    auto r = __builtin_amdgcn_permlane32_swap(h2_bits(x[i]), h2_bits(x[i + N / 2]), false, false);
+    x[i] = best2<MAX>(as_h2(r[0]), as_h2(r[1]));
+  }
+}
+template <bool MAX, int N>
+__device__ __forceinline__ void halve16(f16x2* x) {
+#pragma unroll
+  for (int i = 0; i < N / 2; i++) {
+    auto r = __builtin_amdgcn_permlane16_swap(h2_bits(x[i]), h2_bits(x[i + N / 2]), false, false);
+    x[i] = best2<MAX>(as_h2(r[0]), as_h2(r[1]));
+  }
+}
+template <bool MAX, int CTRL>
+__device__ __forceinline__ f16x2 join2(f16x2 x) {
+  return best2<MAX>(x, as_h2((uint32_t)dppi<CTRL>((int)h2_bits(x))));
+}
+// the upper bytes of four pairs' eight numbers, moved outward where the lower byte has bits
+template <bool UP>
+__device__ __forceinline__ u32x2 outward(const f16x2* x) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint32_t u = (h2_bits(x[i >> 1]) >> (16 * (i & 1))) & 0xFFFFu;
+    b[i] = ((u < 0x8000u) == UP ? u + 0xFFu : u) >> 8;
+  }
+  return (u32x2){b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24};
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_bounds(BoundsArgs A) {
+  constexpr int PASS = D == 128 ? 16 : 32;             // tokens of one load of the wave
+  const int lane = threadIdx.x & 63;
+  const int h = __builtin_amdgcn_readfirstlane((int)(blockIdx.y * 4 + (threadIdx.x >> 6)));
+  if (h >= A.hkv) return;
+  const int i = quot(blockIdx.x, A.by_span), c = blockIdx.x - i * A.span;
+  const int T = A.T, shift = 31 - __builtin_clz(T);
+  const int start = ld_const(A.tok_start + i), fresh = max(ld_const(A.tok_start + i + 1) - start, 0);
+  const int len = (int)min((int64_t)max(ld_const(A.len + i), 0), (int64_t)A.cols << shift);
+  const int64_t base = (int64_t)len - fresh, end = min(base + min(fresh, A.max_new), (int64_t)len);
+  const int64_t col = (max(base, (int64_t)0) >> shift) + c;
+  if (fresh == 0 || end <= 0 || col << shift >= end) return;
+  const int blk = ld_const(A.table + (int64_t)i * A.cols + col);
+  if ((uint32_t)blk >= (uint32_t)A.n_blocks) return;
+  const int last = (int)min((int64_t)T, len - (col << shift)) - 1;
+  const uint64_t unit = (uint64_t)(uint32_t)blk * A.hkv + h;
+  const uint8_t* page = A.cache + unit * ((uint64_t)T * D / 16 * 17);
+  const int cg = (lane >> 2) & (D / 32 - 1);
+  const int tok = (lane & 3) | (D == 128 ? (lane >> 4) << 2 : (lane >> 3) << 2);
+  f16x2 lo[16], hi[16];
+  uint32_t worst = 0;
+  auto pass = [&](int t, bool first) {
+    t = min(t + tok, last);
+    const u32x4 w = *(const u32x4*)(page + t * (D / 2) + 16 * cg);
+    const uint32_t sb = page[T * D + cg * T + t];
+    worst = max(worst, sb);
+    const float sc = bits_f(sb << 23);
+#pragma unroll
+    for (int x = 0; x < 4; x++) {
+      const uint32_t p[4] = {cvt2<0>(w[x], sc), cvt2<1>(w[x], sc), cvt2<2>(w[x], sc), cvt2<3>(w[x], sc)};
+#pragma unroll
+      for (int y = 0; y < 4; y++) {
+        const f16x2 v = as_h2(p[y]);
+        lo[4 * x + y] = first ? v : min2(lo[4 * x + y], v);
+        hi[4 * x + y] = first ? v : max2(hi[4 * x + y], v);
+      }
+    }
+  };
+  pass(0, true);
+  for (int t = PASS; t <= last; t += PASS) pass(t, false);
+  halve32<false, 16>(lo);
+  halve32<true, 16>(hi);
+  halve16<false, 8>(lo);
+  halve16<true, 8>(hi);
+#pragma unroll
+  for (int x = 0; x < 4; x++) {
+    lo[x] = join2<false, 0x4E>(join2<false, 0xB1>(lo[x]));
+    hi[x] = join2<true, 0x4E>(join2<true, 0xB1>(hi[x]));
+    if (D == 64) {
+      lo[x] = join2<false, 0x128>(lo[x]);
+      hi[x] = join2<true, 0x128>(hi[x]);
+    }
+  }
+  const bool poison = __builtin_amdgcn_ballot_w64(worst == 255) != 0;
+  // channels 32 cg + 16 (lane bit 5) + 8 (bit 4) .. + 7: the lower bounds by the first lane of four, the upper by the second
+  if ((lane & 3) > 1 || (D == 64 && (lane & 8))) return;
+  const u32x2 b = lane & 1 ? outward<true>(hi) : outward<false>(lo);
+  const u32x2 nan = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  *(u32x2*)(A.bounds + unit * (2 * D) + (lane & 1) * D + 32 * cg + 16 * (lane >> 5) + 8 * ((lane >> 4) & 1)) = poison ? nan : b;
+}
+
+// ------------------------------------------------------ scores of blocks
+//
+// max over a head group's queries x = scale * q of sum_c max(x_c lo_c, x_c hi_c)
+// = x+ . hi + x- . lo: a matrix product over 2 d terms, the bounds (as binary16:
+// a byte shifted up) against the queries' positive and negative parts.  Rows of a
+// tile: 16 blocks; columns: the heads of a token side by side, the last one
+// repeated up to a power of two (a maximum does not mind), so that the group's
+// maximum is DPP steps.  Products are exact in binary32; queries are scaled by
+// a power of two per row as in the attention.
+struct ScoreArgs : AttnArgs {
+  const uint8_t* bounds;
+  float* score;
+  int rows_shift, tile_run;      // log2 of a token's columns; tiles of 16 blocks that a wave takes in turn
+};
+
+__device__ __forceinline__ uint32_t up2(uint32_t w, uint32_t sel) { return __builtin_amdgcn_perm(0u, w, sel); }
+// 16 bytes as two operands of eight binary16 numbers
+__device__ __forceinline__ void widen(u32x4 w, f16x8* f) {
+#pragma unroll
+  for (int y = 0; y < 2; y++)
+    f[y] = frag(up2(w[2 * y], 0x010C000Cu), up2(w[2 * y], 0x030C020Cu), up2(w[2 * y + 1], 0x010C000Cu), up2(w[2 * y + 1], 0x030C020Cu));
+}
+
+template <int D, int TYPE, int NT>
+__global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
+  constexpr int LD = D / 64;                           // 16-byte loads of one bound
+  const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int i = quot(blockIdx.x, A.by_hkv), h = blockIdx.x - i * A.hkv;
+  const Req R = req_args(A, i);
+  const int fresh = min(R.n_new, A.max_new), rs = A.rows_shift, TOK = 16 >> rs, tok0 = blockIdx.y * NT * TOK;
+  if (tok0 >= fresh) return;
+  const int shift = 31 - __builtin_clz(A.T);
+  const int p1 = R.base + min(tok0 + NT * TOK, fresh) - 1;
+  if (p1 < 0) return;
+  const int total = min((p1 >> shift) + 1, A.cols);     // blocks that the last of these tokens sees
+  const int32_t* tab = A.table + (int64_t)i * A.cols;
+  const int run = 16 * A.tile_run, step = gridDim.z * 4 * run;
+  for (int hc = 0; hc < A.group; hc += 16) {            // sixteen heads of the group at a time
+    bool ready = false;
+    f16x8 qp[NT][D / 32], qn[NT][D / 32];
+    float mul[NT];
+    int ex[NT], top[NT];                               // the token's last block (-1: not this lane's to write)
+    int64_t to[NT];
+    for (int b1 = (blockIdx.z * 4 + wave) * run; b1 < total; b1 += step) {
+      const int b2 = min(b1 + run, total);
+      u32x4 w[2 * LD];
+      bool dead;
+      auto load = [&](int b) {
+        const int blk = tab[min(b + n, b2 - 1)];
+        dead = (uint32_t)blk >= (uint32_t)A.n_blocks;
+        const uint8_t* p = A.bounds + ((uint64_t)(uint32_t)(dead ? 0 : blk) * A.hkv + h) * (2 * D) + 16 * G;
+#pragma unroll
+        for (int x = 0; x < 2 * LD; x++) w[x] = *(const u32x4*)(p + 64 * x);
+      };
+      load(b1);
+      if (!ready) {
+        ready = true;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          const int j = tok0 + nt * TOK + (n >> rs), jj = min(j, fresh - 1);
+          const int g = min(hc + (n & ((1 << rs) - 1)), A.group - 1);
+          const int64_t at = (int64_t)(R.first + jj) * A.qs + (int64_t)(h * A.group + g) * D + 16 * G;
+          float x[D / 4];
+#pragma unroll
+          for (int y = 0; y < LD; y++) {
+            load8<TYPE>(A.q, at + 64 * y, x + 16 * y);
+            load8<TYPE>(A.q, at + 64 * y + 8, x + 16 * y + 8);
+          }
+          float m = 0.0f;
+#pragma unroll
+          for (int u = 0; u < D / 4; u++) m = __builtin_fmaxf(m, __builtin_fabsf(x[u]));
+          const int e = q_shift(max_quads(m));
+          const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+          for (int u = 0; u < D / 4; u++) {
+            const f16 v = (f16)(sign * __builtin_ldexpf(x[u], e));
+            qp[nt][u >> 3][u & 7] = v > (f16)0 || v != v ? v : (f16)0;
+            qn[nt][u >> 3][u & 7] = v < (f16)0 || v != v ? v : (f16)0;
+          }
+          mul[nt] = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(A.scale));
+          ex[nt] = __builtin_amdgcn_frexp_expf(A.scale) - e;
+          const int p = R.base + jj;
+          top[nt] = j < fresh && (n & ((1 << rs) - 1)) == 0 ? min(p >> shift, A.cols - 1) : -1;
+          to[nt] = ((int64_t)(R.first + jj) * A.hkv + h) * A.cols;
+        }
+      }
+      for (int b = b1; b < b2; b += 16) {
+        f32x4 s[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) s[nt] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int x = 0; x < 2 * LD; x++) {
+          f16x8 f[2];
+          widen(w[x], f);
+#pragma unroll
+          for (int y = 0; y < 2; y++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+              s[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[y], x < LD ? qn[nt][2 * x + y] : qp[nt][2 * (x - LD) + y], s[nt], 0, 0, 0);
+        }
+        const uint32_t gone = (uint32_t)__builtin_amdgcn_ballot_w64(dead) & 0xFFFFu;
+        if (b + 16 < b2) load(b + 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          f32x4 v;
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            float y = __builtin_ldexpf(s[nt][u] * mul[nt], ex[nt]);
+            if (rs > 0) y = __builtin_fmaxf(y, dpp<0xB1>(y));
+            if (rs > 1) y = __builtin_fmaxf(y, dpp<0x4E>(y));
+            if (rs > 2) y = __builtin_fmaxf(y, dpp<0x141>(y));
+            if (rs > 3) y = __builtin_fmaxf(y, dpp<0x140>(y));
+            v[u] = (gone >> (4 * G + u)) & 1 ? NEG_INF : y;
+          }
+          const int b4 = b + 4 * G;
+          if (b4 > top[nt]) continue;
+          typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+          float* out = A.score + to[nt] + b4;
+          if (hc > 0)                                  // what this lane has written for the heads before
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+              if (b4 + u <= top[nt]) v[u] = __builtin_fmaxf(v[u], out[u]);
+          if (b4 + 3 <= top[nt]) {
+            *(f32x4_a4*)out = v;
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+              if (b4 + u <= top[nt]) out[u] = v[u];
+          }
+        }
+      }
+    }
+  }
+}
+
+// --------------------------------------------------- selection of blocks
+//
+// The `want` largest of a row's scores beside the blocks that are always
+// taken, as a threshold on the scores' bits in the order of integers: bits
+// below those that all candidates share are settled from the top, each by one
+// count over the row (compare, ballot, population count), until a count meets
+// `want` exactly or the bits are used up; then equal ones are taken in order.
+// W waves a row, 64 W M blocks at most, M of them in a lane's registers: block
+// 64 (M wave + m) + lane.
+struct SelectArgs {
+  const float* score;
+  const int32_t *tok_start, *len;
+  int32_t* sel;
+  int n_req, n_tok, hkv, T, cols, n_sel, n_first, n_last, max_new;
+  Div by_hkv, by_max_new;
+};
+
+template <int W>
+struct Rendezvous {                                     // sums over a row's waves
+  int (*s)[W];
+  int turn = 0;
+  __device__ __forceinline__ explicit Rendezvous(int (*x)[W]) : s(x) {}
+  // of one number a wave: the sum, and the sum of the waves before this one
+  __device__ __forceinline__ int sum(int x, int* before) {
+    if constexpr (W == 1) {
+      *before = 0;
+      return x;
+    } else {
+      const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+      if (lane == 0) s[turn][wave] = x;
+      __syncthreads();
+      const int y = lane < W ? s[turn][lane] : 0;
+      turn ^= 1;
+      *before = wave_sum_i(lane < wave ? y : 0);
+      return wave_sum_i(y);
+    }
+  }
+};
+
+template <int W, int M>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_kv_select(SelectArgs A) {
+  __shared__ int shared[W == 1 ? 1 : 2][W];
+  Rendezvous<W> all(shared);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t row = W == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
+  const int w = W == 1 ? 0 : wave;
+  const int x = quot(row, A.by_hkv), h = row - x * A.hkv;
+  const int i = quot(x, A.by_max_new), j = x - i * A.max_new;
+  if (i >= A.n_req) return;
+  const int start = max(ld_const(A.tok_start + i), 0), end = max(ld_const(A.tok_start + i + 1), start);
+  const int shift = 31 - __builtin_clz(A.T);
+  if (j >= min(min(end, A.n_tok) - start, A.max_new)) return;
+  const int len = (int)min((int64_t)max(ld_const(A.len + i), 0), (int64_t)A.cols << shift);
+  const int p = max(len - (end - start), -(1 << 28)) + j;
+  const int nb = p < 0 ? 0 : min((p >> shift) + 1, A.cols);
+  const int64_t at = (int64_t)(start + j) * A.hkv + h;
+  const float* in = A.score + at * A.cols;
+  int32_t* out = A.sel + at * A.n_sel;
+  const int last0 = max(nb - A.n_last, 0);              // blocks below n_first and from last0 on are taken
+  const int must = min(nb, A.n_first) + nb - max(last0, min(nb, A.n_first));
+  const int want = min(A.n_sel, nb) - must;
+  // Keys in the order of integers: 0 for what is no candidate (taken already, not
+  // seen, -inf), the largest for NaN; -0 counts as 0.
+  uint32_t key[M];
+  uint32_t big = 0, small = 0xFFFFFFFFu;
+  const int b0 = 64 * M * w + lane;
+#pragma unroll
+  for (int m = 0; m < M; m++) {
+    const int b = b0 + 64 * m;
+    uint32_t u = b < nb ? __float_as_uint(in[b]) : 0xFF800000u;
+    const bool nan = (u & 0x7FFFFFFFu) > 0x7F800000u, none = u == 0xFF800000u || b < A.n_first || b >= last0;
+    if (u == 0x80000000u) u = 0;
+    u = (int)u < 0 ? ~u : u | 0x80000000u;
+    key[m] = none ? 0u : nan ? 0xFFFFFFFFu : u;
+    big = max(big, key[m]);
+    small = min(small, none ? 0xFFFFFFFFu : key[m]);
+  }
+  auto count = [&](uint32_t t, int* before) {           // candidates at t or above
+    int c = 0;
+#pragma unroll
+    for (int m = 0; m < M; m++) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[m] >= t));
+    return all.sum(c, before);
+  };
+  int before;
+  uint32_t t = want > 0 ? 1u : 0xFFFFFFFFu;             // all candidates, or none
+  const int have = count(1u, &before);
+  int ties = 0x7FFFFFFF;                                // of the equal ones at t: how many are taken
+  if (want <= 0) ties = 0;
+  else if (have > want) {
+    // range of the keys over the row
+    uint32_t hi = (uint32_t)wave_max_i((int)(big ^ 0x80000000u)) ^ 0x80000000u;
+    uint32_t lo = ~((uint32_t)wave_max_i((int)(~small ^ 0x80000000u)) ^ 0x80000000u);
+    if constexpr (W > 1) {
+      __shared__ uint32_t range[2][W];
+      if (lane == 0) { range[0][wave] = hi; range[1][wave] = lo; }
+      __syncthreads();
+#pragma unroll
+      for (int y = 0; y < W; y++) { hi = max(hi, range[0][y]); lo = min(lo, range[1][y]); }
+    }
+    int bit = hi == lo ? -1 : 31 - __builtin_clz(hi ^ lo);
+    t = bit < 0 ? hi : bit == 31 ? 0u : (hi >> (bit + 1)) << (bit + 1);
+    for (; bit >= 0; bit--) {
+      const uint32_t c = t | (1u << bit);
+      const int y = count(c, &before);
+      if (y < want) continue;
+      t = c;
+      if (y == want) break;
+    }
+    if (bit < 0) ties = want - (t == 0xFFFFFFFFu ? 0 : count(t + 1, &before));
+  }
+  // equal ones before this wave's, then the places of what is taken
+  int equal = 0;
+#pragma unroll
+  for (int m = 0; m < M; m++) equal += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[m] == t));
+  int seen = 0;
+  if (ties != 0x7FFFFFFF) all.sum(equal, &seen);
+  const uint64_t below = (1ull << lane) - 1;
+  uint64_t take[M];
+  int mine = 0;
+#pragma unroll
+  for (int m = 0; m < M; m++) {
+    const int b = b0 + 64 * m;
+    const uint64_t same = __builtin_amdgcn_ballot_w64(key[m] == t);
+    bool on = key[m] > t || (key[m] == t && (ties == 0x7FFFFFFF || seen + __builtin_popcountll(same & below) < ties));
+    on = on && key[m] != 0;
+    if (want <= 0) on = false;
+    on = on || (b < nb && (b < A.n_first || b >= last0));
+    seen += __builtin_popcountll(same);
+    take[m] = __builtin_amdgcn_ballot_w64(on);
+    mine += __builtin_popcountll(take[m]);
+  }
+  int pos;
+  const int total = all.sum(mine, &pos);
+#pragma unroll
+  for (int m = 0; m < M; m++) {
+    if ((take[m] >> lane) & 1) out[pos + __builtin_popcountll(take[m] & below)] = b0 + 64 * m;
+    pos += __builtin_popcountll(take[m]);
+  }
+  for (int y = total + 64 * w + lane; y < A.n_sel; y += 64 * W) out[y] = -1;
+}
+
+// ------------------------------------------------------------------ host
+bool touch(const void* a, int64_t an, const void* b, int64_t bn) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
+bool long_ok(const stq_kv_desc* d, const stq_attend_desc* a) { return attend_ok(d, a) && a->window == 0 && a->n_sink == 0; }
+uint64_t bounds_size(const stq_kv_desc* d) { return (uint64_t)d->n_blocks * d->n_kv_heads * 2 * d->d; }
+
+void fill(AttnArgs& A, const stq_kv_desc* d, const void* cache, const stq_attend_desc* a, const int32_t* table,
+          const int32_t* tok_start, const int32_t* len, const void* q, void* o, const Split& sp) {
+  A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.q = q; A.o = o;
+  A.po = A.pml = nullptr;
+  A.n_req = a->n_req; A.n_tok = a->n_tok; A.hq = a->n_heads; A.hkv = d->n_kv_heads; A.group = a->n_heads / d->n_kv_heads;
+  A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = a->table_cols; A.max_new = a->max_new;
+  A.window = A.sink = 0;
+  A.splits = sp.splits; A.per = sp.per; A.tiles = sp.tiles;
+  A.by_hkv = div_of(A.hkv); A.by_group = div_of(A.group); A.by_max_new = div_of(A.max_new); A.by_per = div_of(A.per);
+  A.qs = a->q_stride; A.os = a->o_stride;
+  A.scale = a->scale;
+}
+
+// Work of the blocks' attention: by what a whole list holds.
+Split blocks_split(const stq_kv_desc* d, const stq_attend_desc* a, int n_sel) {
+  Split s;
+  const int64_t rows = a->n_heads / d->n_kv_heads;
+  s.staged = s.once = false;
+  s.tile_rows = rows > 16 ? 32 : 16;
+  s.tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
+  cut(&s, (int64_t)a->n_req * a->max_new * d->n_kv_heads * s.tiles, (int64_t)n_sel * d->block_tokens / 32);
+  return s;
+}
+
+// Parts of the shared prefixes and of the requests' own tokens.
+struct Shares { Split own, pre; int64_t pre_units; };
+constexpr int64_t MOST_PARTS = 64;                     // of each kind: the join holds 128 parts' statistics in its lanes
+Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_shared_desc* g) {
+  Shares s;
+  const int64_t group = a->n_heads / d->n_kv_heads, rows = (int64_t)a->max_new * group;
+  s.own.once = s.pre.once = false;
+  s.own.staged = rows > STAGED_ROWS;
+  s.own.tile_rows = s.own.staged ? 32 * TILE_WAVES : rows > 16 ? 32 : 16;
+  s.own.tiles = (int)((rows + s.own.tile_rows - 1) / s.own.tile_rows);
+  cut(&s.own, (int64_t)a->n_req * d->n_kv_heads * s.own.tiles, ((int64_t)a->max_len + 31) / 32);
+  const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
+  const int64_t mean = g->n_groups > 0 ? all / g->n_groups : 0;
+  s.pre.staged = mean > STAGED_ROWS;
+  s.pre.tile_rows = s.pre.staged ? 32 * TILE_WAVES : mean > 16 ? 32 : 16;
+  s.pre_units = (all + s.pre.tile_rows - 1) / s.pre.tile_rows + g->n_groups;
+  s.pre.tiles = 1;
+  cut(&s.pre, ((all + s.pre.tile_rows - 1) / s.pre.tile_rows) * d->n_kv_heads, (int64_t)g->max_prefix / 32 + 1);
+  for (Split* x : {&s.own, &s.pre})
+    if (x->splits > MOST_PARTS) {
+      const int64_t chunks = (int64_t)x->per * x->splits;
+      x->per = (int)(((chunks + MOST_PARTS - 1) / MOST_PARTS + 3) & ~3ll);
+      x->splits = (int)((chunks + x->per - 1) / x->per);
+    }
+  if (s.pre.waves == 16) s.pre.waves = 4;
+  if (s.own.waves == 16) s.own.waves = 4;
+  return s;
+}
+
+template <int D, int TYPE>
+void launch_blocks(const LongArgs& A, const Split& s, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)A.n_req * A.max_new * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
+  if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, LIST>), grid, dim3(256), 0, st, A);
+  else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16, false, LIST>), grid, dim3(1024), 0, st, A);
+  else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, false, LIST>), grid, dim3(256), 0, st, A);
+  if (A.splits > 1) {
+    const dim3 rows((unsigned)(A.n_req * A.max_new), (unsigned)((A.hq + 3) / 4));
+    hipLaunchKernelGGL((k_attend_join<D, TYPE, LIST>), rows, dim3(256), 0, st, A, 0);
+  }
+}
+
+template <int D, int TYPE>
+void launch_shared(const LongArgs& A, const Shares& s, hipStream_t st) {
+  if (A.n_groups > 0) {
+    const int64_t units = s.pre_units * A.hkv;
+    if (s.pre.staged) {
+      hipLaunchKernelGGL((k_attend_tiles<D, TYPE, PREFIX>), dim3((unsigned)(units * s.pre.splits)), dim3(64 * TILE_WAVES), 0, st, A);
+    } else {
+      const dim3 grid((unsigned)units, 1u, (unsigned)s.pre.splits);
+      if (s.pre.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, PREFIX>), grid, dim3(256), 0, st, A);
+      else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, false, PREFIX>), grid, dim3(256), 0, st, A);
+    }
+  }
+  if (s.own.staged) {
+    const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
+    hipLaunchKernelGGL((k_attend_tiles<D, TYPE, SUFFIX>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
+  } else {
+    const dim3 grid((unsigned)(A.n_req * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
+    if (s.own.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, SUFFIX>), grid, dim3(256), 0, st, A);
+    else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, false, SUFFIX>), grid, dim3(256), 0, st, A);
+  }
+  if (A.n_groups > 0 || A.splits > 1) {
+    const dim3 rows((unsigned)(A.n_req * A.max_new), (unsigned)((A.hq + 3) / 4));
+    hipLaunchKernelGGL((k_attend_join<D, TYPE, SUFFIX>), rows, dim3(256), 0, st, A, __builtin_ctz(s.own.tile_rows));
+  }
+}
+
+template <int D, int TYPE>
+void launch_score(const ScoreArgs& A, int nt, unsigned z, hipStream_t st) {
+  const int tokens = nt * (16 >> A.rows_shift);
+  const dim3 grid((unsigned)(A.n_req * A.hkv), (unsigned)((A.max_new + tokens - 1) / tokens), z);
+  if (nt == 1) hipLaunchKernelGGL((k_kv_score<D, TYPE, 1>), grid, dim3(256), 0, st, A);
+  else hipLaunchKernelGGL((k_kv_score<D, TYPE, 4>), grid, dim3(256), 0, st, A);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t stq_kv_bounds_bytes(const stq_kv_desc* d) { return kv_ok(d) ? (size_t)bounds_size(d) : 0; }
+
+stq_status stq_kv_bounds(const stq_kv_desc* d, const void* cache, size_t bytes, int32_t n_req, int32_t max_new,
+                         const int32_t* table, int32_t table_cols, const int32_t* tok_start, const int32_t* len,
+                         void* bounds, hipStream_t st) {
+  const stq_status s = kv_check(d, cache, bytes);
+  if (s != STQ_OK) return s;
+  if (n_req < 0 || max_new < 1 || table_cols < 1 || (int64_t)table_cols * d->block_tokens > (1ll << 30)) return STQ_ERR_ARG;
+  if (n_req == 0) return STQ_OK;
+  if (!table || !tok_start || !len || !bounds) return STQ_ERR_ARG;
+  if (!aligned(bounds)) return STQ_ERR_LAYOUT;
+  if (touch(bounds, (int64_t)bounds_size(d), cache, (int64_t)kv_size(d))) return STQ_ERR_ARG;
+  BoundsArgs A;
+  A.cache = (const uint8_t*)cache; A.table = table; A.tok_start = tok_start; A.len = len; A.bounds = (uint8_t*)bounds;
+  A.n_req = n_req; A.hkv = d->n_kv_heads; A.T = d->block_tokens; A.n_blocks = d->n_blocks; A.cols = table_cols; A.max_new = max_new;
+  const int64_t span = ((int64_t)max_new - 1) / d->block_tokens + 2;       // blocks that so many tokens touch at most
+  A.span = (int)(span < table_cols ? span : table_cols);
+  A.by_span = div_of(A.span);
+  if ((int64_t)n_req * A.span * 256 > MOST_THREADS) return STQ_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)(n_req * A.span), (unsigned)((A.hkv + 3) / 4)), b(256);
+  if (d->d == 64) hipLaunchKernelGGL((k_kv_bounds<64>), g, b, 0, st, A);
+  else hipLaunchKernelGGL((k_kv_bounds<128>), g, b, 0, st, A);
+  return launched();
+}
+
+stq_status stq_kv_score(const stq_kv_desc* d, const stq_attend_desc* a, const void* bounds, const int32_t* table,
+                        const int32_t* tok_start, const int32_t* len, const void* q, float* score, hipStream_t st) {
+  if (!kv_ok(d) || !long_ok(d, a)) return STQ_ERR_ARG;
+  if (a->n_req == 0 || a->n_tok == 0) return STQ_OK;
+  if (!bounds || !table || !tok_start || !len || !q || !score) return STQ_ERR_ARG;
+  const int64_t w = (int64_t)a->n_heads * d->d;
+  if (!aligned(bounds) || !aligned(q) || !aligned(score) || !stride_ok(a->q_stride, w, a->type)) return STQ_ERR_LAYOUT;
+  const int64_t out = (int64_t)a->n_tok * d->n_kv_heads * a->table_cols * 4;
+  if (touch(score, out, bounds, (int64_t)bounds_size(d)) || touch(score, out, q, ((a->n_tok - 1) * a->q_stride + w) * 2)) return STQ_ERR_ARG;
+  Split none;
+  none.splits = none.per = none.tiles = 1;
+  ScoreArgs A;
+  fill(A, d, nullptr, a, table, tok_start, len, q, nullptr, none);
+  A.bounds = (const uint8_t*)bounds; A.score = score;
+  A.rows_shift = 0;
+  while (A.rows_shift < 4 && (1 << A.rows_shift) < A.group) A.rows_shift++;
+  const int nt = a->max_new > (16 >> A.rows_shift) ? 4 : 1;
+  const int64_t toks = nt * (16 >> A.rows_shift), units = (int64_t)a->n_req * A.hkv, ys = (a->max_new + toks - 1) / toks;
+  int64_t cols = ((int64_t)a->max_len + A.T - 1) / A.T;
+  if (cols > a->table_cols) cols = a->table_cols;
+  const int64_t tiles = (cols + 15) / 16;
+  int64_t run = tiles * units * ys / 8192;
+  A.tile_run = (int)(run < 1 ? 1 : run > 8 ? 8 : run);
+  int64_t z = (tiles + 4 * A.tile_run - 1) / (4 * A.tile_run);
+  if (z > 65535) z = 65535;                             // (the kernel goes round)
+  if (units * 256 > MOST_THREADS || ys > 65535) return STQ_ERR_UNSUPPORTED;
+  if (d->d == 64) {
+    if (a->type == STQ_BF16) launch_score<64, STQ_BF16>(A, nt, (unsigned)z, st);
+    else launch_score<64, STQ_FP16>(A, nt, (unsigned)z, st);
+  } else {
+    if (a->type == STQ_BF16) launch_score<128, STQ_BF16>(A, nt, (unsigned)z, st);
+    else launch_score<128, STQ_FP16>(A, nt, (unsigned)z, st);
+  }
+  return launched();
+}
+
+stq_status stq_kv_select(const stq_select_desc* c, const int32_t* tok_start, const int32_t* len, const float* score,
+                         int32_t* sel, hipStream_t st) {
+  if (!c || c->n_req < 0 || c->n_tok < 0 || c->n_tok > (1 << 28) || c->n_kv_heads < 1 || c->n_kv_heads > 4096) return STQ_ERR_ARG;
+  if (c->block_tokens != 32 && c->block_tokens != 64 && c->block_tokens != 128 && c->block_tokens != 256) return STQ_ERR_ARG;
+  if (c->table_cols < 1 || (int64_t)c->table_cols * c->block_tokens > (1ll << 30) || c->max_new < 1) return STQ_ERR_ARG;
+  if (c->n_sel < 1 || c->n_first < 0 || c->n_last < 0 || (int64_t)c->n_first + c->n_last > c->n_sel) return STQ_ERR_ARG;
+  if (c->table_cols > 32768) return STQ_ERR_UNSUPPORTED;
+  if (c->n_req == 0 || c->n_tok == 0) return STQ_OK;
+  if (!tok_start || !len || !score || !sel) return STQ_ERR_ARG;
+  if (!aligned(score) || !aligned(sel)) return STQ_ERR_LAYOUT;
+  const int64_t rows = (int64_t)c->n_tok * c->n_kv_heads;
+  if (touch(sel, rows * c->n_sel * 4, score, rows * c->table_cols * 4)) return STQ_ERR_ARG;
+  SelectArgs A;
+  A.score = score; A.tok_start = tok_start; A.len = len; A.sel = sel;
+  A.n_req = c->n_req; A.n_tok = c->n_tok; A.hkv = c->n_kv_heads; A.T = c->block_tokens; A.cols = c->table_cols;
+  A.n_sel = c->n_sel; A.n_first = c->n_first; A.n_last = c->n_last; A.max_new = c->max_new;
+  A.by_hkv = div_of(A.hkv); A.by_max_new = div_of(A.max_new);
+  const int waves = A.cols <= 512 ? 1 : A.cols <= 2048 ? 4 : 16;
+  const int64_t units = (int64_t)c->n_req * c->max_new * c->n_kv_heads, groups = waves == 1 ? (units + 3) / 4 : units;
+  if (units > INT32_MAX || groups * (waves == 1 ? 256 : 64 * waves) > MOST_THREADS) return STQ_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)groups);
+  if (A.cols <= 128) hipLaunchKernelGGL((k_kv_select<1, 2>), g, dim3(256), 0, st, A);
+  else if (waves == 1) hipLaunchKernelGGL((k_kv_select<1, 8>), g, dim3(256), 0, st, A);
+  else if (waves == 4) hipLaunchKernelGGL((k_kv_select<4, 8>), g, dim3(256), 0, st, A);
+  else if (A.cols <= 8192) hipLaunchKernelGGL((k_kv_select<16, 8>), g, dim3(1024), 0, st, A);
+  else hipLaunchKernelGGL((k_kv_select<16, 32>), g, dim3(1024), 0, st, A);
+  return launched();
+}
+
+size_t stq_kv_attend_blocks_bytes(const stq_kv_desc* d, const stq_attend_desc* a, int32_t n_sel) {
+  if (!kv_ok(d) || !long_ok(d, a) || n_sel < 1 || (int64_t)n_sel * d->block_tokens > (1ll << 30)) return 0;
+  const Split s = blocks_split(d, a, n_sel);
+  return s.splits <= 1 ? 0 : (size_t)s.splits * a->n_tok * a->n_heads * (d->d + 2) * 4;
+}
+
+stq_status stq_kv_attend_blocks(const stq_kv_desc* d, const void* cache, size_t bytes, const stq_attend_desc* a,
+                                int32_t n_sel, const int32_t* table, const int32_t* tok_start, const int32_t* len,
+                                const int32_t* sel, const void* q, void* o, void* work, size_t work_bytes, hipStream_t st) {
+  const stq_status s = kv_check(d, cache, bytes);
+  if (s != STQ_OK) return s;
+  if (!long_ok(d, a) || n_sel < 1 || (int64_t)n_sel * d->block_tokens > (1ll << 30)) return STQ_ERR_ARG;
+  if (a->n_req == 0 || a->n_tok == 0) return STQ_OK;
+  if (!table || !tok_start || !len || !sel || !q || !o) return STQ_ERR_ARG;
+  const int64_t w = (int64_t)a->n_heads * d->d;
+  if (!aligned(sel) || !aligned(q) || !aligned(o) || !stride_ok(a->q_stride, w, a->type) || !stride_ok(a->o_stride, w, a->type))
+    return STQ_ERR_LAYOUT;
+  const Rows rq = {q, a->q_stride * 2, w * 2}, ro = {o, a->o_stride * 2, w * 2};
+  if (!same(rq, ro) && meet(rq, ro, a->n_tok)) return STQ_ERR_ARG;
+  if (touch(o, ((a->n_tok - 1) * a->o_stride + w) * 2, sel, (int64_t)a->n_tok * d->n_kv_heads * n_sel * 4)) return STQ_ERR_ARG;
+  const Split sp = blocks_split(d, a, n_sel);
+  const size_t need = stq_kv_attend_blocks_bytes(d, a, n_sel);
+  if (need > 0 && (!work || !aligned(work) || work_bytes < need)) return STQ_ERR_LAYOUT;
+  const int64_t units = (int64_t)a->n_req * a->max_new;
+  if (units * a->n_heads > INT32_MAX || units * d->n_kv_heads * 64 * sp.waves > MOST_THREADS || (sp.splits > 1 && units * 256 > MOST_THREADS))
+    return STQ_ERR_UNSUPPORTED;
+  LongArgs A;
+  fill(A, d, cache, a, table, tok_start, len, q, o, sp);
+  A.sel = sel; A.n_sel = n_sel;
+  A.group_start = A.prefix = nullptr; A.shared = nullptr;
+  A.n_groups = A.pre_splits = A.pre_per = 0;
+  A.po = (float*)work;
+  A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
+  if (d->d == 64) {
+    if (a->type == STQ_BF16) launch_blocks<64, STQ_BF16>(A, sp, st);
+    else launch_blocks<64, STQ_FP16>(A, sp, st);
+  } else {
+    if (a->type == STQ_BF16) launch_blocks<128, STQ_BF16>(A, sp, st);
+    else launch_blocks<128, STQ_FP16>(A, sp, st);
+  }
+  return launched();
+}
+
+size_t stq_kv_attend_shared_bytes(const stq_kv_desc* d, const stq_attend_desc* a, const stq_shared_desc* g) {
+  if (!kv_ok(d) || !long_ok(d, a) || !g || g->n_groups < 0 || g->max_prefix < 0) return 0;
+  const Shares s = shares_of(d, a, g);
+  return (size_t)(s.own.splits + s.pre.splits) * a->n_tok * a->n_heads * (d->d + 2) * 4 + ((size_t)a->n_req * 4 + 15) / 16 * 16;
+}
+
+stq_status stq_kv_attend_shared(const stq_kv_desc* d, const void* cache, size_t bytes, const stq_attend_desc* a,
+                                const stq_shared_desc* g, const int32_t* table, const int32_t* tok_start, const int32_t* len,
+                                const int32_t* group_start, const int32_t* prefix, const void* q, void* o, void* work,
+                                size_t work_bytes, hipStream_t st) {
+  const stq_status s = kv_check(d, cache, bytes);
+  if (s != STQ_OK) return s;
+  if (!long_ok(d, a) || !g || g->n_groups < 0 || g->max_prefix < 0) return STQ_ERR_ARG;
+  if (a->n_req == 0 || a->n_tok == 0) return STQ_OK;
+  if (!table || !tok_start || !len || (g->n_groups > 0 && (!group_start || !prefix)) || !q || !o) return STQ_ERR_ARG;
+  const int64_t w = (int64_t)a->n_heads * d->d;
+  if (!aligned(q) || !aligned(o) || !stride_ok(a->q_stride, w, a->type) || !stride_ok(a->o_stride, w, a->type))
+    return STQ_ERR_LAYOUT;
+  const Rows rq = {q, a->q_stride * 2, w * 2}, ro = {o, a->o_stride * 2, w * 2};
+  if (!same(rq, ro) && meet(rq, ro, a->n_tok)) return STQ_ERR_ARG;
+  const Shares sp = shares_of(d, a, g);
+  const size_t need = stq_kv_attend_shared_bytes(d, a, g);
+  if (!work || !aligned(work) || work_bytes < need) return STQ_ERR_LAYOUT;
+  const int64_t groups = (int64_t)a->n_req * d->n_kv_heads, pre = sp.pre_units * d->n_kv_heads;
+  if ((int64_t)a->n_req * a->max_new * a->n_heads > INT32_MAX || (int64_t)a->n_tok * a->n_heads > INT32_MAX ||
+      (sp.own.staged ? groups * sp.own.tiles * sp.own.splits : groups) * 256 > MOST_THREADS ||
+      (sp.pre.staged ? pre * sp.pre.splits : pre) * 256 > MOST_THREADS || (int64_t)a->n_req * a->max_new * 256 > MOST_THREADS)
+    return STQ_ERR_UNSUPPORTED;
+  LongArgs A;
+  fill(A, d, cache, a, table, tok_start, len, q, o, sp.own);
+  A.sel = nullptr; A.n_sel = 0;
+  A.group_start = group_start; A.prefix = prefix;
+  A.n_groups = g->n_groups; A.pre_splits = sp.pre.splits; A.pre_per = sp.pre.per;
+  const int64_t rows = (int64_t)(sp.own.splits + sp.pre.splits) * a->n_tok * a->n_heads;
+  A.po = (float*)work;
+  A.pml = A.po + rows * d->d;
+  A.shared = (int32_t*)(A.pml + 2 * rows);
+  if (d->d == 64) {
+    if (a->type == STQ_BF16) launch_shared<64, STQ_BF16>(A, sp, st);
+    else launch_shared<64, STQ_FP16>(A, sp, st);
+  } else {
+    if (a->type == STQ_BF16) launch_shared<128, STQ_BF16>(A, sp, st);
+    else launch_shared<128, STQ_FP16>(A, sp, st);
+  }
+  return launched();
+}
+
+}  // extern "C"
