@@ -118,14 +118,17 @@ struct AttnArgs {
 // that a token's and head's list names (one query token a workgroup); PREFIX the
 // tokens that a group of requests shares, for the rows of all of them; SUFFIX
 // those of a request behind what its group shares.
-enum Mode { SPAN, LIST, PREFIX, SUFFIX };
+enum Mode { SPAN, LIST, PREFIX, SUFFIX };              // (k_attend_rows takes PREFIX and SUFFIX in one launch: SUFFIX)
 
 struct LongArgs : AttnArgs {
   const int32_t* sel;                    // LIST: [n_tok][hkv][n_sel] block columns
   int n_sel;
   const int32_t *group_start, *prefix;   // PREFIX and SUFFIX: [n_groups + 1], [n_groups]
-  int n_groups, pre_splits, pre_per;     // parts of a prefix at most, chunks of one
-  int32_t* shared;                       // [n_req] tokens that the request's group shares
+  int n_groups, pre_per;                 // chunks of a prefix' part at least
+  int slot0;                             // parts of a prefix at most; in the workspace those of the requests' own tokens follow
+  float pre_fill;                        // heads / workgroups that fill the card
+  int pre_units;                         // SUFFIX: workgroups (times heads) that take a prefix' part
+  int32_t* shared;                       // [n_req] tokens that the request's group shares, then the chunks of a prefix' part
 };
 template <int MODE> using ArgsOf = std::conditional_t<MODE == SPAN, AttnArgs, LongArgs>;
 
@@ -158,69 +161,162 @@ __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
   return req_of(A, ld_const(A.tok_start + i), ld_const(A.tok_start + i + 1), ld_const(A.len + i));
 }
 
-// The member requests [s, e) of a group and the tokens that they share: whole
-// blocks, and none behind the first new token of any member that has one, so that
-// every row sees all of them.  By all lanes of a wave.
-struct Group { int s, e, len; };
+// What the workgroups of requests that share prefixes have to know of the whole
+// batch, by all lanes of a wave: `Members` of a group g are requests [s, e) with
+// query rows [first, last) of q; they share `len` tokens: whole blocks, and none
+// behind the first new token of any member that has one, so that every row sees
+// all of them.  Up to 256 requests in 64 groups are loaded at once, one request or
+// group a lane, and the rest is exchanged between lanes: a chain of one load
+// instead of three or four, each a microsecond where the lines are cold.
+struct Members { int s, e, first, last, len; };
 __device__ __forceinline__ int wave_max_i(int x);
-__device__ __forceinline__ Group group_at(const LongArgs& A, int g) {
-  Group r;
-  r.s = min(max(ld_const(A.group_start + g), 0), A.n_req);
-  r.e = min(max(ld_const(A.group_start + g + 1), r.s), A.n_req);
-  int last = (int)min((int64_t)max(ld_const(A.prefix + g), 0), (int64_t)A.cols * A.T);
-  for (int b = r.s; b < r.e; b += 64) {
-    const int i = min(b + (int)(threadIdx.x & 63), r.e - 1);
-    const int start = A.tok_start[i], end = A.tok_start[i + 1];
-    if (end > start) last = min(last, req_of(A, start, end, A.len[i]).base);
-  }
-  r.len = max(-wave_max_i(-last), 0) & ~(A.T - 1);
-  return r;
-}
-// What request i shares (0 in no group).  The group that holds it is the last
-// one that starts at or before it.
-__device__ __forceinline__ int shared_of(const LongArgs& A, int i) {
-  int g = -1;
-  for (int b = 0; b < A.n_groups; b += 64) {
-    const int x = b + (int)(threadIdx.x & 63);
-    const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(x < A.n_groups && A.group_start[min(x, A.n_groups - 1)] <= i));
-    if (n > 0) g = b + n - 1;
-  }
-  if (g < 0) return 0;
-  const Group r = group_at(A, g);
-  return i < r.e ? r.len : 0;
-}
-// First and last query token's row of a group, in q and o.
-__device__ __forceinline__ void group_tokens(const LongArgs& A, int s, int e, int* first, int* last) {
-  *first = min(max(A.tok_start[s], 0), A.n_tok);
-  *last = min(max(A.tok_start[e], *first), A.n_tok);
-}
-// The x-th tile of rows of all groups that share anything: group and tile of it.
-__device__ __forceinline__ bool group_tile(const LongArgs& A, int rows_of_tile, int x, int* group, int* tile) {
-  const int lane = threadIdx.x & 63;
-  for (int b = 0; b < A.n_groups; b += 64) {
-    const int g = min(b + lane, A.n_groups - 1);
-    const int s = min(max(A.group_start[g], 0), A.n_req), e = min(max(A.group_start[g + 1], s), A.n_req);
-    int first, last;
-    group_tokens(A, s, e, &first, &last);
-    const int mine = b + lane < A.n_groups && A.prefix[g] >= A.T
-                         ? (int)(((int64_t)(last - first) * A.group + rows_of_tile - 1) / rows_of_tile) : 0;
-    int sum = mine;                                      // inclusive
+struct Whole {
+  static constexpr int N = 4;                          // registers of 64 requests
+  const LongArgs& A;
+  bool fits;
+  int start[N + 1], end[N], base[N];                   // base: position of the first new token, the largest without one
+  int g0, g1, pre;                                     // lane = group
+  __device__ __forceinline__ explicit Whole(const LongArgs& args) : A(args) {
+    const int lane = threadIdx.x & 63;
+    fits = A.n_req <= 64 * N && A.n_groups <= 64 && A.n_groups > 0;
+    if (!fits) return;
+    g0 = A.group_start[min(lane, A.n_groups)];
+    g1 = A.group_start[min(lane + 1, A.n_groups)];
+    pre = A.prefix[min(lane, A.n_groups - 1)];
+    int len[N];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += y;
+    for (int r = 0; r <= N; r++) start[r] = 64 * r <= A.n_req ? A.tok_start[min(64 * r + lane, A.n_req)] : 0;
+#pragma unroll
+    for (int r = 0; r < N; r++) {
+      end[r] = 64 * r < A.n_req ? A.tok_start[min(64 * r + lane + 1, A.n_req)] : 0;
+      len[r] = 64 * r < A.n_req ? A.len[min(64 * r + lane, A.n_req - 1)] : 0;
     }
-    const int all = __builtin_amdgcn_readlane(sum, 63);
-    if (x < all) {
-      const int k = __builtin_ctzll(__builtin_amdgcn_ballot_w64(sum > x));
-      *group = b + k;
-      *tile = x - (__builtin_amdgcn_readlane(sum, k) - __builtin_amdgcn_readlane(mine, k));
-      return true;
-    }
-    x -= all;
+#pragma unroll
+    for (int r = 0; r < N; r++) base[r] = end[r] > start[r] ? req_of(A, start[r], end[r], len[r]).base : INT32_MAX;
+    g0 = min(max(g0, 0), A.n_req);
+    g1 = min(max(g1, g0), A.n_req);
+    pre = shared_blocks(pre);
   }
-  return false;
-}
+  __device__ __forceinline__ int shared_blocks(int x) const { return (int)min((int64_t)max(x, 0), (int64_t)A.cols * A.T) & ~(A.T - 1); }
+  // tok_start of request x (any lane's own)
+  __device__ __forceinline__ int start_at(int x) const {
+    int v = __shfl(start[0], x & 63, 64);
+#pragma unroll
+    for (int r = 1; r <= N; r++) {
+      if (64 * r > A.n_req) break;
+      const int y = __shfl(start[r], x & 63, 64);
+      v = x >> 6 == r ? y : v;
+    }
+    return v;
+  }
+  __device__ __forceinline__ Members group(int g) const {
+    Members m;
+    int least = INT32_MAX;
+    if (fits) {
+      m.s = __builtin_amdgcn_readlane(g0, g);
+      m.e = __builtin_amdgcn_readlane(g1, g);
+      m.len = __builtin_amdgcn_readlane(pre, g);
+#pragma unroll
+      for (int r = 0; r < N; r++) {
+        const int x = 64 * r + (int)(threadIdx.x & 63);
+        least = min(least, x >= m.s && x < m.e ? base[r] : INT32_MAX);
+      }
+      m.first = __builtin_amdgcn_readfirstlane(start_at(m.s));
+      m.last = __builtin_amdgcn_readfirstlane(start_at(m.e));
+    } else {
+      m.s = min(max(ld_const(A.group_start + g), 0), A.n_req);
+      m.e = min(max(ld_const(A.group_start + g + 1), m.s), A.n_req);
+      m.len = shared_blocks(ld_const(A.prefix + g));
+      for (int b = m.s; b < m.e; b += 64) {
+        const int i = min(b + (int)(threadIdx.x & 63), m.e - 1);
+        const int x = A.tok_start[i], y = A.tok_start[i + 1];
+        if (y > x) least = min(least, req_of(A, x, y, A.len[i]).base);
+      }
+      m.first = A.tok_start[m.s];
+      m.last = A.tok_start[m.e];
+    }
+    m.first = min(max(m.first, 0), A.n_tok);
+    m.last = min(max(m.last, m.first), A.n_tok);
+    m.len = max(min(m.len, -wave_max_i(-least)), 0) & ~(A.T - 1);
+    return m;
+  }
+  // What request i shares (0 in no group).  The group that holds it is the last one
+  // that starts at or before it.
+  __device__ __forceinline__ int shared_of(int i) const {
+    int g = -1;
+    if (fits) {
+      g = __builtin_popcountll(__builtin_amdgcn_ballot_w64((int)(threadIdx.x & 63) < A.n_groups && g0 <= i)) - 1;
+    } else {
+      for (int b = 0; b < A.n_groups; b += 64) {
+        const int x = b + (int)(threadIdx.x & 63);
+        const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(x < A.n_groups && A.group_start[min(x, A.n_groups - 1)] <= i));
+        if (n > 0) g = b + n - 1;
+      }
+    }
+    if (g < 0) return 0;
+    const Members m = group(g);
+    return i < m.e ? m.len : 0;
+  }
+  // The x-th part of all prefixes' work: group, tile of its rows, part of its chunks
+  // and how many chunks a part has, the same for all.  Parts are sized by what all
+  // groups together have to do, so that the card is filled once (with parts for a
+  // whole group of the longest prefix a host can only guess: four groups of 12,000
+  // to 16,384 shared tokens 235 us, 199 by the best fixed size).
+  struct Part { int g, tile, sp, per; };
+  __device__ __forceinline__ bool part(int rows_of_tile, int x, Part* r) const {
+    const int lane = threadIdx.x & 63;
+    float total = 0.0f;
+    int most = 0;
+    auto of = [&](int b, int* tiles, int* chunks) {      // of group b + lane
+      int s = g0, e = g1, first, last, share = pre;
+      if (fits) {
+        first = start_at(s);
+        last = start_at(e);
+      } else {
+        const int y = min(b + lane, A.n_groups - 1);
+        s = min(max(A.group_start[y], 0), A.n_req);
+        e = min(max(A.group_start[y + 1], s), A.n_req);
+        share = shared_blocks(A.prefix[y]);
+        first = A.tok_start[s];
+        last = A.tok_start[e];
+      }
+      first = min(max(first, 0), A.n_tok);
+      last = min(max(last, first), A.n_tok);
+      const bool on = b + lane < A.n_groups && share > 0;
+      *tiles = on ? (int)(((int64_t)(last - first) * A.group + rows_of_tile - 1) / rows_of_tile) : 0;
+      *chunks = on ? share >> 5 : 0;
+    };
+    int tiles, chunks;
+    for (int b = 0; b < A.n_groups; b += 64) {
+      of(b, &tiles, &chunks);
+      total += wave_sum((float)tiles * (float)chunks);
+      most = max(most, wave_max_i(chunks));
+    }
+    const int fill = (int)__builtin_fminf(total * A.pre_fill, 0x1p30f);
+    r->per = (max(max(fill, A.pre_per), (most + A.slot0 - 1) / A.slot0) + 3) & ~3;
+    for (int b = 0; b < A.n_groups; b += 64) {
+      if (A.n_groups > 64) of(b, &tiles, &chunks);
+      const int parts = (chunks + r->per - 1) / r->per, mine = tiles * parts;
+      int sum = mine;                                    // inclusive
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(sum, d, 64);
+        if (lane >= d) sum += y;
+      }
+      const int all = __builtin_amdgcn_readlane(sum, 63);
+      if (x < all) {
+        const int k = __builtin_ctzll(__builtin_amdgcn_ballot_w64(sum > x));
+        const int y = x - (__builtin_amdgcn_readlane(sum, k) - __builtin_amdgcn_readlane(mine, k)), t = __builtin_amdgcn_readlane(tiles, k);
+        r->g = b + k;
+        r->sp = y / t;                                   // (the tiles of a part side by side: they read the same tokens)
+        r->tile = y - r->sp * t;
+        return true;
+      }
+      x -= all;
+    }
+    return false;
+  }
+};
 // Entries of a list up to its last one that names a block the token at position
 // p may see.  By all lanes of a wave.
 __device__ __forceinline__ bool listed(const LongArgs& A, int col, int p) { return col >= 0 && col < A.cols && (int64_t)col * A.T <= p; }
@@ -234,22 +330,14 @@ __device__ __forceinline__ int entries_of(const LongArgs& A, const int32_t* list
   return n;
 }
 
-// Where part sp of a row lies in the workspace: a prefix' parts, then the request's own.
-template <int MODE>
-__device__ __forceinline__ int slot_of(const ArgsOf<MODE>& A, int sp) {
-  if constexpr (MODE == SUFFIX) return A.pre_splits + sp;
-  else return sp;
-}
-
 // Chunks of one part of a request's work: the host's size for a request of the
 // stated longest length, more for a request that is longer than that (a
 // multiple of four: one per wave).  Shorter requests have fewer parts, all of
 // one size.
-__device__ __forceinline__ int split_into(int total, int per, int splits) {
-  if (total <= per * splits) return per;
-  return ((total + splits - 1) / splits + 3) & ~3;
+__device__ __forceinline__ int split_chunks(const AttnArgs& A, int total) {
+  if (total <= A.per * A.splits) return A.per;
+  return ((total + A.splits - 1) / A.splits + 3) & ~3;
 }
-__device__ __forceinline__ int split_chunks(const AttnArgs& A, int total) { return split_into(total, A.per, A.splits); }
 
 __device__ __forceinline__ float max_quads(float x) {   // over the four 16-lane groups
   auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -568,17 +656,33 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
   // the splits slowest: a short request has none of the last ones, and
   // neighbouring workgroups go to different XCDs
   int i = quot(blockIdx.x, A.by_hkv), tile = blockIdx.y;
-  const int h = blockIdx.x - i * A.hkv, sp = blockIdx.z;
+  const int h = blockIdx.x - i * A.hkv;
+  int sp = blockIdx.z;
   Req R;
-  if constexpr (MODE == PREFIX) {
-    int g;
-    if (!group_tile(A, 16 * NT, i, &g, &tile)) return;
-    const Group r = group_at(A, g);
-    int last;
-    group_tokens(A, r.s, r.e, &R.first, &last);
-    R.n_new = last - R.first;
-    R.base = r.len;                                      // (no row lies before what is shared)
-    i = r.s;                                             // by the table of the first
+  int shared = 0, pre_per = 0;
+  bool pre = false;            // SUFFIX: a tile of rows of a whole group over what they share
+  if constexpr (MODE == SUFFIX) {
+    const Whole whole_batch(A);
+    if (i < A.pre_units) {
+      if (tile > 0 || sp > 0) return;
+      pre = true;
+      Whole::Part part;
+      const bool on = whole_batch.part(16 * NT, i, &part);
+      if (blockIdx.x == 0 && threadIdx.x == 0) A.shared[A.n_req] = part.per;
+      if (!on) return;
+      const Members m = whole_batch.group(part.g);
+      tile = part.tile;
+      sp = part.sp;
+      pre_per = part.per;
+      R.first = m.first;
+      R.n_new = m.last - m.first;
+      R.base = m.len;                                    // (no row lies before what is shared)
+      i = m.s;                                           // by the table of the first
+    } else {
+      i -= A.pre_units;
+      R = req_args(A, i);
+      shared = whole_batch.shared_of(i);
+    }
   } else if constexpr (MODE == LIST) {
     const int x = i;
     i = quot(x, A.by_max_new);
@@ -591,10 +695,10 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
   } else {
     R = req_args(A, i);
   }
-  const int fresh = MODE == PREFIX ? R.n_new : min(R.n_new, A.max_new), rows = fresh * A.group, row0 = tile * 16 * NT;
+  const int fresh = pre ? R.n_new : min(R.n_new, A.max_new), rows = fresh * A.group, row0 = tile * 16 * NT;
   if (row0 >= rows) return;
   int p0 = R.base, p1 = R.base + fresh - 1;             // positions of the tile's first and last row
-  if (MODE == SPAN || MODE == SUFFIX)
+  if (MODE == SPAN || (MODE == SUFFIX && !pre))
     if (A.tiles > 1) {
       p0 = R.base + quot(row0, A.by_group);
       p1 = R.base + quot(min(row0 + 16 * NT, rows) - 1, A.by_group);
@@ -609,11 +713,10 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
     list = A.sel + ((int64_t)R.first * A.hkv + h) * A.n_sel;
     sn.total = entries_of(A, list, p0) * (A.T >> 5);
     per = split_chunks(A, sn.total);
-  } else if constexpr (MODE == PREFIX) {
+  } else if (pre) {
     sn.total = R.base >> 5;
-    per = split_into(sn.total, A.pre_per, A.pre_splits);
+    per = pre_per;
   } else {
-    const int shared = shared_of(A, i);
     if (h == 0 && tile == 0 && sp == 0 && threadIdx.x == 0) A.shared[i] = shared;
     sn.lo = shared >> 5;
     sn.total = max((p1 >> 5) + 1 - sn.lo, 0);
@@ -621,9 +724,10 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
   }
   const int window = MODE == SPAN ? A.window : 0, sink = MODE == SPAN ? A.sink : 0;
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
-  if (c0 >= c1 && (sp > 0 || MODE == PREFIX)) return;
+  if (c0 >= c1 && (sp > 0 || pre)) return;
   // one part: its result is the output's
-  const bool whole = MODE != PREFIX && sn.total <= per && (MODE != SUFFIX || sn.lo == 0);
+  const bool whole = !pre && sn.total <= per && (MODE != SUFFIX || sn.lo == 0);
+  if constexpr (MODE == SUFFIX) sp += pre ? 0 : A.slot0;  // (a prefix' parts come first in the workspace)
 
   const int32_t* tab = A.table + (int64_t)i * A.cols;
   const int blk_shift = 31 - __builtin_clz(A.T) - 5;    // chunks of a block, as a power of two
@@ -708,7 +812,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
   // two waves: 147 -> 162 us and 73 -> 77 for the long and the ragged batch).
   while (k < c1) {
     const int t0 = MODE == LIST ? at.t : chunk_at(k) * 32, t1 = t0 + 31;
-    const bool dead = at.dead, full = !dead && (MODE == PREFIX || t1 <= p0) && (window == 0 || t0 > p1 - window || t1 < sink);
+    const bool dead = at.dead, full = !dead && t1 <= p0 && (window == 0 || t0 > p1 - window || t1 < sink);
     k += NWV;
     f32x4 s[NT][2];
     key_products<D, NT>(C, q, s);
@@ -758,6 +862,37 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
     }
     value_products<D, NT>(C, full, P, o);
     values(at);
+  }
+  if constexpr (NWV == 1) {                            // a wave on its own: a lane holds channels (D/16)(4G + i) .. in tiles 0 ..
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const float L = sum_quads(l[nt]);
+      if (grow[nt] < 0) continue;
+      const int ch0 = NC * 4 * G;
+      if (whole) {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int64_t t = R.first + quot(row0 + 16 * nt + n, A.by_group);
+        uint16_t* out = (uint16_t*)A.o + t * A.os + (grow[nt] - t * A.hq) * D + ch0;
+#pragma unroll
+        for (int i4 = 0; i4 < 4; i4++) {
+          uint32_t y[NC / 2];
+#pragma unroll
+          for (int c = 0; c < NC / 2; c++) y[c] = pack2<TYPE>(o[nt][2 * c][i4] * inv, o[nt][2 * c + 1][i4] * inv);
+          if constexpr (NC == 8) *(u32x4*)(out + NC * i4) = (u32x4){y[0], y[1], y[2], y[3]};
+          else *(u32x2*)(out + NC * i4) = (u32x2){y[0], y[1]};
+        }
+      } else {
+        const int64_t row = (int64_t)sp * A.n_tok * A.hq + grow[nt];
+        if (G == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){ref[nt].m == NEG_INF ? NEG_INF : __builtin_fmaf(ref[nt].m, cf[nt], -LIFT), L};
+        float* out = A.po + row * D + ch0;
+#pragma unroll
+        for (int i4 = 0; i4 < 4; i4++)
+#pragma unroll
+          for (int c = 0; c < NC / 4; c++)
+            *(f32x4*)(out + NC * i4 + 4 * c) = (f32x4){o[nt][4 * c][i4], o[nt][4 * c + 1][i4], o[nt][4 * c + 2][i4], o[nt][4 * c + 3][i4]};
+      }
+    }
+    return;
   }
   // Join the waves through LDS, each of them a share of the channels: the
   // waves' sums are rescaled to the row's largest product where they are read.
@@ -811,7 +946,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
         else out[NC * i4] = (uint16_t)pack2<TYPE>(x[0][i4] * inv, 0.0f);
       }
     } else {
-      const int64_t row = (int64_t)slot_of<MODE>(A, sp) * A.n_tok * A.hq + grow[nt];
+      const int64_t row = (int64_t)sp * A.n_tok * A.hq + grow[nt];
       // (parts of a shared prefix may come from k_attend_tiles, whose sums count from the reference's lift)
       const float at_m = MODE == SPAN ? M * cf[nt] : M == NEG_INF ? NEG_INF : __builtin_fmaf(M, cf[nt], -LIFT);
       if (G == 0 && wave == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){at_m, L};
@@ -923,24 +1058,27 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
   // multiple of 8
   int b = blockIdx.x;
   const int h = b % A.hkv; b /= A.hkv;
-  int most = A.splits;
-  if constexpr (MODE == PREFIX) most = A.pre_splits;
-  const int sp = b % most;
-  int i, row0;
+  int sp = MODE == PREFIX ? 0 : b % A.splits;
+  int i, row0, shared = 0, pre_per = 0;
   Req R;
   if constexpr (MODE == PREFIX) {
-    int g;
-    if (!group_tile(A, ROWS, b / most, &g, &row0)) return;
-    row0 *= ROWS;
-    const Group r = group_at(A, g);
-    int last;
-    group_tokens(A, r.s, r.e, &R.first, &last);
-    R.n_new = last - R.first;
-    R.base = r.len;                                      // (no row lies before what is shared)
-    i = r.s;                                             // by the table of the first
+    const Whole whole_batch(A);
+    Whole::Part part;
+    const bool on = whole_batch.part(ROWS, b, &part);
+    if (blockIdx.x == 0 && tid == 0) A.shared[A.n_req] = part.per;
+    if (!on) return;
+    const Members m = whole_batch.group(part.g);
+    row0 = part.tile * ROWS;
+    sp = part.sp;
+    pre_per = part.per;
+    R.first = m.first;
+    R.n_new = m.last - m.first;
+    R.base = m.len;                                      // (no row lies before what is shared)
+    i = m.s;                                             // by the table of the first
   } else {
     if (!tile_of(A, ROWS, b / A.splits, &i, &row0)) return;
     R = req_args(A, i);
+    if constexpr (MODE == SUFFIX) shared = Whole(A).shared_of(i);
   }
   const int rows = (MODE == PREFIX ? R.n_new : min(R.n_new, A.max_new)) * A.group;
   if (row0 < 0 || row0 >= rows) return;
@@ -952,9 +1090,8 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
     per = split_chunks(A, sn.total);
   } else if constexpr (MODE == PREFIX) {
     sn.total = R.base >> 5;
-    per = split_into(sn.total, A.pre_per, A.pre_splits);
+    per = pre_per;
   } else {
-    const int shared = shared_of(A, i);
     if (h == 0 && row0 == 0 && sp == 0 && tid == 0) A.shared[i] = shared;
     sn.lo = shared >> 5;
     sn.total = max((p1 >> 5) + 1 - sn.lo, 0);
@@ -964,6 +1101,7 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
   const int c0 = sp * per, c1 = min(c0 + per, sn.total);
   if (c0 >= c1 && (sp > 0 || MODE == PREFIX)) return;
   const int parts = MODE == PREFIX || (MODE == SUFFIX && sn.lo > 0) ? 2 : (sn.total + per - 1) / per;
+  if constexpr (MODE == SUFFIX) sp += A.slot0;          // (a prefix' parts come first in the workspace)
 
   // the wave's rows
   const bool on = row0 + 32 * wave + n < rows;         // rows past the last compute the last one again and are not written
@@ -972,7 +1110,7 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
   const int pw0 = min(R.base + (row0 + 32 * wave) / A.group, pw1), pos = R.base + j;
   f16x8 q[KSTEP];
   float cf;
-  {
+  auto queries = [&] {
     float x[D / 2];
     const int64_t at = (int64_t)(R.first + j) * A.qs + (int64_t)(h * A.group + g) * D + 8 * G;
 #pragma unroll
@@ -988,7 +1126,8 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
 #pragma unroll
       for (int u = 0; u < 8; u++) q[s][u] = (f16)(sign * __builtin_ldexpf(x[8 * s + u], e));
     cf = q_factor(A.scale, e);
-  }
+  };
+  if (MODE == SPAN) queries();
   f32x16 o[NC];
 #pragma unroll
   for (int c = 0; c < NC; c++)
@@ -1159,10 +1298,12 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
         }
     __builtin_amdgcn_s_setprio(0);
   };
+  if (MODE != SPAN && c0 >= c1) cf = 0.0f;
   if (c0 < c1) {
     Tile t0 = locate(c0), t1 = locate(c0 + 2), t2 = locate(c0 + 4);
     fetch_k(t0);
     fetch_v(t0);
+    if (MODE != SPAN) queries();                        // (short parts: their loads on the way together)
     put_k(0);
     put_v(0);
     fetch_k(t1);
@@ -1204,7 +1345,7 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
         *(u32x2*)(out + 32 * c + 8 * a) = (u32x2){pack2<TYPE>(o[c][4 * a] * inv, o[c][4 * a + 1] * inv),
                                                   pack2<TYPE>(o[c][4 * a + 2] * inv, o[c][4 * a + 3] * inv)};
   } else {
-    const int64_t row = (int64_t)slot_of<MODE>(A, sp) * A.n_tok * A.hq + (int64_t)(R.first + j) * A.hq + h * A.group + g;
+    const int64_t row = (int64_t)sp * A.n_tok * A.hq + (int64_t)(R.first + j) * A.hq + h * A.group + g;
     if (G == 0) {
       A.pml[2 * row] = ref.m == NEG_INF ? NEG_INF : ref.mc;
       A.pml[2 * row + 1] = L;
@@ -1248,10 +1389,10 @@ __global__ void __launch_bounds__(256) k_attend_join(ArgsOf<MODE> A, int tile_sh
   if (sn.total <= per && (MODE != SUFFIX || sn.lo == 0)) return;   // written by its only part
   int parts = per == A.per ? quot(sn.total + per - 1, A.by_per) : (sn.total + per - 1) / per, shared_parts = 0, gap = 0;
   if constexpr (MODE == SUFFIX) {
-    const int pre = split_into(sn.lo, A.pre_per, A.pre_splits);
+    const int pre = sn.lo > 0 ? ld_const(A.shared + A.n_req) : 1;
     shared_parts = (sn.lo + pre - 1) / pre;
     parts += shared_parts;
-    gap = A.pre_splits - shared_parts;
+    gap = A.slot0 - shared_parts;
   }
   auto at = [&](int s) { return MODE == SUFFIX && s >= shared_parts ? s + gap : s; };
   const int64_t stride = (int64_t)A.n_tok * A.hq, row = (int64_t)(R.first + j) * A.hq + hd;
@@ -1364,12 +1505,12 @@ constexpr int STAGED_ROWS = 64;
 // caches; 8 requests of 32,768 to 131,072 tokens: 156 us at four, 153 at six, 146
 // at eight, 150 at ten, 152 at sixteen).
 constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
-void cut(Split* x, int64_t base, int64_t chunks) {
+void cut(Split* x, int64_t base, int64_t chunks, int64_t few_chunks = FEW_CHUNKS) {
   Split& s = *x;
   auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
   int64_t k = 1;
   if (base > 0) {
-    const int64_t few = least(FEW_GROUPS / base, chunks / FEW_CHUNKS), many = least(MANY_GROUPS / base, chunks / MANY_CHUNKS);
+    const int64_t few = least(FEW_GROUPS / base, chunks / few_chunks), many = least(MANY_GROUPS / base, chunks / MANY_CHUNKS);
     k = least(few > many ? few : many, MOST_SPLITS);
     if (k < 1) k = 1;
   }

@@ -88,26 +88,37 @@ __global__ void __launch_bounds__(256) k_kv_bounds(BoundsArgs A) {
   const int cg = (lane >> 2) & (D / 32 - 1);
   const int tok = (lane & 3) | (D == 128 ? (lane >> 4) << 2 : (lane >> 3) << 2);
   f16x2 lo[16], hi[16];
+#pragma unroll
+  for (int x = 0; x < 16; x++) {
+    lo[x] = as_h2(0x7C007C00u);
+    hi[x] = as_h2(0xFC00FC00u);
+  }
   uint32_t worst = 0;
-  auto pass = [&](int t, bool first) {
-    t = min(t + tok, last);
-    const u32x4 w = *(const u32x4*)(page + t * (D / 2) + 16 * cg);
-    const uint32_t sb = page[T * D + cg * T + t];
-    worst = max(worst, sb);
-    const float sc = bits_f(sb << 23);
+  constexpr int U = 4;                                 // passes under way at once
+  for (int t0 = 0; t0 <= last; t0 += U * PASS) {
+    u32x4 w[U];
+    uint32_t sb[U];
 #pragma unroll
-    for (int x = 0; x < 4; x++) {
-      const uint32_t p[4] = {cvt2<0>(w[x], sc), cvt2<1>(w[x], sc), cvt2<2>(w[x], sc), cvt2<3>(w[x], sc)};
+    for (int u = 0; u < U; u++) {
+      const int t = min(t0 + u * PASS + tok, last);
+      w[u] = *(const u32x4*)(page + t * (D / 2) + 16 * cg);
+      sb[u] = page[T * D + cg * T + t];
+    }
 #pragma unroll
-      for (int y = 0; y < 4; y++) {
-        const f16x2 v = as_h2(p[y]);
-        lo[4 * x + y] = first ? v : min2(lo[4 * x + y], v);
-        hi[4 * x + y] = first ? v : max2(hi[4 * x + y], v);
+    for (int u = 0; u < U; u++) {
+      worst = max(worst, sb[u]);
+      const float sc = bits_f(sb[u] << 23);
+#pragma unroll
+      for (int x = 0; x < 4; x++) {
+        const uint32_t p[4] = {cvt2<0>(w[u][x], sc), cvt2<1>(w[u][x], sc), cvt2<2>(w[u][x], sc), cvt2<3>(w[u][x], sc)};
+#pragma unroll
+        for (int y = 0; y < 4; y++) {
+          lo[4 * x + y] = min2(lo[4 * x + y], as_h2(p[y]));
+          hi[4 * x + y] = max2(hi[4 * x + y], as_h2(p[y]));
+        }
       }
     }
-  };
-  pass(0, true);
-  for (int t = PASS; t <= last; t += PASS) pass(t, false);
+  }
   halve32<false, 16>(lo);
   halve32<true, 16>(hi);
   halve16<false, 8>(lo);
@@ -152,9 +163,62 @@ __device__ __forceinline__ void widen(u32x4 w, f16x8* f) {
     f[y] = frag(up2(w[2 * y], 0x010C000Cu), up2(w[2 * y], 0x030C020Cu), up2(w[2 * y + 1], 0x010C000Cu), up2(w[2 * y + 1], 0x030C020Cu));
 }
 
-template <int D, int TYPE, int NT>
+// A lane's channels of N query rows, as they lie in memory (16 bytes: eight channels).
+template <int D, int N> struct Raw { u32x4 w[N][D / 32]; };
+template <int D, int N>
+__device__ __forceinline__ void load_raw(const ScoreArgs& A, int64_t at, Raw<D, N>& x, int n) {
+  const uint16_t* p = (const uint16_t*)A.q + at;
+#pragma unroll
+  for (int y = 0; y < D / 64; y++) {
+    x.w[n][2 * y] = *(const u32x4*)(p + 64 * y);
+    x.w[n][2 * y + 1] = *(const u32x4*)(p + 64 * y + 8);
+  }
+}
+// Their positive and negative parts as operands.  binary16 queries go in as they
+// are; bfloat16 ones times a power of two that brings the rows' largest magnitude
+// to [2^14, 2^15) (times 2^127 at most: smaller ones are exact in binary16's
+// subnormals then): exact down to 2^-29 of it.  *ex: the power of two that the
+// products are to be multiplied with, beside the scale's mantissa.
+template <int D, int TYPE, int N>
+__device__ __forceinline__ void signed_parts(const ScoreArgs& A, const Raw<D, N>& x, f16x8 (*qp)[D / 32], f16x8 (*qn)[D / 32], int* ex) {
+  float by = 1.0f;
+  *ex = __builtin_amdgcn_frexp_expf(A.scale);
+  if constexpr (TYPE == STQ_BF16) {
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int n = 0; n < N; n++)
+#pragma unroll
+      for (int i = 0; i < D / 32; i++)
+#pragma unroll
+        for (int u = 0; u < 4; u++) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x.w[n][i][u] & 0x7FFF7FFFu));
+    const int e = min(q_shift(max_quads(bits_f((uint32_t)max(m[0], m[1]) << 16))), 127);
+    by = __builtin_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, e);
+    *ex -= e;
+  }
+  const uint32_t turned = A.scale < 0.0f ? 0x80008000u : 0u;
+  const f16x2 zero = {(f16)0.0f, (f16)0.0f};
+#pragma unroll
+  for (int n = 0; n < N; n++)
+#pragma unroll
+    for (int i = 0; i < D / 32; i++) {
+      uint32_t p[4], q[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const uint32_t w = x.w[n][i][u];
+        f16x2 v;
+        if constexpr (TYPE == STQ_BF16) v = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(bits_f(w << 16) * by, bits_f(w & 0xFFFF0000u) * by));
+        else v = as_h2(w ^ turned);
+        p[u] = h2_bits(max2(v, zero));
+        q[u] = h2_bits(min2(v, zero));
+      }
+      qp[n][i] = frag(p[0], p[1], p[2], p[3]);
+      qn[n][i] = frag(q[0], q[1], q[2], q[3]);
+    }
+}
+
+template <int D, int TYPE>
 __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
-  constexpr int LD = D / 64;                           // 16-byte loads of one bound
+  constexpr int LD = D / 64, NT = 1;                   // 16-byte loads of one bound
   const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int i = quot(blockIdx.x, A.by_hkv), h = blockIdx.x - i * A.hkv;
@@ -192,25 +256,10 @@ __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
           const int j = tok0 + nt * TOK + (n >> rs), jj = min(j, fresh - 1);
           const int g = min(hc + (n & ((1 << rs) - 1)), A.group - 1);
           const int64_t at = (int64_t)(R.first + jj) * A.qs + (int64_t)(h * A.group + g) * D + 16 * G;
-          float x[D / 4];
-#pragma unroll
-          for (int y = 0; y < LD; y++) {
-            load8<TYPE>(A.q, at + 64 * y, x + 16 * y);
-            load8<TYPE>(A.q, at + 64 * y + 8, x + 16 * y + 8);
-          }
-          float m = 0.0f;
-#pragma unroll
-          for (int u = 0; u < D / 4; u++) m = __builtin_fmaxf(m, __builtin_fabsf(x[u]));
-          const int e = q_shift(max_quads(m));
-          const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
-#pragma unroll
-          for (int u = 0; u < D / 4; u++) {
-            const f16 v = (f16)(sign * __builtin_ldexpf(x[u], e));
-            qp[nt][u >> 3][u & 7] = v > (f16)0 || v != v ? v : (f16)0;
-            qn[nt][u >> 3][u & 7] = v < (f16)0 || v != v ? v : (f16)0;
-          }
+          Raw<D, 1> x;
+          load_raw<D>(A, at, x, 0);
+          signed_parts<D, TYPE, 1>(A, x, &qp[nt], &qn[nt], &ex[nt]);
           mul[nt] = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(A.scale));
-          ex[nt] = __builtin_amdgcn_frexp_expf(A.scale) - e;
           const int p = R.base + jj;
           top[nt] = j < fresh && (n & ((1 << rs) - 1)) == 0 ? min(p >> shift, A.cols - 1) : -1;
           to[nt] = ((int64_t)(R.first + jj) * A.hkv + h) * A.cols;
@@ -265,15 +314,152 @@ __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
   }
 }
 
+// Many tokens of a request: the products bound the work.  Columns of a product
+// are sixteen tokens, and HT products side by side are heads of the group, so that
+// the group's maximum is taken between a lane's own registers; a wave holds TT
+// such sets of tokens (HT TT products to each widened bound) and goes over the
+// blocks that they see.  One power of two scales all of a token's HT queries.
+template <int D, int TYPE, int HT, int TT>
+__global__ void __launch_bounds__(256, 2) k_kv_score_wide(ScoreArgs A) {
+  constexpr int LD = D / 64, NT = HT * TT;
+  const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int i = quot(blockIdx.x, A.by_hkv), h = blockIdx.x - i * A.hkv;
+  const Req R = req_args(A, i);
+  const int fresh = min(R.n_new, A.max_new), tok0 = (blockIdx.y * 4 + wave) * 16 * TT;
+  if (tok0 >= fresh) return;
+  const int shift = 31 - __builtin_clz(A.T);
+  const int p1 = R.base + min(tok0 + 16 * TT, fresh) - 1;
+  if (p1 < 0) return;
+  const int total = min((p1 >> shift) + 1, A.cols);     // blocks that the last of these tokens sees
+  const int32_t* tab = A.table + (int64_t)i * A.cols;
+  const int run = 16 * A.tile_run, step = gridDim.z * run;
+  struct Tile { u32x4 w[2 * LD]; bool dead; } tile[2];
+  __shared__ int entry[4][256];
+  // The table entries of 256 blocks of a run, in LDS of the wave's own: asked for
+  // tile by tile, each would wait for the scores stored before it.
+  int from = 0;
+  auto look = [&](int b) {
+    from = b;
+    int x[4];
+#pragma unroll
+    for (int y = 0; y < 4; y++) x[y] = tab[min(b + 64 * y + lane, total - 1)];
+#pragma unroll
+    for (int y = 0; y < 4; y++) entry[wave][64 * y + lane] = x[y];
+    lds_wave_fence();
+  };
+  auto load = [&](Tile& x, int b) {
+    if (b < from || b >= from + 256) look(b);
+    const int blk = entry[wave][b - from + n];
+    const bool dead = (uint32_t)blk >= (uint32_t)A.n_blocks;
+    const uint8_t* p = A.bounds + ((uint64_t)(uint32_t)(dead ? 0 : blk) * A.hkv + h) * (2 * D) + 16 * G;
+#pragma unroll
+    for (int y = 0; y < 2 * LD; y++) x.w[y] = *(const u32x4*)(p + 64 * y);
+    x.dead = dead;
+  };
+  int top[TT];                                         // the token's last block (-1: none)
+  int64_t to[TT];
+#pragma unroll
+  for (int tt = 0; tt < TT; tt++) {
+    const int j = tok0 + 16 * tt + n, p = R.base + j;
+    top[tt] = j < fresh && p >= 0 ? min(p >> shift, A.cols - 1) : -1;
+    to[tt] = ((int64_t)(R.first + min(j, fresh - 1)) * A.hkv + h) * A.cols + 4 * G;
+  }
+  for (int hc = 0; hc < A.group; hc += HT) {            // HT heads of the group at a time
+    int b = blockIdx.z * run, b1 = b;
+    if (b >= total) return;
+    auto behind = [&](int x) { return x + 16 < b1 + run ? x + 16 : (b1 += step); };   // (past `total`: the end)
+    int next = behind(b);
+    look(b);
+    load(tile[0], b);
+    if (next < total) load(tile[1], next);
+    f16x8 qp[NT][D / 32], qn[NT][D / 32];
+    int ex[TT];
+#pragma unroll
+    for (int tt = 0; tt < TT; tt++) {
+      const int jj = min(tok0 + 16 * tt + n, fresh - 1);
+      Raw<D, HT> x;
+#pragma unroll
+      for (int g = 0; g < HT; g++)
+        load_raw<D>(A, (int64_t)(R.first + jj) * A.qs + (int64_t)(h * A.group + min(hc + g, A.group - 1)) * D + 16 * G, x, g);
+      signed_parts<D, TYPE, HT>(A, x, &qp[tt * HT], &qn[tt * HT], &ex[tt]);
+    }
+    const float mul = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(A.scale));
+    // one tile of sixteen blocks; the bounds of the one behind the next are asked
+    // for before its scores are stored, since waits count both in order
+    auto work = [&](Tile& x, int b, int ahead) {
+      f32x4 s[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) s[nt] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int z = 0; z < 2 * LD; z++) {
+        f16x8 f[2];
+        widen(x.w[z], f);
+#pragma unroll
+        for (int y = 0; y < 2; y++)
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+            s[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[y], z < LD ? qn[nt][2 * z + y] : qp[nt][2 * (z - LD) + y], s[nt], 0, 0, 0);
+      }
+      const uint32_t gone = ((uint32_t)__builtin_amdgcn_ballot_w64(x.dead) & 0xFFFFu) >> (4 * G);
+      if (ahead < total) load(x, ahead);
+#pragma unroll
+      for (int tt = 0; tt < TT; tt++) {
+        const int b4 = b + 4 * G;
+        f32x4 v;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          float y = s[tt * HT][u];
+#pragma unroll
+          for (int g = 1; g < HT; g++) y = __builtin_fmaxf(y, s[tt * HT + g][u]);
+          v[u] = (gone >> u) & 1 ? NEG_INF : __builtin_ldexpf(y * mul, ex[tt]);
+        }
+        if (b4 > top[tt]) continue;
+        typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+        float* out = A.score + to[tt] + b;
+        if (hc > 0)                                    // what this lane has written for the heads before
+#pragma unroll
+          for (int u = 0; u < 4; u++)
+            if (b4 + u <= top[tt]) v[u] = __builtin_fmaxf(v[u], out[u]);
+        if (b4 + 3 <= top[tt]) {
+          *(f32x4_a4*)out = v;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; u++)
+            if (b4 + u <= top[tt]) out[u] = v[u];
+        }
+      }
+    };
+    while (true) {
+      int ahead = behind(next);
+      work(tile[0], b, ahead);
+      if (next >= total) break;
+      b = next;
+      next = ahead;
+      ahead = behind(next);
+      work(tile[1], b, ahead);
+      if (next >= total) break;
+      b = next;
+      next = ahead;
+    }
+  }
+}
+
 // --------------------------------------------------- selection of blocks
 //
-// The `want` largest of a row's scores beside the blocks that are always
-// taken, as a threshold on the scores' bits in the order of integers: bits
-// below those that all candidates share are settled from the top, each by one
-// count over the row (compare, ballot, population count), until a count meets
-// `want` exactly or the bits are used up; then equal ones are taken in order.
-// W waves a row, 64 W M blocks at most, M of them in a lane's registers: block
-// 64 (M wave + m) + lane.
+// The `want` largest of a row's scores beside the blocks that are always taken,
+// by a threshold on the scores' bits in the order of integers: the number of
+// keys above a trial threshold (compares, ballots and population counts, so that
+// the search itself runs on the scalar unit) says on which side to go on; trials
+// are interpolated between the counts at both ends (every fifth halves the
+// range), and from the fifth on the end that moves goes to the next key.  A count
+// that meets `want` ends it, or a range of one key, whose equal ones are taken in
+// order: 6 to 8 trials for rows of 230 to 2,000 scores, equal ones among them,
+// where one bit a trial takes 15 to 18.  The places of the taken blocks are
+// population counts of the ballots below, so the list is ascending and the same
+// whatever the split.
+//
+// W waves a row, each with M blocks a lane: block 64 (M wave + m) + lane.
 struct SelectArgs {
   const float* score;
   const int32_t *tok_start, *len;
@@ -282,125 +468,147 @@ struct SelectArgs {
   Div by_hkv, by_max_new;
 };
 
-template <int W>
-struct Rendezvous {                                     // sums over a row's waves
-  int (*s)[W];
-  int turn = 0;
-  __device__ __forceinline__ explicit Rendezvous(int (*x)[W]) : s(x) {}
-  // of one number a wave: the sum, and the sum of the waves before this one
-  __device__ __forceinline__ int sum(int x, int* before) {
-    if constexpr (W == 1) {
-      *before = 0;
-      return x;
-    } else {
-      const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-      if (lane == 0) s[turn][wave] = x;
-      __syncthreads();
-      const int y = lane < W ? s[turn][lane] : 0;
-      turn ^= 1;
-      *before = wave_sum_i(lane < wave ? y : 0);
-      return wave_sum_i(y);
-    }
-  }
-};
-
 template <int W, int M>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) k_kv_select(SelectArgs A) {
-  __shared__ int shared[W == 1 ? 1 : 2][W];
-  Rendezvous<W> all(shared);
+  __shared__ uint32_t meet_at[2][W];
+  int turn = 0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const uint32_t row = W == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
   const int w = W == 1 ? 0 : wave;
+  // one number a wave -> f over the row's waves; `before`: over those ahead of this one
+  auto all_waves = [&](uint32_t x, auto f, uint32_t none, uint32_t* before) {
+    if constexpr (W == 1) {
+      *before = none;
+      return x;
+    } else {
+      if (lane == 0) meet_at[turn][wave] = x;
+      __syncthreads();
+      uint32_t y = none, z = none;
+#pragma unroll
+      for (int v = 0; v < W; v++) {
+        const uint32_t u = meet_at[turn][v];
+        if (v < wave) z = f(z, u);
+        y = f(y, u);
+      }
+      turn ^= 1;
+      *before = __builtin_amdgcn_readfirstlane(z);
+      return (uint32_t)__builtin_amdgcn_readfirstlane(y);
+    }
+  };
+  auto plus = [](uint32_t a, uint32_t b) { return a + b; };
+  auto top = [](uint32_t a, uint32_t b) { return max(a, b); };
+  auto wave_top = [](uint32_t x) { return (uint32_t)wave_max_i((int)(x ^ 0x80000000u)) ^ 0x80000000u; };
+  uint32_t before;
+
+  const uint32_t row = W == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
   const int x = quot(row, A.by_hkv), h = row - x * A.hkv;
   const int i = quot(x, A.by_max_new), j = x - i * A.max_new;
   if (i >= A.n_req) return;
   const int start = max(ld_const(A.tok_start + i), 0), end = max(ld_const(A.tok_start + i + 1), start);
   const int shift = 31 - __builtin_clz(A.T);
-  if (j >= min(min(end, A.n_tok) - start, A.max_new)) return;
   const int len = (int)min((int64_t)max(ld_const(A.len + i), 0), (int64_t)A.cols << shift);
+  if (j >= min(min(end, A.n_tok) - start, A.max_new)) return;
   const int p = max(len - (end - start), -(1 << 28)) + j;
-  const int nb = p < 0 ? 0 : min((p >> shift) + 1, A.cols);
+  const int nb = p < 0 ? 0 : min((p >> shift) + 1, A.cols);         // blocks that the token sees
   const int64_t at = (int64_t)(start + j) * A.hkv + h;
   const float* in = A.score + at * A.cols;
   int32_t* out = A.sel + at * A.n_sel;
-  const int last0 = max(nb - A.n_last, 0);              // blocks below n_first and from last0 on are taken
-  const int must = min(nb, A.n_first) + nb - max(last0, min(nb, A.n_first));
+  const int last0 = max(nb - A.n_last, 0), first1 = min(nb, A.n_first);    // blocks below first1 and from last0 on are taken
+  const int must = first1 + nb - max(last0, first1);
   const int want = min(A.n_sel, nb) - must;
   // Keys in the order of integers: 0 for what is no candidate (taken already, not
   // seen, -inf), the largest for NaN; -0 counts as 0.
   uint32_t key[M];
-  uint32_t big = 0, small = 0xFFFFFFFFu;
   const int b0 = 64 * M * w + lane;
+#pragma unroll
+  for (int m = 0; m < M; m++) key[m] = __float_as_uint(in[max(min(b0 + 64 * m, nb - 1), 0)]);
+  uint32_t big = 0, small = 0;
 #pragma unroll
   for (int m = 0; m < M; m++) {
     const int b = b0 + 64 * m;
-    uint32_t u = b < nb ? __float_as_uint(in[b]) : 0xFF800000u;
-    const bool nan = (u & 0x7FFFFFFFu) > 0x7F800000u, none = u == 0xFF800000u || b < A.n_first || b >= last0;
+    uint32_t u = key[m];
+    const bool nan = (u & 0x7FFFFFFFu) > 0x7F800000u, none = u == 0xFF800000u || b < first1 || b >= last0;
     if (u == 0x80000000u) u = 0;
     u = (int)u < 0 ? ~u : u | 0x80000000u;
     key[m] = none ? 0u : nan ? 0xFFFFFFFFu : u;
     big = max(big, key[m]);
-    small = min(small, none ? 0xFFFFFFFFu : key[m]);
+    small = max(small, 0u - key[m]);                    // (the least but 0, turned over)
   }
-  auto count = [&](uint32_t t, int* before) {           // candidates at t or above
-    int c = 0;
+  auto above = [&](uint32_t t) {
+    uint32_t c = 0;
 #pragma unroll
-    for (int m = 0; m < M; m++) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[m] >= t));
-    return all.sum(c, before);
+    for (int m = 0; m < M; m++) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[m] > t));
+    return (int)all_waves(c, plus, 0u, &before);
   };
-  int before;
-  uint32_t t = want > 0 ? 1u : 0xFFFFFFFFu;             // all candidates, or none
-  const int have = count(1u, &before);
-  int ties = 0x7FFFFFFF;                                // of the equal ones at t: how many are taken
-  if (want <= 0) ties = 0;
-  else if (have > want) {
-    // range of the keys over the row
-    uint32_t hi = (uint32_t)wave_max_i((int)(big ^ 0x80000000u)) ^ 0x80000000u;
-    uint32_t lo = ~((uint32_t)wave_max_i((int)(~small ^ 0x80000000u)) ^ 0x80000000u);
-    if constexpr (W > 1) {
-      __shared__ uint32_t range[2][W];
-      if (lane == 0) { range[0][wave] = hi; range[1][wave] = lo; }
-      __syncthreads();
+  // count(key > lo) > want > count(key > hi); t and need: what the search ends with
+  int flo = above(0), fhi = 0, need = 0;
+  uint32_t t = want > 0 ? 0u : 0xFFFFFFFFu;
+  if (want > 0 && flo > want) {
+    uint32_t hi = all_waves(wave_top(big), top, 0u, &before);
+    uint32_t lo = 0u - all_waves(wave_top(small), top, 0u, &before) - 1;
+    for (int trial = 0;; trial++) {
+      const uint32_t width = hi - lo;
+      if (width == 1) {
+        t = hi;
+        need = want - fhi;
+        break;
+      }
+      uint32_t off = width >> 1;                        // (a float's 24 bits of the range: any trial between the ends will do)
+      if (trial % 5 != 4) off = (uint32_t)((float)width * ((float)(flo - want) * __builtin_amdgcn_rcpf((float)(flo - fhi))));
+      const uint32_t mid = __builtin_amdgcn_readfirstlane(lo + min(max(off, 1u), width - 1));
+      const int f = above(mid);
+      if (f == want) {
+        t = mid;
+        break;
+      }
+      uint32_t to = mid;
+      if (trial >= 4) {                                 // the next key that there is: equal keys end the search then
+        const uint32_t turned = f > want ? 0xFFFFFFFFu : 0u, most = f > want ? ~mid - 1 : mid;
+        uint32_t y = 0;
 #pragma unroll
-      for (int y = 0; y < W; y++) { hi = max(hi, range[0][y]); lo = min(lo, range[1][y]); }
+        for (int m = 0; m < M; m++) {
+          const uint32_t k = key[m] ^ turned;
+          y = max(y, k <= most ? k : 0u);
+        }
+        y = all_waves(wave_top(y), top, 0u, &before);
+        to = f > want ? ~y - 1 : y;
+      }
+      if (f > want) {
+        lo = to;
+        flo = f;
+      } else {
+        hi = to;
+        fhi = f;
+      }
     }
-    int bit = hi == lo ? -1 : 31 - __builtin_clz(hi ^ lo);
-    t = bit < 0 ? hi : bit == 31 ? 0u : (hi >> (bit + 1)) << (bit + 1);
-    for (; bit >= 0; bit--) {
-      const uint32_t c = t | (1u << bit);
-      const int y = count(c, &before);
-      if (y < want) continue;
-      t = c;
-      if (y == want) break;
-    }
-    if (bit < 0) ties = want - (t == 0xFFFFFFFFu ? 0 : count(t + 1, &before));
   }
-  // equal ones before this wave's, then the places of what is taken
-  int equal = 0;
-#pragma unroll
-  for (int m = 0; m < M; m++) equal += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[m] == t));
-  int seen = 0;
-  if (ties != 0x7FFFFFFF) all.sum(equal, &seen);
-  const uint64_t below = (1ull << lane) - 1;
+  // Of the equal ones the first `need`, then the places of what is taken.
+  const auto low = [&](uint64_t mask) { return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0)); };
   uint64_t take[M];
-  int mine = 0;
+  int seen = 0, mine = 0;
+  if (need > 0) {                                       // equal ones in the waves ahead
+    uint32_t c = 0;
+#pragma unroll
+    for (int m = 0; m < M; m++) c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[m] == t));
+    all_waves(c, plus, 0u, &before);
+    seen = (int)before;
+  }
 #pragma unroll
   for (int m = 0; m < M; m++) {
     const int b = b0 + 64 * m;
-    const uint64_t same = __builtin_amdgcn_ballot_w64(key[m] == t);
-    bool on = key[m] > t || (key[m] == t && (ties == 0x7FFFFFFF || seen + __builtin_popcountll(same & below) < ties));
-    on = on && key[m] != 0;
-    if (want <= 0) on = false;
-    on = on || (b < nb && (b < A.n_first || b >= last0));
-    seen += __builtin_popcountll(same);
+    bool on = key[m] > t || (b < nb && (b < first1 || b >= last0));
+    if (need > 0) {
+      const uint64_t same = __builtin_amdgcn_ballot_w64(key[m] == t);
+      on = on || (key[m] == t && seen + low(same) < need);
+      seen += __builtin_popcountll(same);
+    }
     take[m] = __builtin_amdgcn_ballot_w64(on);
     mine += __builtin_popcountll(take[m]);
   }
-  int pos;
-  const int total = all.sum(mine, &pos);
+  const int total = (int)all_waves((uint32_t)mine, plus, 0u, &before);
+  int pos = (int)before;
 #pragma unroll
   for (int m = 0; m < M; m++) {
-    if ((take[m] >> lane) & 1) out[pos + __builtin_popcountll(take[m] & below)] = b0 + 64 * m;
+    if ((take[m] >> lane) & 1) out[pos + low(take[m])] = b0 + 64 * m;
     pos += __builtin_popcountll(take[m]);
   }
   for (int y = total + 64 * w + lane; y < A.n_sel; y += 64 * W) out[y] = -1;
@@ -426,50 +634,64 @@ void fill(AttnArgs& A, const stq_kv_desc* d, const void* cache, const stq_attend
   A.scale = a->scale;
 }
 
-// Work of the blocks' attention: by what a whole list holds.
+// Work of the blocks' attention: by what a whole list holds.  Few workgroups are
+// split into parts of 8 chunks (one request, 32 blocks of 64 tokens, 8 heads: 9.8 us
+// on the GPU, 11 in parts of 12 and more, 10.3 of 4).  From 2,048 (token, head) pairs
+// on each has one wave, which needs no join through LDS and starts once instead
+// of four times: 16 blocks of 64 tokens at d = 128, prompts of 256 tokens 39.3 us by
+// four waves, 38.4 by one; 512 73.3, 65.8; 1,024 142, 122 (64 blocks 472, 460; 4
+// blocks 62, 39); 256 requests of one token 57.8, 55.4; but 128 tokens 21.8, 26.0.
+constexpr int64_t FEW_LISTED = 8;
 Split blocks_split(const stq_kv_desc* d, const stq_attend_desc* a, int n_sel) {
   Split s;
   const int64_t rows = a->n_heads / d->n_kv_heads;
   s.staged = s.once = false;
   s.tile_rows = rows > 16 ? 32 : 16;
   s.tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
-  cut(&s, (int64_t)a->n_req * a->max_new * d->n_kv_heads * s.tiles, (int64_t)n_sel * d->block_tokens / 32);
+  const int64_t base = (int64_t)a->n_req * a->max_new * d->n_kv_heads * s.tiles;
+  cut(&s, base, (int64_t)n_sel * d->block_tokens / 32, FEW_LISTED);
+  if (s.tile_rows == 16 && base >= MANY_GROUPS) s.waves = 1;
   return s;
 }
 
-// Parts of the shared prefixes and of the requests' own tokens.
-struct Shares { Split own, pre; int64_t pre_units; };
-constexpr int64_t MOST_PARTS = 64;                     // of each kind: the join holds 128 parts' statistics in its lanes
+// Parts of the requests' own tokens, and room for those of the shared prefixes:
+// sized on the device by what the groups have to do (Whole::part), from `per`
+// chunks up and at most `slots` of them.
+struct Shares { Split own; bool staged; int tile_rows, slots, per; int64_t pre_units; };
+constexpr int64_t MOST_PARTS = 64, PRE_GROUPS = 512;   // (the join holds 128 parts' statistics in its lanes)
 Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_shared_desc* g) {
   Shares s;
   const int64_t group = a->n_heads / d->n_kv_heads, rows = (int64_t)a->max_new * group;
-  s.own.once = s.pre.once = false;
+  s.own.once = false;
   s.own.staged = rows > STAGED_ROWS;
   s.own.tile_rows = s.own.staged ? 32 * TILE_WAVES : rows > 16 ? 32 : 16;
   s.own.tiles = (int)((rows + s.own.tile_rows - 1) / s.own.tile_rows);
   cut(&s.own, (int64_t)a->n_req * d->n_kv_heads * s.own.tiles, ((int64_t)a->max_len + 31) / 32);
-  const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
-  const int64_t mean = g->n_groups > 0 ? all / g->n_groups : 0;
-  s.pre.staged = mean > STAGED_ROWS;
-  s.pre.tile_rows = s.pre.staged ? 32 * TILE_WAVES : mean > 16 ? 32 : 16;
-  s.pre_units = (all + s.pre.tile_rows - 1) / s.pre.tile_rows + g->n_groups;
-  s.pre.tiles = 1;
-  cut(&s.pre, ((all + s.pre.tile_rows - 1) / s.pre.tile_rows) * d->n_kv_heads, (int64_t)g->max_prefix / 32 + 1);
-  for (Split* x : {&s.own, &s.pre})
-    if (x->splits > MOST_PARTS) {
-      const int64_t chunks = (int64_t)x->per * x->splits;
-      x->per = (int)(((chunks + MOST_PARTS - 1) / MOST_PARTS + 3) & ~3ll);
-      x->splits = (int)((chunks + x->per - 1) / x->per);
-    }
-  if (s.pre.waves == 16) s.pre.waves = 4;
+  if (s.own.splits > MOST_PARTS) {
+    const int64_t chunks = (int64_t)s.own.per * s.own.splits;
+    s.own.per = (int)(((chunks + MOST_PARTS - 1) / MOST_PARTS + 3) & ~3ll);
+    s.own.splits = (int)((chunks + s.own.per - 1) / s.own.per);
+  }
   if (s.own.waves == 16) s.own.waves = 4;
+  const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
+  s.staged = g->n_groups > 0 && (s.own.staged || all / g->n_groups > STAGED_ROWS);
+  s.tile_rows = s.staged ? 32 * TILE_WAVES : s.own.tile_rows;
+  const int64_t tiles = (all + s.tile_rows - 1) / s.tile_rows, fill = (PRE_GROUPS + d->n_kv_heads - 1) / d->n_kv_heads;
+  s.pre_units = g->n_groups > 0 ? fill + tiles + g->n_groups : 0;
+  s.per = 12;
+  const int64_t chunks = (int64_t)g->max_prefix / 32 + 1;
+  int64_t slots = 2 * fill / (tiles > 0 ? tiles : 1) + 1;
+  if (slots > (chunks + s.per - 1) / s.per) slots = (chunks + s.per - 1) / s.per;
+  const int64_t room = s.own.splits < 32 ? 32 - s.own.splits : MOST_PARTS;       // (the join asks for 32 parts at once)
+  s.slots = (int)(slots > room ? room : slots);
   return s;
 }
 
 template <int D, int TYPE>
 void launch_blocks(const LongArgs& A, const Split& s, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)A.n_req * A.max_new * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
-  if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, LIST>), grid, dim3(256), 0, st, A);
+  if (s.waves == 1) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 1, false, LIST>), grid, dim3(64), 0, st, A);
+  else if (s.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, LIST>), grid, dim3(256), 0, st, A);
   else if (s.waves == 16) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 16, false, LIST>), grid, dim3(1024), 0, st, A);
   else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, false, LIST>), grid, dim3(256), 0, st, A);
   if (A.splits > 1) {
@@ -479,22 +701,14 @@ void launch_blocks(const LongArgs& A, const Split& s, hipStream_t st) {
 }
 
 template <int D, int TYPE>
-void launch_shared(const LongArgs& A, const Shares& s, hipStream_t st) {
-  if (A.n_groups > 0) {
-    const int64_t units = s.pre_units * A.hkv;
-    if (s.pre.staged) {
-      hipLaunchKernelGGL((k_attend_tiles<D, TYPE, PREFIX>), dim3((unsigned)(units * s.pre.splits)), dim3(64 * TILE_WAVES), 0, st, A);
-    } else {
-      const dim3 grid((unsigned)units, 1u, (unsigned)s.pre.splits);
-      if (s.pre.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, PREFIX>), grid, dim3(256), 0, st, A);
-      else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, false, PREFIX>), grid, dim3(256), 0, st, A);
-    }
-  }
+void launch_shared(LongArgs& A, const Shares& s, hipStream_t st) {
+  if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE, PREFIX>), dim3((unsigned)(s.pre_units * A.hkv)), dim3(64 * TILE_WAVES), 0, st, A);
   if (s.own.staged) {
     const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
     hipLaunchKernelGGL((k_attend_tiles<D, TYPE, SUFFIX>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
-  } else {
-    const dim3 grid((unsigned)(A.n_req * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
+  } else {                                              // and prefixes of few rows, in one launch
+    A.pre_units = s.staged ? 0 : (int)s.pre_units;
+    const dim3 grid((unsigned)((A.n_req + A.pre_units) * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
     if (s.own.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, SUFFIX>), grid, dim3(256), 0, st, A);
     else hipLaunchKernelGGL((k_attend_rows<D, TYPE, 1, 4, false, SUFFIX>), grid, dim3(256), 0, st, A);
   }
@@ -504,12 +718,34 @@ void launch_shared(const LongArgs& A, const Shares& s, hipStream_t st) {
   }
 }
 
+// Sixteen tokens a product from `wide` new tokens on (see k_kv_score_wide), else a token's heads side by side.
+struct Scores { bool wide; int ht, tt, shift; int64_t ys, z; };
+Scores scores_of(const AttnArgs& A, int max_len, int* tile_run) {
+  Scores s;
+  s.shift = 0;
+  while (s.shift < 4 && (1 << s.shift) < A.group) s.shift++;
+  s.wide = A.max_new >= 16;
+  s.ht = A.group >= 3 ? 4 : A.group;
+  s.tt = 4 / s.ht;
+  const int64_t toks = s.wide ? 64 * s.tt : 16 >> s.shift;            // tokens of a workgroup
+  s.ys = (A.max_new + toks - 1) / toks;
+  int64_t cols = ((int64_t)max_len + A.T - 1) / A.T;
+  if (cols > A.cols) cols = A.cols;
+  const int64_t tiles = (cols + 15) / 16, groups = (int64_t)A.n_req * A.hkv * s.ys;
+  int64_t run = s.wide ? tiles * groups / 512 : tiles * groups / 4096;
+  *tile_run = (int)(run < 1 ? 1 : run > 8 && !s.wide ? 8 : run > tiles ? tiles : run);
+  const int64_t per = s.wide ? *tile_run : 4 * *tile_run;
+  s.z = (tiles + per - 1) / per;
+  if (s.z > 65535) s.z = 65535;                                        // (the kernels go round)
+  return s;
+}
 template <int D, int TYPE>
-void launch_score(const ScoreArgs& A, int nt, unsigned z, hipStream_t st) {
-  const int tokens = nt * (16 >> A.rows_shift);
-  const dim3 grid((unsigned)(A.n_req * A.hkv), (unsigned)((A.max_new + tokens - 1) / tokens), z);
-  if (nt == 1) hipLaunchKernelGGL((k_kv_score<D, TYPE, 1>), grid, dim3(256), 0, st, A);
-  else hipLaunchKernelGGL((k_kv_score<D, TYPE, 4>), grid, dim3(256), 0, st, A);
+void launch_score(const ScoreArgs& A, const Scores& s, hipStream_t st) {
+  const dim3 grid((unsigned)(A.n_req * A.hkv), (unsigned)s.ys, (unsigned)s.z);
+  if (!s.wide) hipLaunchKernelGGL((k_kv_score<D, TYPE>), grid, dim3(256), 0, st, A);
+  else if (s.ht == 4) hipLaunchKernelGGL((k_kv_score_wide<D, TYPE, 4, 1>), grid, dim3(256), 0, st, A);
+  else if (s.ht == 2) hipLaunchKernelGGL((k_kv_score_wide<D, TYPE, 2, 2>), grid, dim3(256), 0, st, A);
+  else hipLaunchKernelGGL((k_kv_score_wide<D, TYPE, 1, 4>), grid, dim3(256), 0, st, A);
 }
 
 }  // namespace
@@ -555,24 +791,15 @@ stq_status stq_kv_score(const stq_kv_desc* d, const stq_attend_desc* a, const vo
   ScoreArgs A;
   fill(A, d, nullptr, a, table, tok_start, len, q, nullptr, none);
   A.bounds = (const uint8_t*)bounds; A.score = score;
-  A.rows_shift = 0;
-  while (A.rows_shift < 4 && (1 << A.rows_shift) < A.group) A.rows_shift++;
-  const int nt = a->max_new > (16 >> A.rows_shift) ? 4 : 1;
-  const int64_t toks = nt * (16 >> A.rows_shift), units = (int64_t)a->n_req * A.hkv, ys = (a->max_new + toks - 1) / toks;
-  int64_t cols = ((int64_t)a->max_len + A.T - 1) / A.T;
-  if (cols > a->table_cols) cols = a->table_cols;
-  const int64_t tiles = (cols + 15) / 16;
-  int64_t run = tiles * units * ys / 8192;
-  A.tile_run = (int)(run < 1 ? 1 : run > 8 ? 8 : run);
-  int64_t z = (tiles + 4 * A.tile_run - 1) / (4 * A.tile_run);
-  if (z > 65535) z = 65535;                             // (the kernel goes round)
-  if (units * 256 > MOST_THREADS || ys > 65535) return STQ_ERR_UNSUPPORTED;
+  const Scores sc = scores_of(A, a->max_len, &A.tile_run);
+  A.rows_shift = sc.shift;
+  if ((int64_t)a->n_req * A.hkv * 256 > MOST_THREADS || sc.ys > 65535) return STQ_ERR_UNSUPPORTED;
   if (d->d == 64) {
-    if (a->type == STQ_BF16) launch_score<64, STQ_BF16>(A, nt, (unsigned)z, st);
-    else launch_score<64, STQ_FP16>(A, nt, (unsigned)z, st);
+    if (a->type == STQ_BF16) launch_score<64, STQ_BF16>(A, sc, st);
+    else launch_score<64, STQ_FP16>(A, sc, st);
   } else {
-    if (a->type == STQ_BF16) launch_score<128, STQ_BF16>(A, nt, (unsigned)z, st);
-    else launch_score<128, STQ_FP16>(A, nt, (unsigned)z, st);
+    if (a->type == STQ_BF16) launch_score<128, STQ_BF16>(A, sc, st);
+    else launch_score<128, STQ_FP16>(A, sc, st);
   }
   return launched();
 }
@@ -594,13 +821,14 @@ stq_status stq_kv_select(const stq_select_desc* c, const int32_t* tok_start, con
   A.n_req = c->n_req; A.n_tok = c->n_tok; A.hkv = c->n_kv_heads; A.T = c->block_tokens; A.cols = c->table_cols;
   A.n_sel = c->n_sel; A.n_first = c->n_first; A.n_last = c->n_last; A.max_new = c->max_new;
   A.by_hkv = div_of(A.hkv); A.by_max_new = div_of(A.max_new);
-  const int waves = A.cols <= 512 ? 1 : A.cols <= 2048 ? 4 : 16;
-  const int64_t units = (int64_t)c->n_req * c->max_new * c->n_kv_heads, groups = waves == 1 ? (units + 3) / 4 : units;
-  if (units > INT32_MAX || groups * (waves == 1 ? 256 : 64 * waves) > MOST_THREADS) return STQ_ERR_UNSUPPORTED;
+  const int64_t units = (int64_t)c->n_req * c->max_new * c->n_kv_heads;
+  const int64_t groups = A.cols <= 2048 ? (units + 3) / 4 : units;    // four rows a workgroup, or one
+  if (units > INT32_MAX || groups * (A.cols <= 2048 ? 256 : 1024) > MOST_THREADS) return STQ_ERR_UNSUPPORTED;
   const dim3 g((unsigned)groups);
-  if (A.cols <= 128) hipLaunchKernelGGL((k_kv_select<1, 2>), g, dim3(256), 0, st, A);
-  else if (waves == 1) hipLaunchKernelGGL((k_kv_select<1, 8>), g, dim3(256), 0, st, A);
-  else if (waves == 4) hipLaunchKernelGGL((k_kv_select<4, 8>), g, dim3(256), 0, st, A);
+  if (A.cols <= 64) hipLaunchKernelGGL((k_kv_select<1, 1>), g, dim3(256), 0, st, A);
+  else if (A.cols <= 256) hipLaunchKernelGGL((k_kv_select<1, 4>), g, dim3(256), 0, st, A);
+  else if (A.cols <= 512) hipLaunchKernelGGL((k_kv_select<1, 8>), g, dim3(256), 0, st, A);
+  else if (A.cols <= 2048) hipLaunchKernelGGL((k_kv_select<1, 32>), g, dim3(256), 0, st, A);
   else if (A.cols <= 8192) hipLaunchKernelGGL((k_kv_select<16, 8>), g, dim3(1024), 0, st, A);
   else hipLaunchKernelGGL((k_kv_select<16, 32>), g, dim3(1024), 0, st, A);
   return launched();
@@ -636,7 +864,8 @@ stq_status stq_kv_attend_blocks(const stq_kv_desc* d, const void* cache, size_t 
   fill(A, d, cache, a, table, tok_start, len, q, o, sp);
   A.sel = sel; A.n_sel = n_sel;
   A.group_start = A.prefix = nullptr; A.shared = nullptr;
-  A.n_groups = A.pre_splits = A.pre_per = 0;
+  A.n_groups = A.pre_per = A.slot0 = A.pre_units = 0;
+  A.pre_fill = 0.0f;
   A.po = (float*)work;
   A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
   if (d->d == 64) {
@@ -652,7 +881,7 @@ stq_status stq_kv_attend_blocks(const stq_kv_desc* d, const void* cache, size_t 
 size_t stq_kv_attend_shared_bytes(const stq_kv_desc* d, const stq_attend_desc* a, const stq_shared_desc* g) {
   if (!kv_ok(d) || !long_ok(d, a) || !g || g->n_groups < 0 || g->max_prefix < 0) return 0;
   const Shares s = shares_of(d, a, g);
-  return (size_t)(s.own.splits + s.pre.splits) * a->n_tok * a->n_heads * (d->d + 2) * 4 + ((size_t)a->n_req * 4 + 15) / 16 * 16;
+  return (size_t)(s.own.splits + s.slots) * a->n_tok * a->n_heads * (d->d + 2) * 4 + ((size_t)a->n_req * 4 + 19) / 16 * 16;
 }
 
 stq_status stq_kv_attend_shared(const stq_kv_desc* d, const void* cache, size_t bytes, const stq_attend_desc* a,
@@ -675,14 +904,15 @@ stq_status stq_kv_attend_shared(const stq_kv_desc* d, const void* cache, size_t 
   const int64_t groups = (int64_t)a->n_req * d->n_kv_heads, pre = sp.pre_units * d->n_kv_heads;
   if ((int64_t)a->n_req * a->max_new * a->n_heads > INT32_MAX || (int64_t)a->n_tok * a->n_heads > INT32_MAX ||
       (sp.own.staged ? groups * sp.own.tiles * sp.own.splits : groups) * 256 > MOST_THREADS ||
-      (sp.pre.staged ? pre * sp.pre.splits : pre) * 256 > MOST_THREADS || (int64_t)a->n_req * a->max_new * 256 > MOST_THREADS)
+      (groups + pre) * 256 > MOST_THREADS || (int64_t)a->n_req * a->max_new * 256 > MOST_THREADS)
     return STQ_ERR_UNSUPPORTED;
   LongArgs A;
   fill(A, d, cache, a, table, tok_start, len, q, o, sp.own);
   A.sel = nullptr; A.n_sel = 0;
   A.group_start = group_start; A.prefix = prefix;
-  A.n_groups = g->n_groups; A.pre_splits = sp.pre.splits; A.pre_per = sp.pre.per;
-  const int64_t rows = (int64_t)(sp.own.splits + sp.pre.splits) * a->n_tok * a->n_heads;
+  A.n_groups = g->n_groups; A.pre_per = sp.per; A.slot0 = sp.slots; A.pre_units = 0;
+  A.pre_fill = (float)d->n_kv_heads / PRE_GROUPS;
+  const int64_t rows = (int64_t)(sp.own.splits + sp.slots) * a->n_tok * a->n_heads;
   A.po = (float*)work;
   A.pml = A.po + rows * d->d;
   A.shared = (int32_t*)(A.pml + 2 * rows);
