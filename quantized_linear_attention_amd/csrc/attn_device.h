@@ -126,7 +126,7 @@ struct LongArgs : AttnArgs {
   const int32_t *group_start, *prefix;   // PREFIX and SUFFIX: [n_groups + 1], [n_groups]
   int n_groups, pre_per;                 // chunks of a prefix' part at least
   int slot0;                             // parts of a prefix at most; in the workspace those of the requests' own tokens follow
-  float pre_fill;                        // heads / workgroups that fill the card
+  int pre_fill;                          // workgroups of a head that fill the card
   int pre_units;                         // SUFFIX: workgroups (times heads) that take a prefix' part
   int32_t* shared;                       // [n_req] tokens that the request's group shares, then the chunks of a prefix' part
 };
@@ -259,9 +259,7 @@ struct Whole {
   }
   // The x-th part of all prefixes' work: group, tile of its rows, part of its chunks
   // and how many chunks a part has, the same for all.  Parts are sized by what all
-  // groups together have to do, so that the card is filled once (with parts for a
-  // whole group of the longest prefix a host can only guess: four groups of 12,000
-  // to 16,384 shared tokens 235 us, 199 by the best fixed size).
+  // groups together have to do, so that the card is filled once.
   struct Part { int g, tile, sp, per; };
   __device__ __forceinline__ bool part(int rows_of_tile, int x, Part* r) const {
     const int lane = threadIdx.x & 63;
@@ -292,8 +290,18 @@ struct Whole {
       total += wave_sum((float)tiles * (float)chunks);
       most = max(most, wave_max_i(chunks));
     }
-    const int fill = (int)__builtin_fminf(total * A.pre_fill, 0x1p30f);
+    const int fill = (int)__builtin_fminf(total / A.pre_fill, 0x1p30f);
     r->per = (max(max(fill, A.pre_per), (most + A.slot0 - 1) / A.slot0) + 3) & ~3;
+    // (whole parts are more than the total says: no second round of a few workgroups)
+    for (int n = 0; r->per < most; n++) {
+      int count = 0;
+      for (int b = 0; b < A.n_groups; b += 64) {
+        if (A.n_groups > 64) of(b, &tiles, &chunks);
+        count += wave_sum_i(tiles * ((chunks + r->per - 1) / r->per));
+      }
+      if (count <= A.pre_fill) break;
+      r->per = n < 24 ? r->per + max((r->per >> 4) & ~3, 4) : (most + 3) & ~3;
+    }
     for (int b = 0; b < A.n_groups; b += 64) {
       if (A.n_groups > 64) of(b, &tiles, &chunks);
       const int parts = (chunks + r->per - 1) / r->per, mine = tiles * parts;

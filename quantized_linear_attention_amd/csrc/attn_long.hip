@@ -865,7 +865,7 @@ stq_status stq_kv_attend_blocks(const stq_kv_desc* d, const void* cache, size_t 
   A.sel = sel; A.n_sel = n_sel;
   A.group_start = A.prefix = nullptr; A.shared = nullptr;
   A.n_groups = A.pre_per = A.slot0 = A.pre_units = 0;
-  A.pre_fill = 0.0f;
+  A.pre_fill = 0;
   A.po = (float*)work;
   A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
   if (d->d == 64) {
@@ -911,7 +911,7 @@ stq_status stq_kv_attend_shared(const stq_kv_desc* d, const void* cache, size_t 
   A.sel = nullptr; A.n_sel = 0;
   A.group_start = group_start; A.prefix = prefix;
   A.n_groups = g->n_groups; A.pre_per = sp.per; A.slot0 = sp.slots; A.pre_units = 0;
-  A.pre_fill = (float)d->n_kv_heads / PRE_GROUPS;
+  A.pre_fill = (int)((PRE_GROUPS + d->n_kv_heads - 1) / d->n_kv_heads);
   const int64_t rows = (int64_t)(sp.own.splits + sp.slots) * a->n_tok * a->n_heads;
   A.po = (float*)work;
   A.pml = A.po + rows * d->d;
