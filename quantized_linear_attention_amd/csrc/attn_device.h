@@ -128,6 +128,7 @@ struct LongArgs : AttnArgs {
   int slot0;                             // parts of a prefix at most; in the workspace those of the requests' own tokens follow
   int pre_fill;                          // workgroups of a head that fill the card
   int pre_units;                         // SUFFIX: workgroups (times heads) that take a prefix' part
+  int pre_blocks;                        // PREFIX: workgroups that do; the others take the requests' own tokens
   int32_t* shared;                       // [n_req] tokens that the request's group shares, then the chunks of a prefix' part
 };
 template <int MODE> using ArgsOf = std::conditional_t<MODE == SPAN, AttnArgs, LongArgs>;
@@ -654,18 +655,16 @@ __device__ __forceinline__ void scale_rows(uint64_t far, float f, f32x4 (*o)[D /
 // up to 8,192 tokens 24 rows 40 us, 36 rows 41, 64 rows 60 (the bytes take 17 to 20):
 // at 191 registers two workgroups a CU, and each tile of 32 rows reads and
 // unpacks the cache for itself.
-template <int D, int TYPE, int NT, int NWV, bool ONCE, int MODE = SPAN>
-__global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(ArgsOf<MODE> A) {
+template <int D, int TYPE, int NT, int NWV, bool ONCE, int MODE>
+__device__ __forceinline__ void attend_rows(const ArgsOf<MODE>& A, uint32_t bx, int by, int bz, f32x4 (*so)[NT * (D / 16)][64], f32x2 (*sml)[NT][16]) {
   constexpr int NC = D / 16;
-  __shared__ f32x4 so[NWV][NT * NC][64];
-  __shared__ f32x2 sml[NWV][NT][16];
   const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   // the splits slowest: a short request has none of the last ones, and
   // neighbouring workgroups go to different XCDs
-  int i = quot(blockIdx.x, A.by_hkv), tile = blockIdx.y;
-  const int h = blockIdx.x - i * A.hkv;
-  int sp = blockIdx.z;
+  int i = quot(bx, A.by_hkv), tile = by;
+  const int h = bx - i * A.hkv;
+  int sp = bz;
   Req R;
   int shared = 0, pre_per = 0;
   bool pre = false;            // SUFFIX: a tile of rows of a whole group over what they share
@@ -676,7 +675,7 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
       pre = true;
       Whole::Part part;
       const bool on = whole_batch.part(16 * NT, i, &part);
-      if (blockIdx.x == 0 && threadIdx.x == 0) A.shared[A.n_req] = part.per;
+      if (bx == 0 && threadIdx.x == 0) A.shared[A.n_req] = part.per;
       if (!on) return;
       const Members m = whole_batch.group(part.g);
       tile = part.tile;
@@ -968,6 +967,13 @@ __global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(Arg
   }
 }
 
+template <int D, int TYPE, int NT, int NWV, bool ONCE, int MODE = SPAN>
+__global__ void __launch_bounds__(64 * NWV, NWV == 16 ? 4 : 2) k_attend_rows(ArgsOf<MODE> A) {
+  __shared__ f32x4 so[NWV][NT * (D / 16)][64];
+  __shared__ f32x2 sml[NWV][NT][16];
+  attend_rows<D, TYPE, NT, NWV, ONCE, MODE>(A, blockIdx.x, blockIdx.y, blockIdx.z, so, sml);
+}
+
 // Many query rows per key/value head (prompts): the matrix products bound the
 // work.  One workgroup = one (request, head, tile of 128 rows, split), each wave
 // 32 rows.  Tiles of 64 cached tokens (two chunks) go through LDS as
@@ -1062,9 +1068,18 @@ __global__ void __launch_bounds__(64 * TILE_WAVES, 2) k_attend_tiles(ArgsOf<MODE
   __shared__ __attribute__((aligned(16))) uint8_t lds_k[2][64 * D * 2], lds_v[2][64 * D * 2];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, G = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int b = blockIdx.x;
+  if constexpr (MODE == PREFIX) {
+    // Behind the prefixes' parts, where there are few rows of a request's own, these
+    // too: they wait for memory where the others wait for the matrix cores.
+    if (b >= A.pre_blocks) {
+      const uint32_t x = b - A.pre_blocks, sp = x / (uint32_t)(A.n_req * A.hkv);
+      attend_rows<D, TYPE, 1, 4, false, SUFFIX>(A, x - sp * (uint32_t)(A.n_req * A.hkv), 0, sp, (f32x4(*)[D / 16][64])lds_k[0], (f32x2(*)[1][16])lds_v[0]);
+      return;
+    }
+  }
   // heads fastest: a head's workgroups share an XCD where the heads are a
   // multiple of 8
-  int b = blockIdx.x;
   const int h = b % A.hkv; b /= A.hkv;
   int sp = MODE == PREFIX ? 0 : b % A.splits;
   int i, row0, shared = 0, pre_per = 0;

@@ -657,7 +657,7 @@ Split blocks_split(const stq_kv_desc* d, const stq_attend_desc* a, int n_sel) {
 // Parts of the requests' own tokens, and room for those of the shared prefixes:
 // sized on the device by what the groups have to do (Whole::part), from `per`
 // chunks up and at most `slots` of them.
-struct Shares { Split own; bool staged; int tile_rows, slots, per; int64_t pre_units; };
+struct Shares { Split own; bool staged, both; int tile_rows, slots, per; int64_t pre_units; };
 constexpr int64_t MOST_PARTS = 64, PRE_GROUPS = 512;   // (the join holds 128 parts' statistics in its lanes)
 Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_shared_desc* g) {
   Shares s;
@@ -675,6 +675,7 @@ Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_share
   if (s.own.waves == 16) s.own.waves = 4;
   const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
   s.staged = g->n_groups > 0 && (s.own.staged || all / g->n_groups > STAGED_ROWS);
+  s.both = s.staged && s.own.tile_rows == 16;
   s.tile_rows = s.staged ? 32 * TILE_WAVES : s.own.tile_rows;
   const int64_t tiles = (all + s.tile_rows - 1) / s.tile_rows, fill = (PRE_GROUPS + d->n_kv_heads - 1) / d->n_kv_heads;
   s.pre_units = g->n_groups > 0 ? fill + tiles + g->n_groups : 0;
@@ -702,11 +703,15 @@ void launch_blocks(const LongArgs& A, const Split& s, hipStream_t st) {
 
 template <int D, int TYPE>
 void launch_shared(LongArgs& A, const Shares& s, hipStream_t st) {
-  if (s.staged) hipLaunchKernelGGL((k_attend_tiles<D, TYPE, PREFIX>), dim3((unsigned)(s.pre_units * A.hkv)), dim3(64 * TILE_WAVES), 0, st, A);
+  if (s.staged) {
+    A.pre_blocks = (int)(s.pre_units * A.hkv);
+    const int64_t more = s.both ? (int64_t)A.n_req * A.hkv * A.splits : 0;
+    hipLaunchKernelGGL((k_attend_tiles<D, TYPE, PREFIX>), dim3((unsigned)(A.pre_blocks + more)), dim3(64 * TILE_WAVES), 0, st, A);
+  }
   if (s.own.staged) {
     const unsigned grid = (unsigned)((int64_t)A.n_req * A.hkv * A.tiles * A.splits);
     hipLaunchKernelGGL((k_attend_tiles<D, TYPE, SUFFIX>), dim3(grid), dim3(64 * TILE_WAVES), 0, st, A);
-  } else {                                              // and prefixes of few rows, in one launch
+  } else if (!s.both) {                                 // and prefixes of few rows, in one launch
     A.pre_units = s.staged ? 0 : (int)s.pre_units;
     const dim3 grid((unsigned)((A.n_req + A.pre_units) * A.hkv), (unsigned)A.tiles, (unsigned)A.splits);
     if (s.own.tile_rows == 32) hipLaunchKernelGGL((k_attend_rows<D, TYPE, 2, 4, false, SUFFIX>), grid, dim3(256), 0, st, A);
@@ -864,7 +869,7 @@ stq_status stq_kv_attend_blocks(const stq_kv_desc* d, const void* cache, size_t 
   fill(A, d, cache, a, table, tok_start, len, q, o, sp);
   A.sel = sel; A.n_sel = n_sel;
   A.group_start = A.prefix = nullptr; A.shared = nullptr;
-  A.n_groups = A.pre_per = A.slot0 = A.pre_units = 0;
+  A.n_groups = A.pre_per = A.slot0 = A.pre_units = A.pre_blocks = 0;
   A.pre_fill = 0;
   A.po = (float*)work;
   A.pml = A.po + (int64_t)sp.splits * a->n_tok * a->n_heads * d->d;
@@ -904,13 +909,13 @@ stq_status stq_kv_attend_shared(const stq_kv_desc* d, const void* cache, size_t 
   const int64_t groups = (int64_t)a->n_req * d->n_kv_heads, pre = sp.pre_units * d->n_kv_heads;
   if ((int64_t)a->n_req * a->max_new * a->n_heads > INT32_MAX || (int64_t)a->n_tok * a->n_heads > INT32_MAX ||
       (sp.own.staged ? groups * sp.own.tiles * sp.own.splits : groups) * 256 > MOST_THREADS ||
-      (groups + pre) * 256 > MOST_THREADS || (int64_t)a->n_req * a->max_new * 256 > MOST_THREADS)
+      (groups * sp.own.splits + pre) * 256 > MOST_THREADS || (int64_t)a->n_req * a->max_new * 256 > MOST_THREADS)
     return STQ_ERR_UNSUPPORTED;
   LongArgs A;
   fill(A, d, cache, a, table, tok_start, len, q, o, sp.own);
   A.sel = nullptr; A.n_sel = 0;
   A.group_start = group_start; A.prefix = prefix;
-  A.n_groups = g->n_groups; A.pre_per = sp.per; A.slot0 = sp.slots; A.pre_units = 0;
+  A.n_groups = g->n_groups; A.pre_per = sp.per; A.slot0 = sp.slots; A.pre_units = A.pre_blocks = 0;
   A.pre_fill = (int)((PRE_GROUPS + d->n_kv_heads - 1) / d->n_kv_heads);
   const int64_t rows = (int64_t)(sp.own.splits + sp.slots) * a->n_tok * a->n_heads;
   A.po = (float*)work;
