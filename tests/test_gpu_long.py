@@ -569,3 +569,83 @@ def test_together_in_a_graph(stq):
             assert torch.equal(A.bounds.view(torch.uint8), X.bounds.view(torch.uint8))
         freed += int(A.used.item())
         torch.ones(1000, device="cuda").sum().item()
+
+
+def test_blocks_of_many_tokens(stq):
+    """Token and head pairs enough for a wave each."""
+    for dtype, heads, kv, d, T in (("bf16", 8, 4, 128, 32), ("fp16", 4, 4, 64, 64)):
+        x = Long(stq, [700, 40], [520, 3], heads, kv, d, T, dtype, seed=d, extra_cols=1)
+        x.table[0, 2] = -1
+        sel = lists(x, 5, np.random.default_rng(d))
+        x.check_blocks(x.blocks(sel), sel)
+
+
+@pytest.mark.parametrize("heads,kv,d,news", [(4, 2, 128, [20, 1]), (2, 2, 64, [70, 3]), (12, 2, 64, [17, 17]), (8, 2, 128, [2, 1])])
+def test_score_of_long_requests(stq, heads, kv, d, news):
+    """More blocks than a wave's window of the table, over several parts of the work."""
+    x = Long(stq, [32 * 701, 32 * 300 + 5], news, heads, kv, d, 32, "bf16", seed=d)
+    b = x.all_bounds()
+    x.table[0, 300:310] = -1
+    s = x.score(b)
+    check_score(x, b, s)
+    assert (host(x.score(b, max_len=50)) == host(s)).all()
+
+
+def test_shared_more_requests_than_lanes(stq):
+    """Past 256 requests what the workgroups know of the batch is looked up another way; the result is the same."""
+    rng = np.random.default_rng(11)
+    for new, prefix in ((1, [128, 0, 96]), (9, [128, 64, 96])):
+        sizes = [200, 3, 90]
+        lens = np.concatenate([p + new + rng.integers(0, 40, s) for s, p in zip(sizes, prefix)])
+        x = Long(stq, lens, [new] * 293, 8, 1, 64, 32, "bf16", seed=new)
+        x.share(sizes, prefix)
+        o = x.shared()
+        x.check(o)
+
+
+def test_long_contexts_past_32_bits(stq):
+    """Blocks more than 4 GiB into the cache give what the first ones give, bit for bit."""
+    import torch
+    T, kv, d = 256, 8, 128
+    x = Long(stq, [900, 256, 513], [3, 1, 40], 16, kv, d, T, "bf16", seed=12)
+    x.share([3], [256])
+    small, nb = x.kvc, x.kvc.desc.n_blocks
+    sel = lists(x, 3, np.random.default_rng(1), odd=False)
+    b = x.all_bounds()
+    want = (x.score(b), x.blocks(sel), x.shared())
+    at = (5 << 30) // (x.pages.numel() // nb)
+    big = torch.zeros((at + nb) * (x.pages.numel() // nb), dtype=torch.uint8, device="cuda")
+    big[at * (x.pages.numel() // nb):] = x.pages.flatten()
+    x.kvc = stq.make_kv(big, T, kv, d)
+    x.table = np.where(x.table >= 0, x.table + at, -1)
+    bb = x.all_bounds()
+    assert torch.equal(bb[at:].view(torch.uint8), b.view(torch.uint8)) and (e5m2_raw(bb[:at]) == 0x7F).all()
+    for a, c in zip(want, (x.score(bb), x.blocks(sel), x.shared())):
+        assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(c))
+    assert small.desc.n_blocks == nb
+
+
+def test_calls_of_slices(stq):
+    """Requests a .. b-1 of a plan in a call of their own: the same rows, the others left alone."""
+    import torch
+    x = Long(stq, [300, 64, 500, 33], [2, 1, 30, 1], 8, 2, 128, 32, "bf16", seed=13)
+    b = x.all_bounds()
+    s = x.score(b)
+    sel = lists(x, 4, np.random.default_rng(2), odd=False)
+    o, c = x.blocks(sel), x.shared(groups=[0], prefix=[])
+    i, n = torch.int32, 4
+    table, start, lens = i32(x.table), i32(x.start), i32(x.lens)
+    s2, o2, c2 = torch.full_like(s, 7.0), torch.full_like(o, 5.0), torch.full_like(c, 5.0)
+    for lo, hi, new in ((0, 2, 2), (2, 3, 30), (3, 4, 1)):
+        t, st, le = table[lo:hi], start[lo:hi + 1], lens[lo:hi]
+        stq.stq_kv_score(x.kvc, b, t, st, le, x.q, s2, x.scale, new, 500)
+        w = stq.stq_kv_attend_blocks_bytes(x.kvc, hi - lo, x.tok, 8, 4, new)
+        stq.stq_kv_attend_blocks(x.kvc, t, st, le, sel, x.q, o2, x.scale, new, torch.empty(w, dtype=torch.uint8, device="cuda") if w else None)
+        w = stq.stq_kv_attend_shared_bytes(x.kvc, hi - lo, x.tok, 8, 0, new, 500, 0)
+        stq.stq_kv_attend_shared(x.kvc, t, st, le, torch.zeros(1, dtype=i, device="cuda"), torch.zeros(0, dtype=i, device="cuda"), x.q, c2,
+                                 x.scale, new, 500, 0, torch.empty(w, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert n == len(x.lens)
+    check_score(x, b, s2)
+    x.check_blocks(o2, sel)
+    x.check(c2)
