@@ -597,7 +597,8 @@ size_t stq_kv_bounds_bytes(const stq_kv_desc* desc);
  * belong to one request.  A block with a poisoned key (one stored with NaN
  * scales) gets NaN bounds.  STQ_ERR_UNSUPPORTED from 2^24 (request, block)
  * pairs on that max_new makes possible: n_req * min((max_new - 1) /
- * block_tokens + 2, table_cols). */
+ * block_tokens + 2, table_cols).  The bounds may not overlap the cache
+ * (STQ_ERR_ARG). */
 stq_status stq_kv_bounds(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, int32_t n_req, int32_t max_new,
                          const int32_t* table_dev, int32_t table_cols, const int32_t* tok_start_dev,
                          const int32_t* len_dev, void* bounds_dev, hipStream_t stream);
@@ -609,10 +610,10 @@ stq_status stq_kv_bounds(const stq_kv_desc* desc, const void* cache_dev, size_t 
  * blocks outside the cache get -inf, blocks with NaN bounds NaN, columns behind
  * p's block are left as they were.  max_len sets the split of the work, never the
  * result; o_stride is not used.  Products are exact (queries scaled by a power
- * of two per row), sums binary32.  score may overlap neither q nor the bounds
+ * of two per row or token), sums binary32; a query with infinities or NaN has no
+ * meaningful score.  score may overlap neither q nor the bounds
  * (STQ_ERR_ARG).  STQ_ERR_UNSUPPORTED from n_req * n_kv_heads = 2^24 on and from
- * 65,536 tiles of a request's tokens on (16 query rows each, 64 where max_new
- * needs more than one). */
+ * max_new = 2^22 on (2^23 with two query heads to a key/value head, 2^24 with one). */
 stq_status stq_kv_score(const stq_kv_desc* desc, const stq_attend_desc* a, const void* bounds_dev,
                         const int32_t* table_dev, const int32_t* tok_start_dev, const int32_t* len_dev,
                         const void* q_dev, float* score_dev, hipStream_t stream);
@@ -668,7 +669,8 @@ typedef struct stq_shared_desc {
  * group_start[0] or from group_start[n_groups] on are in no group.  In the
  * descriptor max_len is about the longest own part (len minus prefix): it sets
  * the split of the work, never the result.  The workspace is always needed.
- * Errors, overlap and roundings as stq_kv_attend. */
+ * Errors, overlap and roundings as stq_kv_attend; STQ_ERR_UNSUPPORTED also where
+ * n_kv_heads times the groups and the tiles of all query rows passes 2^24. */
 size_t stq_kv_attend_shared_bytes(const stq_kv_desc* desc, const stq_attend_desc* a, const stq_shared_desc* g);
 stq_status stq_kv_attend_shared(const stq_kv_desc* desc, const void* cache_dev, size_t bytes, const stq_attend_desc* a,
                                 const stq_shared_desc* g, const int32_t* table_dev, const int32_t* tok_start_dev,

@@ -17,7 +17,10 @@ namespace {
 // 32 channels of a scale; tokens of a pass lie on lane bits 0, 1, 4, 5 (and 3
 // at d = 64), channel groups on bit 2 (and 3), so that the joins over tokens
 // are register swaps (permlane32 and 16, each halving what a lane holds) and
-// DPP steps.  Lanes past the last token read the last one again.
+// DPP steps.  Lanes past the last token read the last one again.  All of a block's
+// loads are asked for at once.  A chain of counts, table and keys bounds it: the
+// blocks of 32,768 tokens of 8 heads (d = 128) 7.7 us, 1.8 TB/s; 512 blocks
+// scattered over 2.6 GB of pages 12.6 us, where a launch alone takes 2.
 struct BoundsArgs {
   const uint8_t* cache;
   const int32_t *table, *tok_start, *len;
@@ -147,8 +150,12 @@ __global__ void __launch_bounds__(256) k_kv_bounds(BoundsArgs A) {
 // a byte shifted up) against the queries' positive and negative parts.  Rows of a
 // tile: 16 blocks; columns: the heads of a token side by side, the last one
 // repeated up to a power of two (a maximum does not mind), so that the group's
-// maximum is DPP steps.  Products are exact in binary32; queries are scaled by
-// a power of two per row as in the attention.
+// maximum is DPP steps.  Products are exact in binary32.
+//
+// Memory and latency bound: 64 requests of 8,192 to 32,768 tokens in blocks of
+// 64, 32 heads over 8, d = 128: 14 us for 42 MB (3.0 TB/s; the chain of counts,
+// table, bounds and store is 5 us of it).  A wave takes four tiles of blocks there:
+// 16.6 us with one, 14.9 with two, 15.3 with eight.
 struct ScoreArgs : AttnArgs {
   const uint8_t* bounds;
   float* score;
@@ -319,6 +326,13 @@ __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
 // the group's maximum is taken between a lane's own registers; a wave holds TT
 // such sets of tokens (HT TT products to each widened bound) and goes over the
 // blocks that they see.  One power of two scales all of a token's HT queries.
+//
+// Two prompts of 1,024 to 2,048 tokens over 16,384 positions, 32 heads over 8, d =
+// 128: 27 us for 59 MB and 12.8 GFLOP (70 us by the kernel above, whose columns
+// are mostly repeated queries there).  Half of a wave's life is waiting: 33 MB of
+// queries come in before its first product and two waves a SIMD fill the registers;
+// the matrix cores are busy 20 % of the time.  Waves that take all of a request's
+// blocks are the fastest (16 tiles 27 us, 8 33, 4 41: each converts the queries).
 template <int D, int TYPE, int HT, int TT>
 __global__ void __launch_bounds__(256, 2) k_kv_score_wide(ScoreArgs A) {
   constexpr int LD = D / 64, NT = HT * TT;
@@ -460,6 +474,12 @@ __global__ void __launch_bounds__(256, 2) k_kv_score_wide(ScoreArgs A) {
 // whatever the split.
 //
 // W waves a row, each with M blocks a lane: block 64 (M wave + m) + lane.
+//
+// Instruction bound: 32,768 rows of up to 256 scores 29 us (0.34 us a thousand rows
+// and wave slot; 340 vector instructions a row and as many scalar ones), 512 rows of
+// 128 to 512 7.6 us, of which the launch and the row's loads are five.  Four rows a
+// wave with sums over sixteen lanes: 27 us, but 8.1 us for the 512 rows; one bit a
+// trial: 53 and 8.6 us.
 struct SelectArgs {
   const float* score;
   const int32_t *tok_start, *len;
@@ -675,10 +695,15 @@ Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_share
   if (s.own.waves == 16) s.own.waves = 4;
   const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
   s.staged = g->n_groups > 0 && (s.own.staged || all / g->n_groups > STAGED_ROWS);
+  // The requests' own tokens, few rows each, in the same launch as the staged prefixes:
+  // 64 requests behind two prefixes of 8,192 tokens 46 us in two, 38 in one; behind one
+  // 44, 37; 128 59, 58; 770 query tokens behind four of 16,384 280, 262.
   s.both = s.staged && s.own.tile_rows == 16;
   s.tile_rows = s.staged ? 32 * TILE_WAVES : s.own.tile_rows;
   const int64_t tiles = (all + s.tile_rows - 1) / s.tile_rows, fill = (PRE_GROUPS + d->n_kv_heads - 1) / d->n_kv_heads;
   s.pre_units = g->n_groups > 0 ? fill + tiles + g->n_groups : 0;
+  // (prefix kernel and join of 64 requests behind 2,048 tokens: parts of 8 chunks 23 us, of 12 24, of 16 26;
+  // behind 8,192 34, 34, 32; 128 in four groups 48, 40, 39)
   s.per = 12;
   const int64_t chunks = (int64_t)g->max_prefix / 32 + 1;
   int64_t slots = 2 * fill / (tiles > 0 ? tiles : 1) + 1;
@@ -723,7 +748,8 @@ void launch_shared(LongArgs& A, const Shares& s, hipStream_t st) {
   }
 }
 
-// Sixteen tokens a product from `wide` new tokens on (see k_kv_score_wide), else a token's heads side by side.
+// Sixteen tokens a product from 16 new tokens on (k_kv_score_wide: below, its columns
+// would be tokens that are not there), else a token's heads side by side.
 struct Scores { bool wide; int ht, tt, shift; int64_t ys, z; };
 Scores scores_of(const AttnArgs& A, int max_len, int* tile_run) {
   Scores s;
@@ -737,6 +763,7 @@ Scores scores_of(const AttnArgs& A, int max_len, int* tile_run) {
   int64_t cols = ((int64_t)max_len + A.T - 1) / A.T;
   if (cols > A.cols) cols = A.cols;
   const int64_t tiles = (cols + 15) / 16, groups = (int64_t)A.n_req * A.hkv * s.ys;
+  // (as many waves as the card holds: two workgroups a CU there, four waves a SIMD here)
   int64_t run = s.wide ? tiles * groups / 512 : tiles * groups / 4096;
   *tile_run = (int)(run < 1 ? 1 : run > 8 && !s.wide ? 8 : run > tiles ? tiles : run);
   const int64_t per = s.wide ? *tile_run : 4 * *tile_run;
