@@ -576,6 +576,8 @@ stq_status stq_kv_attend(const stq_kv_desc* desc, const void* cache_dev, size_t 
  * request i sits at p = len[i] - (tok_start[i+1] - tok_start[i]) + j; rows and
  * tokens outside of any request, and queries past max_new, are left alone.
  * Their stq_attend_desc has window = n_sink = 0 (else STQ_ERR_ARG).
+ * q, o, bounds, score, sel and the workspace are 16-byte aligned, q and o with
+ * strides a multiple of 16 bytes, else STQ_ERR_LAYOUT.
  *
  * BOUNDS: per block b, key/value head h and channel c the least and the largest
  * key of the block, as E5M2 (the upper byte of a binary16; 0x7F for NaN),
