@@ -168,7 +168,8 @@ __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
 // behind the first new token of any member that has one, so that every row sees
 // all of them.  Up to 256 requests in 64 groups are loaded at once, one request or
 // group a lane, and the rest is exchanged between lanes: a chain of one load
-// instead of three or four, each a microsecond where the lines are cold.
+// instead of three or four (the prefixes' part of 64 requests behind two of them 24.6
+// -> 23.2 us).
 struct Members { int s, e, first, last, len; };
 __device__ __forceinline__ int wave_max_i(int x);
 struct Whole {
