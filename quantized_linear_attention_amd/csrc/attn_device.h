@@ -1532,7 +1532,8 @@ constexpr int STAGED_ROWS = 64;
 // caches; 8 requests of 32,768 to 131,072 tokens: 156 us at four, 153 at six, 146
 // at eight, 150 at ten, 152 at sixteen).
 constexpr int64_t CUS = 256, FEW_GROUPS = 512, FEW_CHUNKS = 12, MANY_GROUPS = 2048, MANY_CHUNKS = 48, MOST_SPLITS = 128;
-void cut(Split* x, int64_t base, int64_t chunks, int64_t few_chunks = FEW_CHUNKS) {
+// (sixteen: whether the caller has a kernel of sixteen waves, and would need no second launch)
+void cut(Split* x, int64_t base, int64_t chunks, int64_t few_chunks = FEW_CHUNKS, bool sixteen = true) {
   Split& s = *x;
   auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
   int64_t k = 1;
@@ -1550,7 +1551,7 @@ void cut(Split* x, int64_t base, int64_t chunks, int64_t few_chunks = FEW_CHUNKS
   // 16.9, 14.1; 16 of 640 7.3, 8.1; 1,100 10.5, 10.1; 1,900 12.7, 12.5; 2,048 12.9,
   // 13.1.  (d = 64 gains from 640 on: 20 requests of 640 6.3, 6.2, of 2,048 11.9, 10.3.)
   s.waves = 4;
-  if (s.tile_rows == 16 && base <= CUS && chunks >= 2 * FEW_CHUNKS && chunks < (2 * base >= CUS ? 65 : 3 * FEW_CHUNKS)) {
+  if (sixteen && s.tile_rows == 16 && base <= CUS && chunks >= 2 * FEW_CHUNKS && chunks < (2 * base >= CUS ? 65 : 3 * FEW_CHUNKS)) {
     s.waves = 16;
     k = 1;
   }

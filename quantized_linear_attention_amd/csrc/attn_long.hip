@@ -686,13 +686,15 @@ Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_share
   s.own.staged = rows > STAGED_ROWS;
   s.own.tile_rows = s.own.staged ? 32 * TILE_WAVES : rows > 16 ? 32 : 16;
   s.own.tiles = (int)((rows + s.own.tile_rows - 1) / s.own.tile_rows);
-  cut(&s.own, (int64_t)a->n_req * d->n_kv_heads * s.own.tiles, ((int64_t)a->max_len + 31) / 32);
+  // (four waves at any length: the prefixes' parts are joined in a second launch anyhow.  Split in parts against
+  // whole, us on the GPU, 8 heads, d = 128, behind 2,048 tokens: 4 requests of up to 1,000 own tokens 13.3, 15.7; 16 of 800
+  // 16.5, 17.0, of 1,200 19.1, 18.5, of 2,000 21.6, 22.4; 32 of 2,000 23.2, 25.8; 16 of 1,500 behind 8,192 23.5, 25.4)
+  cut(&s.own, (int64_t)a->n_req * d->n_kv_heads * s.own.tiles, ((int64_t)a->max_len + 31) / 32, FEW_CHUNKS, false);
   if (s.own.splits > MOST_PARTS) {
     const int64_t chunks = (int64_t)s.own.per * s.own.splits;
     s.own.per = (int)(((chunks + MOST_PARTS - 1) / MOST_PARTS + 3) & ~3ll);
     s.own.splits = (int)((chunks + s.own.per - 1) / s.own.per);
   }
-  if (s.own.waves == 16) s.own.waves = 4;
   const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
   s.staged = g->n_groups > 0 && (s.own.staged || all / g->n_groups > STAGED_ROWS);
   // The requests' own tokens, few rows each, in the same launch as the staged prefixes:

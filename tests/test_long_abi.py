@@ -144,6 +144,23 @@ def test_shared_refusals(L):
     assert call(g=gd(1 << 24)) == -5                                         # a launch takes a workgroup and more a group
 
 
+@pytest.mark.parametrize("n_req,n_kv_heads", [(1, 8), (4, 8), (16, 8), (30, 8), (32, 8), (64, 4), (200, 1)])
+def test_own_tokens_are_split_among_the_waves_there_are(L, n_req, n_kv_heads):
+    """Requests' own tokens behind shared prefixes: one part for every 12 chunks of 32 tokens, until there are 512
+    workgroups, at every length.  (Each is taken by four waves; a part that only sixteen would be enough for is none.)
+    The workspace tells: of n rows of a head's d outputs and 2 statistics, one a part, and one part of the prefix."""
+    d, heads = 128, 4 * n_kv_heads
+    g = gd(n_groups=0, max_prefix=0)
+    for own in range(32, 2500, 32):
+        chunks = own // 32
+        kv = kvd(n_kv_heads=n_kv_heads)
+        a = ad(n_req=n_req, n_tok=n_req, n_heads=heads, max_len=own, q_stride=heads * d, o_stride=heads * d)
+        parts, rest = divmod(L.stq_kv_attend_shared_bytes(ref(kv), ref(a), ref(g)) - (n_req * 4 + 19) // 16 * 16, n_req * heads * (d + 2) * 4)
+        most = max(1, min(512 // (n_req * n_kv_heads), chunks // 12))
+        per = (-(-chunks // most) + 3) // 4 * 4                 # whole chunks for each wave
+        assert rest == 0 and parts - 1 == -(-chunks // per), (own, parts, most)
+
+
 def test_binding_refusals(stq, monkeypatch):
     """Shapes, types, devices and values that the binding does not pass on."""
     import torch
