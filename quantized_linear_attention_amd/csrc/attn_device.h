@@ -874,33 +874,21 @@ __device__ __forceinline__ void attend_rows(const ArgsOf<MODE>& A, uint32_t bx, 
     value_products<D, NT>(C, full, P, o);
     values(at);
   }
-  if constexpr (NWV == 1) {                            // a wave on its own: a lane holds channels (D/16)(4G + i) .. in tiles 0 ..
+  if constexpr (NWV == 1) {    // a wave on its own takes whole lists: a lane holds channels (D/16)(4G + i) .. in tiles 0 ..
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
       const float L = sum_quads(l[nt]);
       if (grow[nt] < 0) continue;
-      const int ch0 = NC * 4 * G;
-      if (whole) {
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const int64_t t = R.first + quot(row0 + 16 * nt + n, A.by_group);
-        uint16_t* out = (uint16_t*)A.o + t * A.os + (grow[nt] - t * A.hq) * D + ch0;
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      const int64_t t = R.first + quot(row0 + 16 * nt + n, A.by_group);
+      uint16_t* out = (uint16_t*)A.o + t * A.os + (grow[nt] - t * A.hq) * D + NC * 4 * G;
 #pragma unroll
-        for (int i4 = 0; i4 < 4; i4++) {
-          uint32_t y[NC / 2];
+      for (int i4 = 0; i4 < 4; i4++) {
+        uint32_t y[NC / 2];
 #pragma unroll
-          for (int c = 0; c < NC / 2; c++) y[c] = pack2<TYPE>(o[nt][2 * c][i4] * inv, o[nt][2 * c + 1][i4] * inv);
-          if constexpr (NC == 8) *(u32x4*)(out + NC * i4) = (u32x4){y[0], y[1], y[2], y[3]};
-          else *(u32x2*)(out + NC * i4) = (u32x2){y[0], y[1]};
-        }
-      } else {
-        const int64_t row = (int64_t)sp * A.n_tok * A.hq + grow[nt];
-        if (G == 0) *(f32x2*)(A.pml + 2 * row) = (f32x2){ref[nt].m == NEG_INF ? NEG_INF : __builtin_fmaf(ref[nt].m, cf[nt], -LIFT), L};
-        float* out = A.po + row * D + ch0;
-#pragma unroll
-        for (int i4 = 0; i4 < 4; i4++)
-#pragma unroll
-          for (int c = 0; c < NC / 4; c++)
-            *(f32x4*)(out + NC * i4 + 4 * c) = (f32x4){o[nt][4 * c][i4], o[nt][4 * c + 1][i4], o[nt][4 * c + 2][i4], o[nt][4 * c + 3][i4]};
+        for (int c = 0; c < NC / 2; c++) y[c] = pack2<TYPE>(o[nt][2 * c][i4] * inv, o[nt][2 * c + 1][i4] * inv);
+        if constexpr (NC == 8) *(u32x4*)(out + NC * i4) = (u32x4){y[0], y[1], y[2], y[3]};
+        else *(u32x2*)(out + NC * i4) = (u32x2){y[0], y[1]};
       }
     }
     return;

@@ -670,6 +670,8 @@ Split blocks_split(const stq_kv_desc* d, const stq_attend_desc* a, int n_sel) {
   s.tiles = (int)((rows + s.tile_rows - 1) / s.tile_rows);
   const int64_t base = (int64_t)a->n_req * a->max_new * d->n_kv_heads * s.tiles;
   cut(&s, base, (int64_t)n_sel * d->block_tokens / 32, FEW_LISTED);
+  // (a wave on its own writes no parts: of so many workgroups none is split)
+  static_assert(FEW_GROUPS <= MANY_GROUPS, "cut() splits none of MANY_GROUPS workgroups");
   if (s.tile_rows == 16 && base >= MANY_GROUPS) s.waves = 1;
   return s;
 }

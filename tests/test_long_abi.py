@@ -161,6 +161,14 @@ def test_own_tokens_are_split_among_the_waves_there_are(L, n_req, n_kv_heads):
         assert rest == 0 and parts - 1 == -(-chunks // per), (own, parts, most)
 
 
+def test_lists_of_many_pairs_are_whole(L):
+    """From 2,048 (token, head) pairs on no list is split, however long: a wave on its own writes no parts."""
+    for n_req, max_new, hkv in ((256, 1, 8), (1, 2048, 1), (683, 3, 1), (64, 16, 2), (5000, 1, 8)):
+        kv, a = kvd(n_kv_heads=hkv), ad(n_req=n_req, n_tok=n_req * max_new, n_heads=2 * hkv, max_new=max_new)
+        for n_sel in (1, 2, 100, 32768, 1 << 24):
+            assert L.stq_kv_attend_blocks_bytes(ref(kv), ref(a), n_sel) == 0, (n_req, n_sel)
+
+
 def test_binding_refusals(stq, monkeypatch):
     """Shapes, types, devices and values that the binding does not pass on."""
     import torch
