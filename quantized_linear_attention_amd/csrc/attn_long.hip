@@ -225,25 +225,25 @@ __device__ __forceinline__ void signed_parts(const ScoreArgs& A, const Raw<D, N>
 
 template <int D, int TYPE>
 __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
-  constexpr int LD = D / 64, NT = 1;                   // 16-byte loads of one bound
+  constexpr int LD = D / 64;                           // 16-byte loads of one bound
   const int lane = threadIdx.x & 63, n = lane & 15, G = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int i = quot(blockIdx.x, A.by_hkv), h = blockIdx.x - i * A.hkv;
   const Req R = req_args(A, i);
-  const int fresh = min(R.n_new, A.max_new), rs = A.rows_shift, TOK = 16 >> rs, tok0 = blockIdx.y * NT * TOK;
+  const int fresh = min(R.n_new, A.max_new), rs = A.rows_shift, TOK = 16 >> rs, tok0 = blockIdx.y * TOK;
   if (tok0 >= fresh) return;
   const int shift = 31 - __builtin_clz(A.T);
-  const int p1 = R.base + min(tok0 + NT * TOK, fresh) - 1;
+  const int p1 = R.base + min(tok0 + TOK, fresh) - 1;
   if (p1 < 0) return;
   const int total = min((p1 >> shift) + 1, A.cols);     // blocks that the last of these tokens sees
   const int32_t* tab = A.table + (int64_t)i * A.cols;
   const int run = 16 * A.tile_run, step = gridDim.z * 4 * run;
   for (int hc = 0; hc < A.group; hc += 16) {            // sixteen heads of the group at a time
     bool ready = false;
-    f16x8 qp[NT][D / 32], qn[NT][D / 32];
-    float mul[NT];
-    int ex[NT], top[NT];                               // the token's last block (-1: not this lane's to write)
-    int64_t to[NT];
+    f16x8 qp[1][D / 32], qn[1][D / 32];
+    float mul;
+    int ex, top;                                       // top: the token's last block (-1: not this lane's to write)
+    int64_t to;
     for (int b1 = (blockIdx.z * 4 + wave) * run; b1 < total; b1 += step) {
       const int b2 = min(b1 + run, total);
       u32x4 w[2 * LD];
@@ -258,63 +258,53 @@ __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
       load(b1);
       if (!ready) {
         ready = true;
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          const int j = tok0 + nt * TOK + (n >> rs), jj = min(j, fresh - 1);
-          const int g = min(hc + (n & ((1 << rs) - 1)), A.group - 1);
-          const int64_t at = (int64_t)(R.first + jj) * A.qs + (int64_t)(h * A.group + g) * D + 16 * G;
-          Raw<D, 1> x;
-          load_raw<D>(A, at, x, 0);
-          signed_parts<D, TYPE, 1>(A, x, &qp[nt], &qn[nt], &ex[nt]);
-          mul[nt] = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(A.scale));
-          const int p = R.base + jj;
-          top[nt] = j < fresh && (n & ((1 << rs) - 1)) == 0 ? min(p >> shift, A.cols - 1) : -1;
-          to[nt] = ((int64_t)(R.first + jj) * A.hkv + h) * A.cols;
-        }
+        const int j = tok0 + (n >> rs), jj = min(j, fresh - 1);
+        const int g = min(hc + (n & ((1 << rs) - 1)), A.group - 1);
+        const int64_t at = (int64_t)(R.first + jj) * A.qs + (int64_t)(h * A.group + g) * D + 16 * G;
+        Raw<D, 1> x;
+        load_raw<D>(A, at, x, 0);
+        signed_parts<D, TYPE, 1>(A, x, qp, qn, &ex);
+        mul = __builtin_amdgcn_frexp_mantf(__builtin_fabsf(A.scale));
+        const int p = R.base + jj;
+        top = j < fresh && (n & ((1 << rs) - 1)) == 0 ? min(p >> shift, A.cols - 1) : -1;
+        to = ((int64_t)(R.first + jj) * A.hkv + h) * A.cols;
       }
       for (int b = b1; b < b2; b += 16) {
-        f32x4 s[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) s[nt] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int x = 0; x < 2 * LD; x++) {
           f16x8 f[2];
           widen(w[x], f);
 #pragma unroll
           for (int y = 0; y < 2; y++)
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-              s[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[y], x < LD ? qn[nt][2 * x + y] : qp[nt][2 * (x - LD) + y], s[nt], 0, 0, 0);
+            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[y], x < LD ? qn[0][2 * x + y] : qp[0][2 * (x - LD) + y], s, 0, 0, 0);
         }
         const uint32_t gone = (uint32_t)__builtin_amdgcn_ballot_w64(dead) & 0xFFFFu;
         if (b + 16 < b2) load(b + 16);
+        f32x4 v;
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          f32x4 v;
+        for (int u = 0; u < 4; u++) {
+          float y = __builtin_ldexpf(s[u] * mul, ex);
+          if (rs > 0) y = __builtin_fmaxf(y, dpp<0xB1>(y));
+          if (rs > 1) y = __builtin_fmaxf(y, dpp<0x4E>(y));
+          if (rs > 2) y = __builtin_fmaxf(y, dpp<0x141>(y));
+          if (rs > 3) y = __builtin_fmaxf(y, dpp<0x140>(y));
+          v[u] = (gone >> (4 * G + u)) & 1 ? NEG_INF : y;
+        }
+        const int b4 = b + 4 * G;
+        if (b4 > top) continue;
+        typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+        float* out = A.score + to + b4;
+        if (hc > 0)                                    // what this lane has written for the heads before
 #pragma unroll
-          for (int u = 0; u < 4; u++) {
-            float y = __builtin_ldexpf(s[nt][u] * mul[nt], ex[nt]);
-            if (rs > 0) y = __builtin_fmaxf(y, dpp<0xB1>(y));
-            if (rs > 1) y = __builtin_fmaxf(y, dpp<0x4E>(y));
-            if (rs > 2) y = __builtin_fmaxf(y, dpp<0x141>(y));
-            if (rs > 3) y = __builtin_fmaxf(y, dpp<0x140>(y));
-            v[u] = (gone >> (4 * G + u)) & 1 ? NEG_INF : y;
-          }
-          const int b4 = b + 4 * G;
-          if (b4 > top[nt]) continue;
-          typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-          float* out = A.score + to[nt] + b4;
-          if (hc > 0)                                  // what this lane has written for the heads before
+          for (int u = 0; u < 4; u++)
+            if (b4 + u <= top) v[u] = __builtin_fmaxf(v[u], out[u]);
+        if (b4 + 3 <= top) {
+          *(f32x4_a4*)out = v;
+        } else {
 #pragma unroll
-            for (int u = 0; u < 4; u++)
-              if (b4 + u <= top[nt]) v[u] = __builtin_fmaxf(v[u], out[u]);
-          if (b4 + 3 <= top[nt]) {
-            *(f32x4_a4*)out = v;
-          } else {
-#pragma unroll
-            for (int u = 0; u < 4; u++)
-              if (b4 + u <= top[nt]) out[u] = v[u];
-          }
+          for (int u = 0; u < 4; u++)
+            if (b4 + u <= top) out[u] = v[u];
         }
       }
     }
