@@ -611,11 +611,15 @@ stq_status stq_kv_bounds(const stq_kv_desc* desc, const void* cache_dev, size_t 
  * which no logit of the block exceeds.  score_dev: fp32 [n_tok][n_kv_heads][table_cols];
  * blocks outside the cache get -inf, blocks with NaN bounds NaN, columns behind
  * p's block are left as they were.  max_len sets the split of the work, never the
- * result; o_stride is not used.  Products are exact (queries scaled by a power
- * of two per row or token), sums binary32; a query with infinities or NaN has no
- * meaningful score.  score may overlap neither q nor the bounds
- * (STQ_ERR_ARG).  STQ_ERR_UNSUPPORTED from n_req * n_kv_heads = 2^24 on and from
- * max_new = 2^22 on (2^23 with two query heads to a key/value head, 2^24 with one). */
+ * result; o_stride is not used.  Products are exact, sums binary32, and no logit
+ * exceeds the score by more than their roundings.  (bfloat16 queries go into the
+ * products as binary16, scaled by a power of two for each query, or from max_new =
+ * 16 on for up to four heads of a token together: exact down to 2^-29 of the
+ * largest magnitude there, cut to 2^-38 of it below.)  A query with infinities or
+ * NaN has no meaningful score.  score may overlap neither q nor the bounds
+ * (STQ_ERR_ARG).  STQ_ERR_UNSUPPORTED from n_req * n_kv_heads = 2^24 on and past
+ * max_new = 4,194,240 (8,388,480 with two query heads to a key/value head,
+ * 16,776,960 with one). */
 stq_status stq_kv_score(const stq_kv_desc* desc, const stq_attend_desc* a, const void* bounds_dev,
                         const int32_t* table_dev, const int32_t* tok_start_dev, const int32_t* len_dev,
                         const void* q_dev, float* score_dev, hipStream_t stream);
@@ -637,9 +641,14 @@ typedef struct stq_select_desc {
  * never taken.  sel_dev int32 [n_tok][n_kv_heads][n_sel]: their columns in
  * ascending order, then -1.  Whole numbers from comparisons: the same scores give
  * the same selection.  sel must not overlap score (STQ_ERR_ARG).
- * STQ_ERR_UNSUPPORTED past 32,768 columns, from n_req * max_new * n_kv_heads =
- * 2^31 on and from 2^32 threads on (a row takes 64, 256 past 512 columns and
- * 1,024 past 2,048). */
+ * The work of a row goes by table_cols (up to 64, 256, 512, 2,048, 8,192 and
+ * 32,768 columns), not by the blocks that its token sees (32,768 rows of 256
+ * blocks: 30 us in 256 columns, 38 in 512, 107 in 2,048, 1,230 in 8,192; 512 rows
+ * of 500 blocks: 7 us in 512, 16 in 2,048, 27 in 8,192).  Where a table is much
+ * wider than the longest request, score and select by a copy of the columns in use.
+ * STQ_ERR_UNSUPPORTED past 32,768 columns, and where
+ * n_req * max_new * n_kv_heads passes 67,108,860 (4,194,303 past 2,048 columns):
+ * 2^32 threads, of which a row takes 64 (1,024 past 2,048 columns). */
 stq_status stq_kv_select(const stq_select_desc* c, const int32_t* tok_start_dev, const int32_t* len_dev,
                          const float* score_dev, int32_t* sel_dev, hipStream_t stream);
 

@@ -650,7 +650,8 @@ def stq_kv_score(kv, bounds, table, tok_start, lens, q, score, scale, max_new, m
 
 def stq_kv_select(score, tok_start, lens, sel, block_tokens, max_new, n_first=1, n_last=1, stream=None):
     """score float32 [tokens][n_kv_heads][cols]; sel int32 [tokens][n_kv_heads][n_sel]: the columns of the
-    first n_first and the last n_last blocks that the token sees and of the best others, ascending, then -1."""
+    first n_first and the last n_last blocks that the token sees and of the best others, ascending, then -1.
+    The work goes by cols, so a table much wider than its longest request is best cut to the columns in use."""
     _there(score=score, sel=sel, lens=lens)
     if score.dim() != 3 or sel.dim() != 3 or sel.shape[:2] != score.shape[:2]:
         raise StqError(-1, "score must be [tokens][n_kv_heads][cols] and sel [tokens][n_kv_heads][n_sel]")

@@ -71,6 +71,14 @@ def test_score_refusals(L):
     assert call(ad(n_req=1, max_new=1 << 26)) == -5
 
 
+@pytest.mark.parametrize("a,d", [(dict(n_req=1 << 23), {}), (dict(n_req=(1 << 24) // 3 + 1), dict(n_kv_heads=3)), (dict(max_new=4194241, n_heads=6), {}),
+                                 (dict(max_new=8388481, n_heads=4), {}), (dict(max_new=16776961, n_heads=2), {})])
+def test_score_just_past_its_limits(L, a, d):
+    """The first number of (request, head) pairs and of new tokens (six, four and two heads over two) that is refused."""
+    a = dict(dict(n_heads=d.get("n_kv_heads", 2), q_stride=6 * 128), **a)
+    assert L.stq_kv_score(ref(kvd(**d)), ref(ad(**a)), FAR, D, D, D, D, P(1 << 41), None) == -5
+
+
 def test_select_refusals(L):
     def call(c=None, tok=D, len=D, score=D, sel=FAR):
         return L.stq_kv_select(ref(c or sd()), tok, len, score, sel, None)
@@ -88,6 +96,11 @@ def test_select_refusals(L):
     assert call(sd(table_cols=32769)) == -5
     assert call(sd(n_req=1 << 20, max_new=1 << 12)) == -5
     assert call(sd(n_req=1 << 20, max_new=4, table_cols=4096)) == -5         # 1,024 threads a row
+    # the first number of rows that is refused: 64 threads a row to 2,048 columns (four rows a workgroup), 1,024 past that
+    for cols in (1, 512, 513, 2048):
+        assert call(sd(n_req=67108861, max_new=1, n_kv_heads=1, table_cols=cols)) == -5, cols
+    for cols in (2049, 32768):
+        assert call(sd(n_req=4194304, max_new=1, n_kv_heads=1, table_cols=cols)) == -5, cols
 
 
 def test_blocks_refusals(L):
