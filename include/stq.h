@@ -576,6 +576,11 @@ stq_status stq_kv_attend(const stq_kv_desc* desc, const void* cache_dev, size_t 
  * request i sits at p = len[i] - (tok_start[i+1] - tok_start[i]) + j; rows and
  * tokens outside of any request, and queries past max_new, are left alone.
  * Their stq_attend_desc has window = n_sink = 0 (else STQ_ERR_ARG).
+ * Neither pays where there is little to spare: bounds, score, select and
+ * attend_blocks of one step together against stq_kv_attend, 32 blocks of 64 tokens,
+ * 32 heads over 8, d = 128, us on the GPU: one request of 32,768 tokens 22, 17, of
+ * 131,072 35, 39; 8 of up to 8,192 24, 17, of up to 32,768 29, 50; 64 of up to 4,096
+ * 44, 43, of up to 8,192 48, 73, of up to 32,768 58, 247.  Shared prefixes: see there.
  * q, o, bounds, score, sel and the workspace are 16-byte aligned, q and o with
  * strides a multiple of 16 bytes, else STQ_ERR_LAYOUT.
  *
@@ -679,7 +684,12 @@ typedef struct stq_shared_desc {
  * group_start int32 [n_groups + 1], non-decreasing; requests before
  * group_start[0] or from group_start[n_groups] on are in no group.  In the
  * descriptor max_len is about the longest own part (len minus prefix): it sets
- * the split of the work, never the result.  The workspace is always needed.
+ * the split of the work, never the result.  The workspace is always needed, and
+ * every call joins parts: behind few shared tokens, or for few requests,
+ * stq_kv_attend is the faster call.  32 heads over 8, d = 128, up to 256 own tokens,
+ * us on the GPU by this call and by that: 2 requests behind 8,192 tokens 14, 13; 8
+ * behind 2,048 12, 11, behind 8,192 17, 17; 32 behind 2,048 23, 17, behind 8,192 26,
+ * 39; 64 behind 1,024 23, 16, behind 2,048 24, 23, behind 8,192 35, 65.
  * Errors, overlap and roundings as stq_kv_attend; STQ_ERR_UNSUPPORTED also where
  * n_kv_heads times the groups and the tiles of all query rows passes 2^24. */
 size_t stq_kv_attend_shared_bytes(const stq_kv_desc* desc, const stq_attend_desc* a, const stq_shared_desc* g);

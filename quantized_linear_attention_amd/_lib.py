@@ -698,7 +698,8 @@ def stq_kv_attend_shared(kv, table, tok_start, lens, group_start, prefix, q, o, 
                          work, stream=None):
     """As stq_kv_attend, for requests of which group_start[g] .. group_start[g+1]-1 share their first prefix[g]
     tokens: group_start int32 [groups + 1], prefix int32 [groups]; max_own, max_prefix: about the longest
-    own part and the longest prefix; work: uint8 tensor of stq_kv_attend_shared_bytes(...) bytes."""
+    own part and the longest prefix; work: uint8 tensor of stq_kv_attend_shared_bytes(...) bytes.  Behind few shared
+    tokens stq_kv_attend is the faster call (include/stq.h has figures)."""
     _there(prefix=prefix)
     i, dev = torch.int32, kv.index
     n, cols = _table(table)

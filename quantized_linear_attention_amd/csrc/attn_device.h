@@ -168,8 +168,10 @@ __device__ __forceinline__ Req req_args(const AttnArgs& A, int i) {
 // behind the first new token of any member that has one, so that every row sees
 // all of them.  Up to 256 requests in 64 groups are loaded at once, one request or
 // group a lane, and the rest is exchanged between lanes: a chain of one load
-// instead of three or four (the prefixes' part of 64 requests behind two of them 24.6
-// -> 23.2 us).
+// instead of three or four (the prefixes' part of 60 requests behind two of them 24.6
+// -> 23.2 us).  More are looked up by every workgroup, a load behind another: 256 -> 257
+// requests behind one prefix of 2,048 tokens 51.9 -> 57.0 us (attention without sharing 64.8
+// -> 70.1), 64 -> 65 groups of one request behind 1,024 23.8 -> 27.1 (15.5 -> 17.5).
 struct Members { int s, e, first, last, len; };
 __device__ __forceinline__ int wave_max_i(int x);
 struct Whole {
@@ -262,7 +264,7 @@ struct Whole {
   // The x-th part of all prefixes' work: group, tile of its rows, part of its chunks
   // and how many chunks a part has, the same for all.  Parts are sized by what all
   // groups together have to do, so that the card is filled once (four groups of
-  // 8,192 to 16,384 shared tokens with 770 query tokens: 235 us in parts by the
+  // 11,648 to 16,384 shared tokens with 619 query tokens: 235 us in parts by the
   // longest prefix alone, 203 so; one line of all tiles' chunks cut evenly takes 275,
   // since a part's tiles no longer read the same tokens at one time).
   struct Part { int g, tile, sp, per; };

@@ -19,8 +19,10 @@ namespace {
 // are register swaps (permlane32 and 16, each halving what a lane holds) and
 // DPP steps.  Lanes past the last token read the last one again.  All of a block's
 // loads are asked for at once.  A chain of counts, table and keys bounds it: the
-// blocks of 32,768 tokens of 8 heads (d = 128) 7.7 us, 1.8 TB/s; 512 blocks
-// scattered over 2.6 GB of pages 12.6 us, where a launch alone takes 2.
+// blocks of 22,871 tokens of 8 heads (d = 128) 7.7 us for 13.3 MB, 1.7 TB/s; 512
+// blocks scattered over 2.9 GB of pages 12.6 us for 10.4 MB, where a launch alone takes 2
+// (half of its waves have no block: one token may touch two; 329 misses of
+// the CUs' address translation a launch against 29).
 struct BoundsArgs {
   const uint8_t* cache;
   const int32_t *table, *tok_start, *len;
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(256) k_kv_bounds(BoundsArgs A) {
 // repeated up to a power of two (a maximum does not mind), so that the group's
 // maximum is DPP steps.  Products are exact in binary32.
 //
-// Memory and latency bound: 64 requests of 8,192 to 32,768 tokens in blocks of
+// Memory and latency bound: 64 requests of 8,839 to 32,768 tokens in blocks of
 // 64, 32 heads over 8, d = 128: 14 us for 42 MB (3.0 TB/s; the chain of counts,
 // table, bounds and store is 5 us of it).  A wave takes four tiles of blocks there:
 // 16.6 us with one, 14.9 with two, 15.3 with eight.
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(256) k_kv_score(ScoreArgs A) {
 // such sets of tokens (HT TT products to each widened bound) and goes over the
 // blocks that they see.  One power of two scales all of a token's HT queries.
 //
-// Two prompts of 1,024 to 2,048 tokens over 16,384 positions, 32 heads over 8, d =
+// Two prompts of 2,048 and 2,020 tokens behind 14,336 and 8,185, 32 heads over 8, d =
 // 128: 27 us for 59 MB and 12.8 GFLOP (70 us by the kernel above, whose columns
 // are mostly repeated queries there).  Half of a wave's life is waiting: 33 MB of
 // queries come in before its first product and two waves a SIMD fill the registers;
@@ -465,9 +467,9 @@ __global__ void __launch_bounds__(256, 2) k_kv_score_wide(ScoreArgs A) {
 //
 // W waves a row, each with M blocks a lane: block 64 (M wave + m) + lane.
 //
-// Instruction bound: 32,768 rows of up to 256 scores 29 us (0.34 us a thousand rows
+// Instruction bound: 32,544 rows of up to 256 scores 29 us (0.34 us a thousand rows
 // and wave slot; 340 vector instructions a row and as many scalar ones), 512 rows of
-// 128 to 512 7.6 us, of which the launch and the row's loads are five.  Four rows a
+// 138 to 512 7.6 us, of which the launch and the row's loads are five.  Four rows a
 // wave with sums over sixteen lanes: 27 us, but 8.1 us for the 512 rows; one bit a
 // trial: 53 and 8.6 us.
 struct SelectArgs {
@@ -646,11 +648,18 @@ void fill(AttnArgs& A, const stq_kv_desc* d, const void* cache, const stq_attend
 
 // Work of the blocks' attention: by what a whole list holds.  Few workgroups are
 // split into parts of 8 chunks (one request, 32 blocks of 64 tokens, 8 heads: 9.8 us
-// on the GPU, 11 in parts of 12 and more, 10.3 of 4).  From 2,048 (token, head) pairs
-// on each has one wave, which needs no join through LDS and starts once instead
-// of four times: 16 blocks of 64 tokens at d = 128, prompts of 256 tokens 39.3 us by
-// four waves, 38.4 by one; 512 73.3, 65.8; 1,024 142, 122 (64 blocks 472, 460; 4
-// blocks 62, 39); 256 requests of one token 57.8, 55.4; but 128 tokens 21.8, 26.0.
+// on the GPU, 11 in parts of 12 and more, 10.3 of 4).  Where cut() gives sixteen waves,
+// they spare the second launch: parts against sixteen waves, us a call and (on the
+// GPU), blocks of 64 tokens, 8 heads, d = 128: one request, 12 blocks 12.9 (8.8), 9.8
+// (9.4); 17 12.8 (9.0), 10.0 (10.7); 8 requests, 17 12.6 (10.1), 10.4 (10.5); 16
+// requests, 12 12.6 (11.8), 9.9 (10.7); 32 14.6 (15.1), 13.6 (14.8); 32 requests, 12 13.4
+// (13.7), 11.1 (11.3); 32 20.2 (20.4), 16.4 (17.0).  (In parts on both sides of
+// that: one request, 8 blocks 12.8, 18 12.7; 32 requests, 33 blocks 20.0.)
+// From 2,048 (token, head) pairs on each has one wave, which needs no join through LDS
+// and starts once instead of four times: 16 blocks of 64 tokens at d = 128, prompts of
+// 256 tokens 35.2 us by four waves, 35.5 by one; 512 63.3, 58.6; 1,024 120.7, 105.1 (64
+// blocks 383, 388; 4 blocks 56, 36); 256 requests of one token 58.6, 55.4; but 128
+// tokens 21.2, 25.9.
 constexpr int64_t FEW_LISTED = 8;
 Split blocks_split(const stq_kv_desc* d, const stq_attend_desc* a, int n_sel) {
   Split s;
@@ -690,14 +699,14 @@ Shares shares_of(const stq_kv_desc* d, const stq_attend_desc* a, const stq_share
   const int64_t all = (int64_t)a->n_tok * group;        // rows of all groups, and of one on average
   s.staged = g->n_groups > 0 && (s.own.staged || all / g->n_groups > STAGED_ROWS);
   // The requests' own tokens, few rows each, in the same launch as the staged prefixes:
-  // 64 requests behind two prefixes of 8,192 tokens 46 us in two, 38 in one; behind one
-  // 44, 37; 128 59, 58; 770 query tokens behind four of 16,384 280, 262.
+  // 60 requests behind prefixes of 8,192 and 4,416 tokens 46 us in two, 38 in one; 64 behind
+  // one of 8,192 44, 37; 128 59, 58; 619 query tokens behind four of 11,648 to 16,384 280, 262.
   s.both = s.staged && s.own.tile_rows == 16;
   s.tile_rows = s.staged ? 32 * TILE_WAVES : s.own.tile_rows;
   const int64_t tiles = (all + s.tile_rows - 1) / s.tile_rows, fill = (PRE_GROUPS + d->n_kv_heads - 1) / d->n_kv_heads;
   s.pre_units = g->n_groups > 0 ? fill + tiles + g->n_groups : 0;
   // (prefix kernel and join of 64 requests behind 2,048 tokens: parts of 8 chunks 23 us, of 12 24, of 16 26;
-  // behind 8,192 34, 34, 32; 128 in four groups 48, 40, 39)
+  // behind 8,192 34, 34, 32; 98 in four groups behind 5,184 to 8,192 48, 40, 39)
   s.per = 12;
   const int64_t chunks = (int64_t)g->max_prefix / 32 + 1;
   int64_t slots = 2 * fill / (tiles > 0 ? tiles : 1) + 1;
